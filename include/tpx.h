@@ -326,6 +326,135 @@ tp_status tp_attn_block_forward(const tp_packed_desc* qkv /* host */, const void
                                 const int32_t* lens, void* y, void* qkv_out, void* o_in, void* ws,
                                 size_t ws_bytes, uint32_t flags, void* stream);
 
+/* ---- Paged key-value cache
+ *
+ * The cache in pages of page_size positions: k_pages, v_pages are [t][n_pages][n_kv/t][page_size][hd]
+ * (device, caller-owned; shard s holds its kv heads' part of every page), and request m's positions
+ * p = 0, 1, .. lie in the pages block_table[m * table_stride + p / page_size].  A token's slot is
+ * page * page_size + p % page_size.  Pages hold bf16, or e4m3 codes with one fp32 scale per kv head
+ * (k_scale, v_scale: [n_kv] on the device; NULL = 1): the value is code * scale.
+ * page_size is 16, 32, 64, 128 or 256 (TP_ERR_SHAPE otherwise) and n_pages * page_size is below 2^31
+ * (TP_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+  int32_t kv_dtype;     /* tp_wtype of the pages */
+  int32_t page_size;    /* positions per page */
+  int32_t n_pages;      /* pages of the pool */
+  int32_t max_pages;    /* page ids in a row of the block table */
+  int32_t table_stride; /* ids from one row to the next, >= max_pages */
+} tp_pages;
+
+/* Block tables and slots of a step from the requests' lengths, on the device.  Request m holds
+ * lens[m] tokens and is to get add[m] more, which are rows cu_rows[m] .. cu_rows[m+1]-1 of the step's
+ * batch (requests in order, cu_rows[0] = 0).  It needs ceil((lens + add) / page_size) -
+ * ceil(lens / page_size) pages more.  Pages are handed out in request order from
+ * free_pages[*head], free_pages[*head + 1], ..., up to free_pages[n_free - 1].  A request is
+ * refused if lens or add is negative, lens + add does not fit in max_pages pages, its rows do not fit
+ * in `rows`, or it needs pages and the requests up to it need more than are left (a request refused for
+ * the other reasons needs none).
+ *   block_table: [M] rows of the caller's table; the entries of a request's new pages are written,
+ *                no other (a refused request's row stays as it is).
+ *   lens_out:    [M] lens + add, or lens for a refused request.
+ *   cu_rows:     [M + 1] as above, refused requests' rows counted (a negative add as 0; at most 2^31-1).
+ *   positions, slots: [rows] the row's position (lens[m] + i for the request's i-th new token, modulo 2^32) and
+ *                slot; slot -1 for a refused request's rows, and where the table or the free list
+ *                names a page outside [0, n_pages).  Rows behind the last request get position 0,
+ *                slot -1, so a batch padded to `rows` appends nothing there.
+ *   counts:      [3] *head after this step, the rows of all requests, the refused requests.
+ * head: device pointer to the number of free_pages already taken (NULL = 0); outside [0, n_free] no
+ * page is left.  The outputs must not overlap the inputs (checked for lens_out against lens and add
+ * and for counts against head): steps alternate between two sets, one call's lens_out and counts
+ * being the next one's lens and head, with nothing read by the host.  int32 arrays on the device, 4-byte aligned.  One kernel
+ * launch.  M == 0 is a no-op. */
+tp_status tp_paged_tables(const tp_pages* pages /* host */, const int32_t* lens, const int32_t* add, int32_t M,
+                          const int32_t* free_pages, int32_t n_free, const int32_t* head, int32_t* block_table,
+                          int32_t* lens_out, int32_t* cu_rows, int32_t* positions, int32_t* slots, int32_t rows,
+                          int32_t* counts, void* stream);
+
+/* ---- Rotary positions
+ *
+ * Pair i of a head's first rot_dim dims (i < rot_dim / 2) is turned by the angle pos * f_i:
+ *   (a, b) -> (a cos - b sin, b cos + a sin) * mscale,   f_i = theta^(-2 i / rot_dim)
+ * with (a, b) = dims (i, i + rot_dim/2) (TP_ROPE_HALF) or (2 i, 2 i + 1) (TP_ROPE_INTERLEAVED); the
+ * dims from rot_dim on are left as they are.  For contexts longer than the original length f_i is
+ * scaled and mscale set by `scaling`:
+ *   TP_ROPE_NONE        f_i as above, mscale 1
+ *   TP_ROPE_LINEAR      f_i / factor
+ *   TP_ROPE_WAVELENGTH  keep f_i + (1 - keep) f_i / factor, keep = clamp((turns - low_freq_factor) /
+ *                       (high_freq_factor - low_freq_factor), 0, 1), turns = original_len f_i / 2 pi
+ *   TP_ROPE_YARN        the same blend by pair index: keep = 1 - clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *                       lo = max(0, floor(dim(beta_fast))), hi = min(rot_dim - 1, ceil(dim(beta_slow))),
+ *                       dim(r) = rot_dim ln(original_len / (2 pi r)) / (2 ln theta);
+ *                       mscale = 0.1 ln(factor) + 1 for factor > 1
+ * ("YaRN: Efficient Context Window Extension of Large Language Models", Peng et al. 2023.) */
+typedef enum { TP_ROPE_HALF = 0, TP_ROPE_INTERLEAVED = 1 } tp_rope_layout;
+typedef enum { TP_ROPE_NONE = 0, TP_ROPE_LINEAR = 1, TP_ROPE_WAVELENGTH = 2, TP_ROPE_YARN = 3 } tp_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim; /* a multiple of 16, 16 .. 256 */
+  int32_t layout, scaling;
+  int32_t original_len;                                 /* WAVELENGTH, YARN */
+  double theta, factor;                                 /* theta > 1; factor > 0 (not used by NONE) */
+  double low_freq_factor, high_freq_factor;             /* WAVELENGTH: 0 < low < high */
+  double beta_fast, beta_slow;                          /* YARN: both > 0 */
+} tp_rope_params;
+
+/* Host struct describing a rotation: step[i] is f_i / 2 pi, the turns per position, as a binary
+ * fraction of 64 bits.  pos * step[i] modulo 2^64 is the fraction of a turn at pos, exact to
+ * 2^-64 |pos| (plus the rounding of f_i, 2^-53 of it), for every int32 position. */
+#define TP_ROPE_MAGIC 0x54505852u /* "TPXR" */
+typedef struct {
+  uint32_t magic;
+  int32_t rot_dim, layout;
+  float mscale;
+  uint64_t step[128];
+} tp_rope;
+
+/* Fill *rope (host) from *params (host); no device work. */
+tp_status tp_rope_describe(const tp_rope_params* params, tp_rope* rope);
+
+/* Rotate the q and k heads of qkv [M, (n_q + 2 n_kv) hd] (bf16, the shard-major order of
+ * tp_colpar_forward's QKV output) at positions[m] (int32, device, any value) into qkv_out in the same
+ * order; v is copied.  qkv_out may be qkv itself (in place, v not touched); any other overlap is not
+ * allowed.  fp32 products and sums, one rounding to bf16.  For the contiguous cache: the rotated qkv is
+ * what tp_attn_decode takes.  head_dim a multiple of 16 up to 256 (TP_ERR_UNSUPPORTED otherwise),
+ * rot_dim at most head_dim (TP_ERR_SHAPE).  One kernel launch.  M == 0 is a no-op. */
+tp_status tp_rope_forward(const tp_shape* shape /* host */, const tp_rope* rope /* host */, const void* qkv,
+                          const int32_t* positions, int32_t M, void* qkv_out, void* stream);
+
+/* The same rotation on the way into a paged cache: the rotated q to q_out [M, n_q hd] (bf16, heads in
+ * order, what tp_paged_attn_decode takes), the rotated k and v to slot slots[m] of the pages.  A row
+ * whose slot is outside [0, n_pages * page_size) is not appended (its q is still written); the slots of
+ * a call's rows must differ (of two rows with one slot either may remain, in parts).  e4m3 pages: code =
+ * e4m3 RNE satfinite of x / scale of the head (binary32 divide), x the fp32 rotated k or v, so k is
+ * rounded once; k_scale, v_scale as above, finite and > 0, NULL for bf16 pages (TP_ERR_INVALID_ARG
+ * otherwise).  rope NULL: nothing is turned and positions is not read.  q_out must not overlap qkv.
+ * One kernel launch.  M == 0 is a no-op. */
+tp_status tp_rope_append(const tp_shape* shape /* host */, const tp_rope* rope /* host */, const tp_pages* pages /* host */,
+                         const void* qkv, const int32_t* positions, const int32_t* slots, int32_t M, void* q_out,
+                         void* k_pages, void* v_pages, const float* k_scale, const float* v_scale, void* stream);
+
+/* Decode attention of one new token per request over the paged cache, head-sharded as
+ * tp_attn_decode, split over the cache's length and joined.  lens[m] is the number of cached
+ * positions, the new token's included (it is appended first: tp_rope_append).  For q head h and its
+ * kv head g = h / (n_q / n_kv), with j over max(0, lens[m] - window) .. lens[m] - 1 (window 0: from 0):
+ *   s_j = scale q[m, h] . k_j;   lse[m, h] = ln sum_j exp(s_j);   o[m, h] = bf16( sum_j exp(s_j - lse) v_j )
+ * q: [M, n_q hd] bf16, o_in: [M, n_q hd] bf16, lse: [M, n_q] fp32 or NULL; scale 0 stands for
+ * 1 / sqrt(hd).  fp32 scores, softmax and accumulation.  A request with lens[m] outside
+ * [1, max_pages * page_size] gets a zero row and lse -inf.  Positions of a page whose id is outside
+ * [0, n_pages) are left out as if masked; a row left without positions is zero with lse -inf.  Cache
+ * rows outside the positions attended to never enter the result, whatever they hold.
+ * head_dim 64, 128 or 256, n_q / n_kv at most 16, t * n_pages * (n_kv / t) * page_size below 2^31
+ * (TP_ERR_UNSUPPORTED otherwise); q, the pages, o_in and ws 16-byte aligned.
+ * ws: tp_paged_attn_workspace_bytes(shape) bytes, whatever M and the lengths are; zero-filled once
+ * before first use (and after a TP_ERR_DEVICE_TIMEOUT), left reusable by every call with any shape
+ * whose size it covers; calls that share it must not overlap on the GPU (replays of two captured graphs
+ * included).  One kernel launch; the split follows the SM count, so runs repeat bit for bit. */
+size_t tp_paged_attn_workspace_bytes(const tp_shape* shape /* host */);
+tp_status tp_paged_attn_decode(const tp_shape* shape /* host */, const tp_pages* pages /* host */, const void* q,
+                               const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                               const int32_t* block_table, const int32_t* lens, int32_t M, float scale, int32_t window,
+                               void* o_in, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Vocabulary-parallel lm_head (the column-parallel GEMM at the model's output edge; each shard's
  * logits are a slice of the output, so the pages' all-gather is a concatenation, scalablesystem.dev
  * "The Tensor-Parallel Shard Group"): logits[m][v] = sum_k x[m][k] W[k][v] for v < vocab, fp32
@@ -333,6 +462,22 @@ tp_status tp_attn_block_forward(const tp_packed_desc* qkv /* host */, const void
  * (padding ids are not written).  ws optional as for tp_colpar_forward.  M == 0 is a no-op. */
 tp_status tp_lm_head_forward(const tp_packed_desc* desc /* host */, const void* w, const void* x, int32_t M,
                              float* logits, void* ws, size_t ws_bytes, uint32_t flags, void* stream);
+
+/* Log probabilities over logits [M, vocab] fp32 (rows ldl apart, ldl >= vocab; tp_lm_head_forward's output),
+ * with P = softmax of the row, in one pass over it:
+ *   logprob[m] = ln P(ids[m]); 0 for an id outside [0, vocab), which asks for no token
+ *   entropy[m] = -sum_v P(v) ln P(v)  (a logit of -inf has probability 0 and adds nothing)
+ *   rank[m]    = 1 + the ids ahead of ids[m]: a greater logit, or an equal one and a lower id; 0 for an
+ *                id outside [0, vocab)
+ *   top_logprob, top_id [M, k]: the k first ids in that order and their ln P; k <= 32 and k <= vocab
+ * A row that holds a NaN or +inf, or only -inf, has no distribution: its values are NaN, its rank 0 and its
+ * top ids -1 (logprob stays 0 where no token is asked for).  ids with logprob and rank, entropy, and the top pair
+ * may be NULL (k 0).  fp32 sums.  Pointers 4-byte aligned, logits' rows too; vocab below 2^30.  No workspace: the CTAs that
+ * share a row are a cluster.  One kernel launch; the result is bitwise the same run to run.  M == 0 is
+ * a no-op. */
+tp_status tp_token_logprobs(const float* logits, int64_t ldl, int32_t M, int32_t vocab, const int32_t* ids, int32_t k,
+                            float* logprob, int32_t* rank, float* entropy, float* top_logprob, int32_t* top_id,
+                            void* stream);
 
 /* Vocabulary-parallel embedding lookup (the table split by vocabulary rows; each shard contributes
  * its row if the id is in its range, else zeros, and the contributions are summed, which leaves

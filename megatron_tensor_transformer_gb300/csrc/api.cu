@@ -3,6 +3,7 @@
 #include <atomic>
 #include <mutex>
 #include <chrono>
+#include <cmath>
 #include <cstring>
 #include <thread>
 
@@ -10,6 +11,7 @@
 #include "common.cuh"
 #include "fused.h"
 #include "pack.h"
+#include "paged.h"
 #include "ring.h"
 #include "skinny.h"
 #include "small.h"
@@ -170,6 +172,47 @@ bool act_scratch(void* ws, size_t ws_bytes, const tp_shape& sh, int M, uint32_t 
   q = static_cast<uint8_t*>(ws) + off;
   s = reinterpret_cast<float*>(q + align_up((uint64_t)M * act_width(&sh)));
   return true;
+}
+
+// ---- paged cache
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+inline int page_shift(const tp_pages* p) {
+  int s = 4;
+  while ((1 << s) < p->page_size) ++s;
+  return s;
+}
+tp_status check_pages(const tp_pages* p) {
+  if (!p || (p->kv_dtype != TP_BF16 && p->kv_dtype != TP_FP8_E4M3)) return TP_ERR_INVALID_ARG;
+  const int ps = p->page_size;
+  if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return TP_ERR_SHAPE;
+  if (p->n_pages <= 0 || p->max_pages <= 0 || p->table_stride < p->max_pages) return TP_ERR_SHAPE;
+  if ((int64_t)p->n_pages * ps >= (int64_t(1) << 31)) return TP_ERR_UNSUPPORTED;  // slots are int32
+  return TP_OK;
+}
+tp_status check_rope(const tp_rope* r, int hd) {
+  if (hd % 16 || hd > 256) return TP_ERR_UNSUPPORTED;
+  if (!r) return TP_OK;
+  if (r->magic != TP_ROPE_MAGIC) return TP_ERR_LAYOUT_MISMATCH;
+  if (r->layout != TP_ROPE_HALF && r->layout != TP_ROPE_INTERLEAVED) return TP_ERR_INVALID_ARG;
+  if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > hd) return TP_ERR_SHAPE;
+  return TP_OK;
+}
+RopeArgs rope_args(const tp_shape* sh, const tp_rope* rope, const void* qkv, const int32_t* positions, int M, void* out) {
+  RopeArgs a{};
+  if (rope) a.rope = *rope;
+  a.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  a.positions = positions;
+  a.q_out = static_cast<__nv_bfloat16*>(out);
+  a.M = M;
+  a.t = sh->t;
+  a.n_q = sh->n_q_heads;
+  a.n_kv = sh->n_kv_heads;
+  a.hd = sh->head_dim;
+  return a;
 }
 
 }  // namespace
@@ -992,6 +1035,164 @@ tp_status tp_attn_block_forward(const tp_packed_desc* qkv, const void* qkv_w, co
   if (st != TP_OK) return st;
   return run_rowpar(o, o_w, static_cast<const bf16*>(o_in), M, static_cast<const bf16*>(residual),
                     static_cast<bf16*>(y), nullptr, ws, proj, flags, s);
+}
+
+tp_status tp_paged_tables(const tp_pages* pages, const int32_t* lens, const int32_t* add, int32_t M,
+                          const int32_t* free_pages, int32_t n_free, const int32_t* head, int32_t* block_table,
+                          int32_t* lens_out, int32_t* cu_rows, int32_t* positions, int32_t* slots, int32_t rows,
+                          int32_t* counts, void* stream) {
+  tp_status st = check_pages(pages);
+  if (st != TP_OK) return st;
+  if (M < 0 || n_free < 0 || rows < 0) return TP_ERR_INVALID_ARG;
+  if (M == 0) return TP_OK;
+  if (!lens || !add || !block_table || !lens_out || !cu_rows || !counts) return TP_ERR_INVALID_ARG;
+  if ((n_free > 0 && !free_pages) || (rows > 0 && (!positions || !slots))) return TP_ERR_INVALID_ARG;
+  const void* ptrs[] = {lens, add, free_pages, head, block_table, lens_out, cu_rows, positions, slots, counts};
+  for (const void* p : ptrs)
+    if (!aligned4(p)) return TP_ERR_ALIGN;
+  const size_t n = (size_t)M * 4;
+  if (overlap(lens_out, n, lens, n) || overlap(lens_out, n, add, n) || (head && overlap(counts, 12, head, 4)))
+    return TP_ERR_INVALID_ARG;
+  TablesArgs a{lens, add, free_pages, head, block_table, lens_out, cu_rows, positions, slots, counts,
+               M, n_free, rows, page_shift(pages), pages->n_pages, pages->max_pages, pages->table_stride};
+  return cuda_status(launch_paged_tables(a, S(stream)));
+}
+
+tp_status tp_rope_describe(const tp_rope_params* p, tp_rope* rope) {
+  if (!p || !rope) return TP_ERR_INVALID_ARG;
+  if (p->layout != TP_ROPE_HALF && p->layout != TP_ROPE_INTERLEAVED) return TP_ERR_INVALID_ARG;
+  if (p->scaling < TP_ROPE_NONE || p->scaling > TP_ROPE_YARN) return TP_ERR_INVALID_ARG;
+  if (p->rot_dim < 16 || p->rot_dim > 256 || p->rot_dim % 16) return TP_ERR_SHAPE;
+  auto positive = [](double v) { return v > 0.0 && std::isfinite(v); };
+  if (!(p->theta > 1.0) || !std::isfinite(p->theta)) return TP_ERR_INVALID_ARG;
+  if (p->scaling != TP_ROPE_NONE && !positive(p->factor)) return TP_ERR_INVALID_ARG;
+  if (p->scaling >= TP_ROPE_WAVELENGTH && p->original_len <= 0) return TP_ERR_INVALID_ARG;
+  if (p->scaling == TP_ROPE_WAVELENGTH &&
+      !(positive(p->low_freq_factor) && positive(p->high_freq_factor) && p->low_freq_factor < p->high_freq_factor))
+    return TP_ERR_INVALID_ARG;
+  if (p->scaling == TP_ROPE_YARN && !(positive(p->beta_fast) && positive(p->beta_slow))) return TP_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  std::memset(rope, 0, sizeof *rope);
+  rope->magic = TP_ROPE_MAGIC;
+  rope->rot_dim = p->rot_dim;
+  rope->layout = p->layout;
+  rope->mscale = 1.0f;
+  double lo = 0.0, hi = 0.0;
+  if (p->scaling == TP_ROPE_YARN) {
+    auto dim = [&](double turns) {
+      return p->rot_dim * std::log(p->original_len / (turns * two_pi)) / (2.0 * std::log(p->theta));
+    };
+    lo = std::fmax(0.0, std::floor(dim(p->beta_fast)));
+    hi = std::fmin(p->rot_dim - 1.0, std::ceil(dim(p->beta_slow)));
+    if (p->factor > 1.0) rope->mscale = (float)(0.1 * std::log(p->factor) + 1.0);
+  }
+  for (int i = 0; i < p->rot_dim / 2; ++i) {
+    double f = std::pow(p->theta, -2.0 * i / p->rot_dim), keep = 1.0;
+    if (p->scaling == TP_ROPE_LINEAR) keep = 0.0;
+    if (p->scaling == TP_ROPE_WAVELENGTH) {
+      const double turns = p->original_len * f / two_pi;
+      keep = (turns - p->low_freq_factor) / (p->high_freq_factor - p->low_freq_factor);
+    }
+    if (p->scaling == TP_ROPE_YARN) keep = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 1e-3)));
+    keep = std::fmin(1.0, std::fmax(0.0, keep));
+    if (p->scaling != TP_ROPE_NONE) f = keep * f + (1.0 - keep) * (f / p->factor);
+    // the fraction of a turn per position; whole turns fall away (f above 2 pi only for a factor below 1)
+    const double turn = std::fmod(f / two_pi, 1.0);
+    rope->step[i] = (uint64_t)std::ldexp(turn, 64);
+  }
+  return TP_OK;
+}
+
+tp_status tp_rope_forward(const tp_shape* sh, const tp_rope* rope, const void* qkv, const int32_t* positions, int32_t M,
+                          void* qkv_out, void* stream) {
+  tp_status st = check_shape(sh, TP_W_QKV);
+  if (st != TP_OK) return st;
+  if (!rope || M < 0) return TP_ERR_INVALID_ARG;
+  st = check_rope(rope, sh->head_dim);
+  if (st != TP_OK) return st;
+  if (M == 0) return TP_OK;
+  if (!qkv || !positions || !qkv_out) return TP_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(qkv_out) || !aligned4(positions)) return TP_ERR_ALIGN;
+  const size_t n = (size_t)M * (sh->n_q_heads + 2 * sh->n_kv_heads) * sh->head_dim * 2;
+  if (qkv != qkv_out && overlap(qkv, n, qkv_out, n)) return TP_ERR_INVALID_ARG;
+  RopeArgs a = rope_args(sh, rope, qkv, positions, M, qkv_out);
+  return cuda_status(launch_rope(a, S(stream)));
+}
+
+tp_status tp_rope_append(const tp_shape* sh, const tp_rope* rope, const tp_pages* pages, const void* qkv,
+                         const int32_t* positions, const int32_t* slots, int32_t M, void* q_out, void* k_pages,
+                         void* v_pages, const float* k_scale, const float* v_scale, void* stream) {
+  tp_status st = check_shape(sh, TP_W_QKV);
+  if (st == TP_OK) st = check_pages(pages);
+  if (st != TP_OK) return st;
+  if (M < 0) return TP_ERR_INVALID_ARG;
+  st = check_rope(rope, sh->head_dim);
+  if (st != TP_OK) return st;
+  if (pages->kv_dtype == TP_BF16 && (k_scale || v_scale)) return TP_ERR_INVALID_ARG;
+  if (M == 0) return TP_OK;
+  if (!qkv || (rope && !positions) || !slots || !q_out || !k_pages || !v_pages) return TP_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned4(positions) ||
+      !aligned4(slots) || !aligned4(k_scale) || !aligned4(v_scale))
+    return TP_ERR_ALIGN;
+  const size_t nq = (size_t)M * sh->n_q_heads * sh->head_dim * 2;
+  if (overlap(q_out, nq, qkv, nq + (size_t)M * 2 * sh->n_kv_heads * sh->head_dim * 2)) return TP_ERR_INVALID_ARG;
+  RopeArgs a = rope_args(sh, rope, qkv, positions, M, q_out);
+  a.slots = slots;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.page_shift = page_shift(pages);
+  a.n_pages = pages->n_pages;
+  return cuda_status(launch_rope_append(a, pages->kv_dtype, S(stream)));
+}
+
+size_t tp_paged_attn_workspace_bytes(const tp_shape* sh) {
+  if (check_shape(sh, TP_W_QKV) != TP_OK || !attn_supported(sh->head_dim, sh->n_q_heads / sh->n_kv_heads)) return 0;
+  return paged_attn_workspace_bytes(sh->n_q_heads / sh->n_kv_heads, sh->head_dim);
+}
+
+tp_status tp_paged_attn_decode(const tp_shape* sh, const tp_pages* pages, const void* q, const void* k_pages,
+                               const void* v_pages, const float* k_scale, const float* v_scale,
+                               const int32_t* block_table, const int32_t* lens, int32_t M, float scale, int32_t window,
+                               void* o_in, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  tp_status st = check_shape(sh, TP_W_QKV);
+  if (st == TP_OK) st = check_pages(pages);
+  if (st != TP_OK) return st;
+  if (M < 0 || window < 0 || !std::isfinite(scale)) return TP_ERR_INVALID_ARG;
+  if (pages->kv_dtype == TP_BF16 && (k_scale || v_scale)) return TP_ERR_INVALID_ARG;
+  if (!attn_supported(sh->head_dim, sh->n_q_heads / sh->n_kv_heads)) return TP_ERR_UNSUPPORTED;
+  if (((int64_t)sh->n_kv_heads * pages->n_pages << page_shift(pages)) >= (int64_t(1) << 31)) return TP_ERR_UNSUPPORTED;
+  if (M == 0) return TP_OK;
+  if (!q || !k_pages || !v_pages || !block_table || !lens || !o_in) return TP_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o_in) || !aligned4(block_table) ||
+      !aligned4(lens) || !aligned4(lse) || !aligned4(k_scale) || !aligned4(v_scale))
+    return TP_ERR_ALIGN;
+  if (!ws || ws_bytes < tp_paged_attn_workspace_bytes(sh)) return TP_ERR_WORKSPACE;
+  if (!aligned16(ws)) return TP_ERR_ALIGN;
+  const size_t n = (size_t)M * sh->n_q_heads * sh->head_dim * 2;
+  if (overlap(q, n, o_in, n)) return TP_ERR_INVALID_ARG;  // a request's q is read by several CTAs
+  unsigned* err = tc_error_word();
+  if (!err) return TP_ERR_CUDA;
+  PagedAttnArgs a{static_cast<const bf16*>(q), k_scale, v_scale, block_table, lens, static_cast<bf16*>(o_in), lse,
+                  static_cast<unsigned*>(ws), err, M, sh->t, sh->n_q_heads, sh->n_kv_heads, window,
+                  page_shift(pages), pages->n_pages, pages->max_pages, pages->table_stride,
+                  scale == 0.f ? 1.0f / sqrtf((float)sh->head_dim) : scale};
+  return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
+}
+
+tp_status tp_token_logprobs(const float* logits, int64_t ldl, int32_t M, int32_t vocab, const int32_t* ids, int32_t k,
+                            float* logprob, int32_t* rank, float* entropy, float* top_logprob, int32_t* top_id,
+                            void* stream) {
+  if (M < 0 || vocab <= 0 || ldl < vocab || k < 0 || k > vocab) return TP_ERR_INVALID_ARG;
+  if (k > 32 || vocab >= (1 << 30)) return TP_ERR_UNSUPPORTED;
+  if (M == 0) return TP_OK;
+  if (!logits || (!ids && (logprob || rank)) || (k > 0 && (!top_logprob || !top_id))) return TP_ERR_INVALID_ARG;
+  if (!aligned4(logits) || !aligned4(ids) || !aligned4(logprob) || !aligned4(rank) || !aligned4(entropy) ||
+      !aligned4(top_logprob) || !aligned4(top_id))
+    return TP_ERR_ALIGN;
+  LogprobsArgs a{logits, ldl, ids, logprob, entropy, top_logprob, rank, top_id, M, vocab, k};
+  return cuda_status(launch_token_logprobs(a, S(stream)));
 }
 
 tp_status tp_lm_head_forward(const tp_packed_desc* desc, const void* w, const void* x, int32_t M, float* logits,

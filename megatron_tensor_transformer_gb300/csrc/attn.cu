@@ -27,6 +27,7 @@
 #include <cuda.h>
 
 #include "attn.h"
+#include "attn_mma.cuh"
 #include "common.cuh"
 #include "tc.h"
 #include "tc_ptx.cuh"
@@ -108,29 +109,11 @@ __device__ __forceinline__ float* part_ptr(const AttnGeo& g, float* ws, int m, i
   return ws + (((size_t)m * g.n_kv + gg) * nch + c) * per;
 }
 
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return (uint32_t)f2bf(lo) | ((uint32_t)f2bf(hi) << 16);
-}
-
 // Byte offset of (position r, dim k) in a chunk staged as HD/64 boxes of [P rows][64 dims] in
 // the 128-byte swizzle (the 16-byte piece j of a row sits at j ^ (r & 7)).
 template <int HD>
 __device__ __forceinline__ uint32_t sw_off(int r, int k) {
   return (uint32_t)((k >> 6) * ACfg<HD>::BOX + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) + ((k & 7) << 1));
-}
-
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // ---- the unit list: (sequence m, kv head gg, chunk c) over sequences whose length is in

@@ -1,0 +1,278 @@
+// Log probabilities of given tokens, the row's entropy, the token's rank and the top alternatives, in
+// one pass over fp32 logits.
+//
+//   m = max x,  S = sum e^(x - m),  T = sum e^(x - m) (x - m):
+//   ln P(v) = x_v - m - ln S,   entropy = ln S - T / S   (both terms >= 0: nothing cancels)
+// with m, S, T running per thread in fp32 (when m grows by d, S shrinks by e^-d and T by the same after
+// T += S (m_old - m_new)).  The rank counts the ids ahead of the given one, whose logit is read first.
+//
+// HBM-bound: 4 bytes a logit.  A row is shared by the 1, 2, 4 or 8 CTAs of a cluster, more the fewer
+// rows there are; they join through distributed shared memory, so there is no workspace and one launch.
+//
+// Top alternatives: (logit, id) as one 64-bit key, the greater the further ahead, so ties go to the
+// lower id.  Each warp keeps its 32 best keys, sorted across its lanes.  A new key is compared with the
+// best "k-th best" that any warp of the CTA has found so far, which all k-th best of the row are at
+// least as good as; few pass it (about k ln(n / k) of n), and those are inserted one by one.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "paged.h"
+#include "tc_ptx.cuh"
+
+namespace tpx {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kNT = 512, kNW = kNT / 32, kMaxC = 8;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Orders as (logit, then the lower id first); 0 is below every key of a number.
+__device__ __forceinline__ uint64_t key_of(float x, int id) {
+  uint32_t b = __float_as_uint(x);
+  if (b == 0x80000000u) b = 0;  // -0 equals +0
+  b = b >> 31 ? ~b : b | 0x80000000u;
+  return (uint64_t)b << 32 | (uint32_t)(0x7fffffff - id);
+}
+__device__ __forceinline__ int key_id(uint64_t k) { return 0x7fffffff - (int)(uint32_t)k; }
+__device__ __forceinline__ float key_logit(uint64_t k) {
+  const uint32_t b = (uint32_t)(k >> 32);
+  return __uint_as_float(b >> 31 ? b & 0x7fffffffu : ~b);
+}
+
+// Sums of a part of a row under its maximum (in units of the logits).
+struct Part {
+  float m, S, T;
+};
+__device__ __forceinline__ Part join(const Part& a, const Part& b) {
+  if (a.m == -INFINITY) return b;
+  if (b.m == -INFINITY) return a;
+  const float m = fmaxf(a.m, b.m), da = a.m - m, db = b.m - m;
+  const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
+  // a part that weighs nothing adds nothing (its difference times its sum may be infinite)
+  return {m, a.S * fa + b.S * fb, (fa > 0.f ? (a.T + a.S * da) * fa : 0.f) + (fb > 0.f ? (b.T + b.S * db) * fb : 0.f)};
+}
+
+// The warp's keys, sorted, the best in lane 0: the 32 best of its own and v's (also sorted).
+__device__ __forceinline__ uint64_t merge_sorted(uint64_t mine, uint64_t v, int lane) {
+  const uint64_t r = __shfl_sync(kFull, v, 31 - lane);
+  uint64_t x = mine > r ? mine : r;  // bitonic, holds the 32 best
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t y = __shfl_xor_sync(kFull, x, o);
+    x = (lane & o) ? (x < y ? x : y) : (x > y ? x : y);
+  }
+  return x;
+}
+
+struct Shared {
+  Part part;
+  int ahead, bad;
+  uint64_t top[32];
+};
+
+template <int C>
+__global__ void __launch_bounds__(kNT) logprobs_kernel(const LogprobsArgs a) {
+  __shared__ Shared sh;
+  __shared__ Part s_part[kNW];
+  __shared__ int s_ahead[kNW], s_bad[kNW];
+  __shared__ uint64_t s_top[kNW][32];
+  __shared__ unsigned s_bar;  // the best k-th best logit any warp has found, as an ordered word
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int m = blockIdx.x / C, c = blockIdx.x % C, V = a.vocab, k = a.k;
+  const float* x = a.logits + (int64_t)m * a.ldl;
+  const int id = a.ids ? a.ids[m] : -1;
+  const bool asked = id >= 0 && id < V;
+  const float mine = asked ? x[id] : 0.f;
+  if (tid == 0) s_bar = 0u;
+  __syncthreads();
+
+  // The row from its first 16-byte boundary on, in vectors of four; what is before and behind it goes one by one.
+  const int lead = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / 4), nv = (V - lead) / 4;
+  const int v0 = (int)((int64_t)nv * c / C), v1 = (int)((int64_t)nv * (c + 1) / C);
+  const float4* xv = reinterpret_cast<const float4*>(x + lead);
+  Part p{-INFINITY, 0.f, 0.f};
+  int ahead = 0, bad = 0;
+  uint64_t top = 0;
+  float bar = -INFINITY;  // nothing below it is among the k first
+
+  auto insert = [&](float val, int at, bool there) {  // whole warp: lane's value, if there
+    const uint64_t key = there ? key_of(val, at) : 0;
+    uint64_t kth = __shfl_sync(kFull, top, k - 1);
+    unsigned cand = __ballot_sync(kFull, key > kth);
+    if (!cand) return;
+    do {
+      const uint64_t nk = __shfl_sync(kFull, key, __ffs(cand) - 1);
+      cand &= cand - 1;
+      if (nk > kth) {
+        const uint64_t up = __shfl_up_sync(kFull, top, 1);
+        if (nk > top) top = lane == 0 || nk < up ? nk : up;
+        kth = __shfl_sync(kFull, top, k - 1);
+      }
+    } while (cand);
+    if (lane == 0 && kth) atomicMax(&s_bar, (unsigned)(kth >> 32));
+  };
+  auto take = [&](const float (&v)[4], int at, bool there) {  // four neighbours from id `at` on
+    float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    if (there) {
+      if (mx > p.m) {
+        if (p.m != -INFINITY) {
+          const float d = p.m - mx, f = ex2(d * kLog2e);
+          p.T = f > 0.f ? (p.T + p.S * d) * f : 0.f;  // as in join()
+          p.S *= f;
+        }
+        p.m = mx;
+      }
+      const float base = p.m == -INFINITY ? 0.f : p.m;  // only -inf so far: every weight is 0
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float d = v[j] - base, e = ex2(d * kLog2e);
+        p.S += e;
+        p.T += e > 0.f ? e * d : 0.f;
+        bad |= !(v[j] < INFINITY);
+        ahead += v[j] > mine || (v[j] == mine && at + j < id);
+      }
+    }
+    if (k > 0) {
+      if (__any_sync(kFull, there && mx >= bar)) {
+        const unsigned w = *reinterpret_cast<volatile unsigned*>(&s_bar);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) insert(v[j], at + j, there && v[j] >= bar);
+        bar = w ? key_logit((uint64_t)w << 32) : -INFINITY;
+      }
+    }
+  };
+  const int steps = (v1 - v0 + kNT - 1) / kNT;
+  for (int s = 0; s < steps; ++s) {
+    const int i = v0 + s * kNT + tid;
+    const bool there = i < v1;
+    float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (there) {
+      const float4 q = __ldcs(xv + i);
+      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    }
+    take(v, lead + 4 * i, there);
+  }
+  if (c == 0 && warp == 0) {  // the ends, at most three values each
+    const int at = lane < 4 ? lane : lead + 4 * nv + lane - 4;
+    const bool there = lane < 4 ? lane < lead : lane < 8 && at < V;
+    const float v = there ? x[at] : -INFINITY;
+    if (there) {
+      p = join(p, Part{v, v == -INFINITY ? 0.f : 1.f, 0.f});
+      bad |= !(v < INFINITY);
+      ahead += v > mine || (v == mine && at < id);
+    }
+    if (k > 0) insert(v, at, there);
+  }
+
+  // the warp's, the CTA's, the cluster's
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Part q{__shfl_xor_sync(kFull, p.m, o), __shfl_xor_sync(kFull, p.S, o), __shfl_xor_sync(kFull, p.T, o)};
+    p = join(p, q);
+    ahead += __shfl_xor_sync(kFull, ahead, o);
+    bad |= __shfl_xor_sync(kFull, bad, o);
+  }
+  if (lane == 0) {
+    s_part[warp] = p;
+    s_ahead[warp] = ahead;
+    s_bad[warp] = bad;
+  }
+  s_top[warp][lane] = top;
+  __syncthreads();
+  if (k > 0) {
+#pragma unroll
+    for (int o = kNW / 2; o > 0; o >>= 1) {
+      if (warp < o) {
+        top = merge_sorted(top, s_top[warp + o][lane], lane);
+        s_top[warp][lane] = top;
+      }
+      __syncthreads();
+    }
+  }
+  if (warp == 0) {
+    p = Part{-INFINITY, 0.f, 0.f};
+    ahead = bad = 0;
+    for (int w = 0; w < kNW; ++w) {
+      p = join(p, s_part[w]);
+      ahead += s_ahead[w];
+      bad |= s_bad[w];
+    }
+    if (C > 1) {
+      if (lane == 0) {
+        sh.part = p;
+        sh.ahead = ahead;
+        sh.bad = bad;
+      }
+      sh.top[lane] = top;
+    }
+  }
+  if (C > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    if (c == 0 && warp == 0) {
+      for (int r = 1; r < C; ++r) {
+        const Shared* o = cl.map_shared_rank(&sh, r);
+        p = join(p, o->part);
+        ahead += o->ahead;
+        bad |= o->bad;
+        if (k > 0) top = merge_sorted(top, o->top[lane], lane);
+      }
+    }
+    cl.sync();  // the others' shared memory is read until here
+  }
+  if (c != 0 || warp != 0) return;
+  const bool none = bad || p.m == -INFINITY;
+  const float lnS = logf(p.S);
+  if (lane == 0) {
+    if (a.logprob) a.logprob[m] = !asked ? 0.f : none ? NAN : mine - p.m - lnS;
+    if (a.rank) a.rank[m] = !asked || none ? 0 : ahead + 1;
+    if (a.entropy) a.entropy[m] = none ? NAN : lnS - p.T / p.S;
+  }
+  if (lane < k) {
+    a.top_logprob[(size_t)m * k + lane] = none ? NAN : key_logit(top) - p.m - lnS;
+    a.top_id[(size_t)m * k + lane] = none ? -1 : key_id(top);
+  }
+}
+
+template <int C>
+cudaError_t launch(const LogprobsArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.M * C);
+  cfg.blockDim = dim3(kNT);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, logprobs_kernel<C>, a);
+  note_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogprobsArgs& a, cudaStream_t st) {
+  // CTAs per row: two per SM over all rows, while each still has 4 vectors per thread
+  int c = 1;
+  while (c < kMaxC && (int64_t)a.M * c < 152 * 2 && a.vocab / (2 * c) >= 4 * 4 * kNT) c *= 2;
+  return c == 1 ? launch<1>(a, st) : c == 2 ? launch<2>(a, st) : c == 4 ? launch<4>(a, st) : launch<8>(a, st);
+}
+
+}  // namespace tpx

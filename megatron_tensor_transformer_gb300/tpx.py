@@ -21,6 +21,8 @@ TP_F_KERNEL_SKINNY, TP_F_KERNEL_TC, TP_F_SERIAL, TP_F_SPLIT_BLOCK = 0x10, 0x20, 
 TP_F_FP8_ACT = 0x200
 TP_F_FP8_HILO = 0x400
 TP_F_FOLD_NORM = 0x800
+TP_ROPE_HALF, TP_ROPE_INTERLEAVED = 0, 1
+TP_ROPE_NONE, TP_ROPE_LINEAR, TP_ROPE_WAVELENGTH, TP_ROPE_YARN = 0, 1, 2, 3
 
 EXPORTS = ["tp_packed_bytes", "tp_describe", "tp_partition_weights", "tp_workspace_bytes",
            "tp_mlp_forward", "tp_proj_forward", "tp_reduce_partials", "tp_colpar_forward",
@@ -28,7 +30,9 @@ EXPORTS = ["tp_packed_bytes", "tp_describe", "tp_partition_weights", "tp_workspa
            "tp_noalloc_scratch_capacity", "tp_rmsnorm", "tp_selftest_bounded_wait",
            "tp_layer_scratch_bytes", "tp_layer_forward", "tp_selftest_e4m3_decode", "tp_sync", "tp_status_str", "tp_launch_count",
            "tp_lm_head_forward", "tp_embed_lookup", "tp_attn_workspace_bytes", "tp_attn_decode",
-           "tp_attn_block_workspace_bytes", "tp_attn_block_forward", "tp_quantize_fp8_per_token"]
+           "tp_attn_block_workspace_bytes", "tp_attn_block_forward", "tp_quantize_fp8_per_token",
+           "tp_paged_tables", "tp_rope_describe", "tp_rope_forward", "tp_rope_append",
+           "tp_paged_attn_workspace_bytes", "tp_paged_attn_decode", "tp_token_logprobs"]
 
 
 class TpxError(RuntimeError):
@@ -49,6 +53,25 @@ class PackedDesc(ctypes.Structure):
                 ("rows_per_shard", ctypes.c_int64), ("k_per_shard", ctypes.c_int64),
                 ("shard_payload_bytes", ctypes.c_uint64), ("scales_offset", ctypes.c_uint64),
                 ("shard_stride_bytes", ctypes.c_uint64), ("total_bytes", ctypes.c_uint64)]
+
+
+class Pages(ctypes.Structure):
+    """Geometry of a paged key-value cache (tp_pages)."""
+    _fields_ = [("kv_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_len", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low_freq_factor", ctypes.c_double), ("high_freq_factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
+
+
+class Rope(ctypes.Structure):
+    """A described rotation (tp_rope)."""
+    _fields_ = [("magic", ctypes.c_uint32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("step", ctypes.c_uint64 * 128)]
 
 
 _lib = None
@@ -92,6 +115,14 @@ def lib():
             "tp_attn_block_forward": (I32, [P(PackedDesc), V, P(PackedDesc), V, V, V, I32, V, V, I32, V, V, V, V,
                                             V, SZ, U32, V]),
             "tp_launch_count": (ctypes.c_uint64, []),
+            "tp_paged_tables": (I32, [P(Pages), V, V, I32, V, I32, V, V, V, V, V, V, I32, V, V]),
+            "tp_rope_describe": (I32, [P(RopeParams), P(Rope)]),
+            "tp_rope_forward": (I32, [P(Shape), P(Rope), V, V, I32, V, V]),
+            "tp_rope_append": (I32, [P(Shape), P(Rope), P(Pages), V, V, V, I32, V, V, V, V, V, V]),
+            "tp_paged_attn_workspace_bytes": (SZ, [P(Shape)]),
+            "tp_paged_attn_decode": (I32, [P(Shape), P(Pages), V, V, V, V, V, V, V, I32, ctypes.c_float, I32, V, V, V,
+                                           SZ, V]),
+            "tp_token_logprobs": (I32, [V, ctypes.c_int64, I32, I32, V, I32, V, V, V, V, V, V]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -299,3 +330,78 @@ def tp_attn_decode(shape, qkv, k_cache, v_cache, lens, o_in, ws, stream=None):
                                 qkv.shape[0], _ptr(o_in), _ptr(ws), ws.numel(), _stream(stream)), "tp_attn_decode")
     return o_in
 
+
+def make_pages(page_size, n_pages, max_pages, kv_dtype=TP_BF16, table_stride=None):
+    """Geometry of a paged cache; max_pages: page ids in a row of the block table."""
+    return Pages(kv_dtype, page_size, n_pages, max_pages, max_pages if table_stride is None else table_stride)
+
+
+def tp_rope_describe(params):
+    r = Rope()
+    _check(lib().tp_rope_describe(ctypes.byref(params), ctypes.byref(r)), "tp_rope_describe")
+    return r
+
+
+def make_rope(rot_dim, theta=10000.0, layout=TP_ROPE_HALF, scaling=TP_ROPE_NONE, factor=1.0, original_len=0,
+              low_freq_factor=1.0, high_freq_factor=4.0, beta_fast=32.0, beta_slow=1.0):
+    return tp_rope_describe(RopeParams(rot_dim, layout, scaling, original_len, theta, factor, low_freq_factor,
+                                       high_freq_factor, beta_fast, beta_slow))
+
+
+def tp_paged_tables(pages, lens, add, free_pages, block_table, lens_out, cu_rows, positions, slots, counts, head=None,
+                    stream=None):
+    """All int32 on the device: lens, add, lens_out [M]; free_pages [n_free]; block_table [M, table_stride]; cu_rows
+    [M + 1]; positions, slots [rows]; counts [3]; head: one element or None.  Returns slots."""
+    _check(lib().tp_paged_tables(ctypes.byref(pages), _ptr(lens), _ptr(add), lens.shape[0], _ptr(free_pages),
+                                 free_pages.shape[0], _ptr(head), _ptr(block_table), _ptr(lens_out), _ptr(cu_rows),
+                                 _ptr(positions), _ptr(slots), slots.shape[0], _ptr(counts), _stream(stream)),
+           "tp_paged_tables")
+    return slots
+
+
+def tp_rope_forward(shape, rope, qkv, positions, qkv_out, stream=None):
+    """qkv, qkv_out (may be qkv): [M, (n_q + 2 n_kv) hd] bf16; positions: [M] int32 on the device."""
+    _check(lib().tp_rope_forward(ctypes.byref(shape), ctypes.byref(rope), _ptr(qkv), _ptr(positions), qkv.shape[0],
+                                 _ptr(qkv_out), _stream(stream)), "tp_rope_forward")
+    return qkv_out
+
+
+def tp_rope_append(shape, rope, pages, qkv, positions, slots, q_out, k_pages, v_pages, k_scale=None, v_scale=None,
+                   stream=None):
+    """q_out: [M, n_q hd] bf16; k_pages, v_pages: [t, n_pages, n_kv/t, page_size, hd], bf16 or e4m3 codes with scales
+    [n_kv] fp32; positions, slots: [M] int32 on the device.  rope None: append without turning."""
+    _check(lib().tp_rope_append(ctypes.byref(shape), None if rope is None else ctypes.byref(rope), ctypes.byref(pages),
+                                _ptr(qkv), _ptr(positions), _ptr(slots), qkv.shape[0], _ptr(q_out), _ptr(k_pages),
+                                _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _stream(stream)), "tp_rope_append")
+    return q_out
+
+
+def tp_paged_attn_workspace_bytes(shape):
+    return lib().tp_paged_attn_workspace_bytes(ctypes.byref(shape))
+
+
+def new_paged_attn_workspace(shape, device):
+    """Zero-filled workspace of tp_paged_attn_decode (its counters start at zero), for every M and length."""
+    return torch.zeros(max(1, tp_paged_attn_workspace_bytes(shape)), dtype=torch.uint8, device=device)
+
+
+def tp_paged_attn_decode(shape, pages, q, k_pages, v_pages, block_table, lens, o_in, ws, lse=None, scale=0.0, window=0,
+                         k_scale=None, v_scale=None, stream=None):
+    """q, o_in: [M, n_q hd] bf16; lse: [M, n_q] fp32 or None; block_table: [M, table_stride], lens: [M] int32 on the
+    device; the pages as for tp_rope_append."""
+    _check(lib().tp_paged_attn_decode(ctypes.byref(shape), ctypes.byref(pages), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+                                      _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(lens), q.shape[0], scale,
+                                      window, _ptr(o_in), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+           "tp_paged_attn_decode")
+    return o_in
+
+
+def tp_token_logprobs(logits, ids, logprob, entropy, rank, top_logprob=None, top_id=None, stream=None):
+    """logits: [M, vocab] fp32, rows logits.stride(0) apart; ids, rank: [M] int32; logprob, entropy: [M] fp32;
+    top_logprob, top_id: [M, k] or None (all on the device; ids, logprob, entropy and rank may be None)."""
+    k = 0 if top_id is None else top_id.shape[1]
+    ldl = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+    _check(lib().tp_token_logprobs(_ptr(logits), ldl, logits.shape[0], logits.shape[1], _ptr(ids), k, _ptr(logprob),
+                                   _ptr(rank), _ptr(entropy), _ptr(top_logprob), _ptr(top_id), _stream(stream)),
+           "tp_token_logprobs")
+    return logprob
