@@ -141,15 +141,18 @@ def _check(st, where):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized():
         if not torch.cuda.is_available():
-            return ctypes.c_void_p(None)
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+            return None
+        torch.cuda.init()
+    # the current stream's handle, without a Stream object: a decode step makes many short calls
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def make_shape(d, ffn=0, n_q=0, n_kv=0, hd=0, t=1, wtype=TP_BF16, vocab=0):
