@@ -10,9 +10,12 @@
 // rows there are; they join through distributed shared memory, so there is no workspace and one launch.
 //
 // Top alternatives: (logit, id) as one 64-bit key, the greater the further ahead, so ties go to the
-// lower id.  Each warp keeps its 32 best keys, sorted across its lanes.  A new key is compared with the
-// best "k-th best" that any warp of the CTA has found so far, which all k-th best of the row are at
-// least as good as; few pass it (about k ln(n / k) of n), and those are inserted one by one.
+// lower id.  Each warp keeps its best keys, sorted across its lanes, and inserts new ones one by one, so
+// few must come that far: a value is a candidate only if it reaches the bar, the k-th largest of the 64
+// maxima that the CTA's groups of 8 threads have seen so far (k values reach it, so no smaller one is
+// among the k first).  The bar is taken anew after 1, 2, 4, 8, .. rounds, before the round's own values
+// are looked at; on average it lies near the k-th largest value so far, and about k ln(n / n_0) of a
+// CTA's n values pass it, whatever the number of warps.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -29,12 +32,20 @@ namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kNT = 512, kNW = kNT / 32, kMaxC = 8;
+constexpr int kNT = 512, kNW = kNT / 32, kMaxC = 8, kVec = 4;
+static_assert(kNT == 64 * 8, "raise_bar takes 64 groups");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// the larger of the two, NaN if x is one (fmaxf drops it)
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
 }
 
 // Orders as (logit, then the lower id first); 0 is below every key of a number.
@@ -50,13 +61,14 @@ __device__ __forceinline__ float key_logit(uint64_t k) {
   return __uint_as_float(b >> 31 ? b & 0x7fffffffu : ~b);
 }
 
-// Sums of a part of a row under its maximum (in units of the logits).
+// Sums of a part of a row under its maximum (in units of the logits).  S is 0 where there is nothing but
+// -inf, and NaN where there was a NaN or +inf (whose difference to the maximum is NaN), for good.
 struct Part {
   float m, S, T;
 };
 __device__ __forceinline__ Part join(const Part& a, const Part& b) {
-  if (a.m == -INFINITY) return b;
-  if (b.m == -INFINITY) return a;
+  if (a.S == 0.f) return b;
+  if (b.S == 0.f) return a;
   const float m = fmaxf(a.m, b.m), da = a.m - m, db = b.m - m;
   const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
   // a part that weighs nothing adds nothing (its difference times its sum may be infinite)
@@ -77,17 +89,17 @@ __device__ __forceinline__ uint64_t merge_sorted(uint64_t mine, uint64_t v, int 
 
 struct Shared {
   Part part;
-  int ahead, bad;
+  int ahead;
   uint64_t top[32];
 };
 
 template <int C>
-__global__ void __launch_bounds__(kNT) logprobs_kernel(const LogprobsArgs a) {
+__global__ void __launch_bounds__(kNT, 2) logprobs_kernel(const LogprobsArgs a) {
   __shared__ Shared sh;
   __shared__ Part s_part[kNW];
-  __shared__ int s_ahead[kNW], s_bad[kNW];
+  __shared__ int s_ahead[kNW];
   __shared__ uint64_t s_top[kNW][32];
-  __shared__ unsigned s_bar;  // the best k-th best logit any warp has found, as an ordered word
+  __shared__ float s_max[64], s_bar;  // maxima of groups of 8 threads; the bar
   tc::griddep_launch_dependents();
   tc::griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -96,15 +108,13 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LogprobsArgs a) {
   const int id = a.ids ? a.ids[m] : -1;
   const bool asked = id >= 0 && id < V;
   const float mine = asked ? x[id] : 0.f;
-  if (tid == 0) s_bar = 0u;
-  __syncthreads();
 
   // The row from its first 16-byte boundary on, in vectors of four; what is before and behind it goes one by one.
   const int lead = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / 4), nv = (V - lead) / 4;
   const int v0 = (int)((int64_t)nv * c / C), v1 = (int)((int64_t)nv * (c + 1) / C);
   const float4* xv = reinterpret_cast<const float4*>(x + lead);
   Part p{-INFINITY, 0.f, 0.f};
-  int ahead = 0, bad = 0;
+  int ahead = 0;
   uint64_t top = 0;
   float bar = -INFINITY;  // nothing below it is among the k first
 
@@ -112,8 +122,7 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LogprobsArgs a) {
     const uint64_t key = there ? key_of(val, at) : 0;
     uint64_t kth = __shfl_sync(kFull, top, k - 1);
     unsigned cand = __ballot_sync(kFull, key > kth);
-    if (!cand) return;
-    do {
+    while (cand) {
       const uint64_t nk = __shfl_sync(kFull, key, __ffs(cand) - 1);
       cand &= cand - 1;
       if (nk > kth) {
@@ -121,57 +130,95 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LogprobsArgs a) {
         if (nk > top) top = lane == 0 || nk < up ? nk : up;
         kth = __shfl_sync(kFull, top, k - 1);
       }
-    } while (cand);
-    if (lane == 0 && kth) atomicMax(&s_bar, (unsigned)(kth >> 32));
+    }
   };
-  auto take = [&](const float (&v)[4], int at, bool there) {  // four neighbours from id `at` on
-    float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-    if (there) {
-      if (mx > p.m) {
-        if (p.m != -INFINITY) {
-          const float d = p.m - mx, f = ex2(d * kLog2e);
-          p.T = f > 0.f ? (p.T + p.S * d) * f : 0.f;  // as in join()
-          p.S *= f;
-        }
-        p.m = mx;
-      }
-      const float base = p.m == -INFINITY ? 0.f : p.m;  // only -inf so far: every weight is 0
+  auto raise_bar = [&](float seen) {  // whole CTA; seen: the thread's maximum so far
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float d = v[j] - base, e = ex2(d * kLog2e);
+    for (int o = 1; o < 8; o <<= 1) seen = fmaxf(seen, __shfl_xor_sync(kFull, seen, o));
+    if ((lane & 7) == 0) s_max[warp * 4 + (lane >> 3)] = seen;
+    __syncthreads();
+    if (warp == 0) {  // the 32 largest of 64, sorted
+      float lo = s_max[lane], hi = s_max[32 + lane];
+#pragma unroll
+      for (int n = 2; n <= 32; n <<= 1) {
+#pragma unroll
+        for (int o = n >> 1; o > 0; o >>= 1) {
+          const float pl = __shfl_xor_sync(kFull, lo, o), ph = __shfl_xor_sync(kFull, hi, o);
+          const bool desc = (lane & n) == 0 || n == 32, first = (lane & o) == 0;
+          lo = desc == first ? fmaxf(lo, pl) : fminf(lo, pl);
+          hi = desc == first ? fmaxf(hi, ph) : fminf(hi, ph);
+        }
+      }
+      const float rev = __shfl_sync(kFull, hi, 31 - lane);
+      float x32 = fmaxf(lo, rev);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float y = __shfl_xor_sync(kFull, x32, o);
+        x32 = (lane & o) ? fminf(x32, y) : fmaxf(x32, y);
+      }
+      if (lane == k - 1) s_bar = x32;
+    }
+    __syncthreads();
+    bar = s_bar;
+  };
+  const int rounds = (v1 - v0 + kNT * kVec - 1) / (kNT * kVec);
+  for (int r = 0; r < rounds; ++r) {
+    const int i0 = v0 + r * kNT * kVec + tid;
+    float v[kVec][4];
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      const int i = i0 + u * kNT;
+      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (i < v1) q = __ldcs(xv + i);
+      v[u][0] = q.x, v[u][1] = q.y, v[u][2] = q.z, v[u][3] = q.w;
+    }
+    float mx[kVec], all = p.m;
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      mx[u] = fmaxf(fmaxf(v[u][0], v[u][1]), fmaxf(v[u][2], v[u][3]));
+      all = fmaxf(all, mx[u]);
+    }
+    if (all > p.m) {
+      if (p.m != -INFINITY) {
+        const float d = p.m - all, f = ex2(d * kLog2e);
+        p.T = f > 0.f ? (p.T + p.S * d) * f : 0.f;  // as in join()
+        p.S *= f;
+      }
+      p.m = all;
+    }
+    const float base = p.m == -INFINITY ? 0.f : p.m;  // only -inf so far: every weight is 0
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // a vector that is not there holds -inf: no weight
+        const float d = max_nan(v[u][j] - base, -1e4f), e = ex2(d * kLog2e);
         p.S += e;
-        p.T += e > 0.f ? e * d : 0.f;
-        bad |= !(v[j] < INFINITY);
-        ahead += v[j] > mine || (v[j] == mine && at + j < id);
+        p.T += e * d;
+      }
+      if (mx[u] >= mine && i0 + u * kNT < v1) {
+        const int at = lead + 4 * (i0 + u * kNT);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ahead += v[u][j] > mine || (v[u][j] == mine && at + j < id);
       }
     }
     if (k > 0) {
-      if (__any_sync(kFull, there && mx >= bar)) {
-        const unsigned w = *reinterpret_cast<volatile unsigned*>(&s_bar);
+      if ((r & (r + 1)) == 0) raise_bar(p.m);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) insert(v[j], at + j, there && v[j] >= bar);
-        bar = w ? key_logit((uint64_t)w << 32) : -INFINITY;
+      for (int u = 0; u < kVec; ++u) {
+        const bool there = i0 + u * kNT < v1;
+        if (__any_sync(kFull, there && mx[u] >= bar)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) insert(v[u][j], lead + 4 * (i0 + u * kNT) + j, there && v[u][j] >= bar);
+        }
       }
     }
-  };
-  const int steps = (v1 - v0 + kNT - 1) / kNT;
-  for (int s = 0; s < steps; ++s) {
-    const int i = v0 + s * kNT + tid;
-    const bool there = i < v1;
-    float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (there) {
-      const float4 q = __ldcs(xv + i);
-      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    }
-    take(v, lead + 4 * i, there);
   }
   if (c == 0 && warp == 0) {  // the ends, at most three values each
     const int at = lane < 4 ? lane : lead + 4 * nv + lane - 4;
     const bool there = lane < 4 ? lane < lead : lane < 8 && at < V;
     const float v = there ? x[at] : -INFINITY;
     if (there) {
-      p = join(p, Part{v, v == -INFINITY ? 0.f : 1.f, 0.f});
-      bad |= !(v < INFINITY);
+      p = join(p, Part{v, v == -INFINITY ? 0.f : v < INFINITY ? 1.f : NAN, 0.f});
       ahead += v > mine || (v == mine && at < id);
     }
     if (k > 0) insert(v, at, there);
@@ -183,12 +230,10 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LogprobsArgs a) {
     const Part q{__shfl_xor_sync(kFull, p.m, o), __shfl_xor_sync(kFull, p.S, o), __shfl_xor_sync(kFull, p.T, o)};
     p = join(p, q);
     ahead += __shfl_xor_sync(kFull, ahead, o);
-    bad |= __shfl_xor_sync(kFull, bad, o);
   }
   if (lane == 0) {
     s_part[warp] = p;
     s_ahead[warp] = ahead;
-    s_bad[warp] = bad;
   }
   s_top[warp][lane] = top;
   __syncthreads();
@@ -204,17 +249,15 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LogprobsArgs a) {
   }
   if (warp == 0) {
     p = Part{-INFINITY, 0.f, 0.f};
-    ahead = bad = 0;
+    ahead = 0;
     for (int w = 0; w < kNW; ++w) {
       p = join(p, s_part[w]);
       ahead += s_ahead[w];
-      bad |= s_bad[w];
     }
     if (C > 1) {
       if (lane == 0) {
         sh.part = p;
         sh.ahead = ahead;
-        sh.bad = bad;
       }
       sh.top[lane] = top;
     }
@@ -227,14 +270,13 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LogprobsArgs a) {
         const Shared* o = cl.map_shared_rank(&sh, r);
         p = join(p, o->part);
         ahead += o->ahead;
-        bad |= o->bad;
         if (k > 0) top = merge_sorted(top, o->top[lane], lane);
       }
     }
     cl.sync();  // the others' shared memory is read until here
   }
   if (c != 0 || warp != 0) return;
-  const bool none = bad || p.m == -INFINITY;
+  const bool none = !(p.S > 0.f);
   const float lnS = logf(p.S);
   if (lane == 0) {
     if (a.logprob) a.logprob[m] = !asked ? 0.f : none ? NAN : mine - p.m - lnS;
