@@ -2,7 +2,7 @@
 //
 // The angle of pair i at position p is p * f_i.  In fp32 that product alone is off by 2^-24 p f_i
 // radians (0.06 at p = 10^6), so it is taken in turns as a 64-bit binary fraction: p * step_i modulo
-// 2^64, whose wrap-around is the reduction modulo whole turns.  The nearest eighth... quarter turn is
+// 2^64, whose wrap-around is the reduction modulo whole turns.  The nearest quarter turn is
 // split off as an integer and the rest, at most 1/8 turn, goes to sincospi in fp32: cos and sin are
 // good to about an fp32 ulp at every position, and no 64-bit floating point is used.
 //
@@ -22,7 +22,7 @@ namespace {
 
 enum { SINK_QKV = 0, SINK_BF16 = 1, SINK_E4M3 = 2 };
 
-constexpr int kTok = 4;  // tokens per CTA at most
+constexpr int kTok = 2;  // tokens per CTA at most
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -52,7 +52,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
 
 // grid (token groups, head groups), block (hd / 16, heads a pass)
 template <int SINK>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a, int toks, int heads) {
+__global__ void __launch_bounds__(256, 6) rope_kernel(const __grid_constant__ RopeArgs a, int toks, int heads) {
   __shared__ __align__(16) float cs[kTok][2][128];
   tc::griddep_launch_dependents();
   tc::griddep_wait();
