@@ -376,8 +376,8 @@ class Case:
             ro, rl, A, B = PO.attention(q[m], rows(k, sc[0]), rows(v, sc[1]), factor, window)
             # A score is a sum of hd exact products in fp32 (at most hd steps of 2^-23 of sum |q||k|), times a few
             # factors rounded to fp32: (hd + 8) 2^-23 B.  e^x: 2^-21 (the argument's rounding and ex2).  P enters
-            # the product in two bf16 (2^-16) or in fp16 (2^-11; below 2^-14 of the running maximum an absolute
-            # 2^-25 each, against a sum of at least 1); the sums over n positions, 16 at a time per warp:
+            # the product in two bf16 (2^-16) or in three e4m3 (2^-12, or an absolute 2^-25 each, against a sum of
+            # at least 1/2: the 2^-11 and 2^-25 n below cover both); the sums over n positions, 16 at a time:
             # n / 16 + 300 steps of 2^-24.  All of it twice, in the numerator and in the sum.
             ps = (self.hd + 8) * 2.0 ** -23 * B + 2.0 ** -21 + (n / 16 + 300) * 2.0 ** -24
             pp = 2.0 ** -16 if self.kv == tpx.TP_BF16 else 2.0 ** -11
