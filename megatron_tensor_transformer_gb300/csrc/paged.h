@@ -36,13 +36,13 @@ struct PagedAttnArgs {
   const int32_t *table, *lens;
   __nv_bfloat16* o;
   float* lse;    // or nullptr
-  unsigned* ws;  // kPagedCounters counters, then the pieces
+  unsigned* ws;  // counters, then the pieces
   unsigned* err;
   int32_t M, t, n_q, n_kv, window;
   int32_t page_shift, n_pages, max_pages, table_stride;
   float scale;
 };
-// one counter per CTA that can start a split (request, kv head); the largest grid
+// the largest grid
 constexpr int kPagedMaxCtas = 256;
 size_t paged_attn_workspace_bytes(int G, int hd);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,

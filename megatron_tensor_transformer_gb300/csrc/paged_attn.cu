@@ -8,13 +8,17 @@
 // maximum takes its place and what was summed is scaled down.  Scores are held times log2 e, for ex2.
 //
 // HBM-bound: the cache is read once, 4 flops per q head and element.  One persistent CTA per SM; the
-// work is a list of units (request, kv head, chunk of 128 positions) split evenly over the CTAs in
-// order, so that one long request and many short ones load all SMs alike.  Both products run on
-// tcgen05 with the cache as the 128-row operand, straight from where TMA put it:
+// work is a list of (request, kv head)s, each a run of 128-position chunks after a fixed cost for its
+// beginning and end, and is split evenly over the CTAs in order, so that one long request and many short
+// ones load all SMs alike.  (Items handed out by a counter balanced the SMs better, whose shares of the
+// HBM differ by 10%, but looking an item up cost each more than that: 110 us instead of XX for 131071 tokens.)
+// Both products run on tcgen05 with the cache as the 128-row operand, straight from where TMA put it:
 //   S^T [128 positions, 16 heads] = K Q^T      K as it lies (rows of positions), Q padded to 16 heads
 //   O^T [dims, 16 heads]         += V^T P^T    V as it lies too, read as the transposed operand
-// so no byte of k or v passes through registers.  A thread of the softmax warps holds one position
-// and half of the heads; maxima are looked for across threads only when a score passes the step.
+// so no byte of k or v passes through registers.  Two softmax teams take the chunks in turn, each with
+// its own reference, sum and O^T (joined at the item's end), so one chunk's exponentials run beside the
+// other's waits.  A thread holds one position and 4 or 8 heads; maxima are looked for across threads only
+// when a score passes the step.
 //   bf16 pages: P enters the product as two bf16 (its rounding and the rest), so that P's rounding
 //     does not show beside the output's own; the tensor cores have the time.
 //   e4m3 pages: e4m3 products (kind::f8f6f4).  q is split into two codes (q / 2^e = hi + lo, all of a
@@ -26,13 +30,14 @@
 // are added when tensor memory is read: an MMA costs the 128-row operand's way out of shared memory,
 // whatever N is, so a code more costs nothing and an MMA more does (62 cycles alone, 150 beside TMA's
 // writes; one MMA per code took 120.8 us for 131071 tokens of the 70B heads).
-// Warps: 0-7 softmax, 8 TMA producer (lane i looks up the page of box i and copies it: 16 to 128
-// positions by 128 bytes), 9 issues the scores' MMAs and 11 those of P V, each as soon as its operands are
-// there (one thread for both made every chunk wait for the one before: 107.1 us instead of 95.5 for 131071 tokens),
-// 10 brings the q of the next (request, kv head).
-// A (request, kv head) that is split over CTAs leaves a piece per CTA (sum of p v, ref, sum) and the
-// CTA that counts in last joins the pieces in order.  Every sum's order follows from the lengths and
-// the SM count: runs repeat bit for bit.
+// Warps: the softmax teams; a TMA producer (lane i looks up the page of box i and copies it: 16 to 128
+// positions by 128 bytes); one issuing the scores' MMAs and one those of P V, each as soon as its operands are
+// there (one thread for both made every chunk wait for the one before: 107.1 us instead of 95.5 for 131071
+// tokens); one that walks the CTA's items (its part of a (request, kv head)) and brings their q.
+// A (request, kv head) that is split over CTAs leaves a piece per CTA (sum of p v, ref, sum) in the workspace;
+// the CTA that counts in last joins up to kFan of them in order, and the last of those joins these (one CTA
+// joining 19 pieces took 10 us).  Every sum's order follows from the lengths and the SM count: runs repeat
+// bit for bit.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -53,9 +58,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kP = 128;                    // positions per chunk: the rows of an MMA
 constexpr int kN = 16;                     // heads of an MMA (its columns)
-constexpr int kSoft = 256;                 // softmax threads
-constexpr int kThreads = kSoft + 128;      // and the producer, the q warp and one MMA warp per product
 constexpr int kMasks = 32;                 // ring of the chunks' masks: above the chunks in flight
+constexpr int kFan = 8;                    // pieces joined at once
+constexpr int kSlots = 2 * kPagedMaxCtas;  // pieces: a split (request, kv head) is a CTA's first item or its last
+constexpr int kWsHead = 2 * kSlots;        // counters: by the slot of the first of kFan pieces, then of the first of all
 
 template <int HD, bool FP8>
 struct PCfg {
@@ -75,10 +81,13 @@ struct PCfg {
   static constexpr float kStep = FP8 ? 1.f : 8.f;                 // ref may be behind the maximum by this
   static constexpr float kPMul = FP8 ? 128.f : 1.f;               // P is held times this: up to 256 in e4m3
   static constexpr float kNext = FP8 ? 16.f : 1.f;                // each code of P after the first is held times this
-  static constexpr uint32_t kCols = FP8 || NB == 2 ? 256 : 128;   // TMEM: S [2][QTERMS][16], O [2][NB][TERMS][16]
-  static_assert(2 * kN * (QTERMS + NB * TERMS) <= (int)kCols, "TMEM");
+  static constexpr int kUsed = 2 * kN * (QTERMS + 2 * NB * TERMS);  // TMEM: S [2][QTERMS][16], O [2][team][NB][TERMS][16]
+  static constexpr uint32_t kCols = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
+  // A chunk is two units of work, and a (request, kv head)'s beginning and end about 1 us: one unit where a
+  // chunk's 64 KB or more take 1.4 us or more at an SM's share of the HBM, else three.
+  static constexpr int kEnds = STAGE >= 32 * 1024 ? 1 : 3;
   static constexpr size_t kRing = (size_t)NS * STAGE;
-  static constexpr size_t SMEM = 1024 + kRing + 2 * TERMS * PTILE + 2 * QTILE;
+  static constexpr size_t SMEM = kRing + 2 * TERMS * PTILE + 2 * QTILE;
   static_assert(NS >= 3, "a chunk's k and v and the next one's k");
 };
 
@@ -172,36 +181,25 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, int m) {
   return s;
 }
 
-// A unit: chunk c of (m, gg).  `seg` counts the (m, gg) that the CTA has begun.
-struct Cursor {
-  int m, gg, c, seg;
-  Span s;
-  __device__ __forceinline__ bool ends() const { return c + 1 == s.c1; }
-};
-__device__ __forceinline__ void advance(const PagedAttnArgs& a, Cursor& cu) {  // only when there is a next unit
-  if (++cu.c < cu.s.c1) return;
-  ++cu.seg;
-  if (++cu.gg == a.n_kv) {
-    cu.gg = 0;
-    do {
-      ++cu.m;
-      cu.s = span_of(a, cu.m);
-    } while (cu.s.c0 == cu.s.c1 && cu.m + 1 < a.M);
-  }
-  cu.c = cu.s.c0;
-}
-// Bits of the chunk's 16-position groups with a position that counts: within [lo, n) and loaded.
-__device__ __forceinline__ uint32_t group_bits(const Cursor& cu, uint32_t loaded) {
-  const int a0 = max(0, cu.s.lo - cu.c * kP), a1 = min(kP, cu.s.n - cu.c * kP);
-  return loaded & ((1u << ((a1 + 15) >> 4)) - 1) & ~((1u << (a0 >> 4)) - 1);
-}
-
-// CTA i of nct (at most U) takes units [U i / nct, U (i + 1) / nct); owner(u) is the CTA of unit u.
+// Units of a request's (request, kv head)s: `ends`, then two per chunk.
+__device__ __forceinline__ int units_of(const Span& s, int ends) { return s.c0 == s.c1 ? 0 : ends + 2 * (s.c1 - s.c0); }
+// CTA i of nct takes units [U i / nct, U (i + 1) / nct), nct at most U / 2; a chunk belongs to the CTA of its
+// first unit, which is owner(u).
 __device__ __forceinline__ long long split_at(long long U, int nct, int i) { return U * i / nct; }
 __device__ __forceinline__ int owner(long long U, int nct, long long u) {
   return (int)(((u + 1) * nct + U - 1) / U) - 1;
 }
 
+// Chunks [c0, c1) of (m, gg), whose request attends to [lo, n): the piece of CTA blockIdx.x of those that CTAs
+// a .. b leave in slots 2 a + second, 2 (a + 1), .., 2 b.  a == b: the whole of it.  m < 0: no more items.
+struct __align__(16) Item {
+  int m, gg, c0, c1, lo, n, a, b, second, pad[3];
+};
+// Bits of chunk c's 16-position groups with a position that counts: within [lo, n) and loaded.
+__device__ __forceinline__ uint32_t group_bits(const Item& it, int c, uint32_t loaded) {
+  const int a0 = max(0, it.lo - c * kP), a1 = min(kP, it.n - c * kP);
+  return loaded & ((1u << ((a1 + 15) >> 4)) - 1) & ~((1u << (a0 >> 4)) - 1);
+}
 // A role's bounded waits: one that runs out sets the error word, and the role goes on without
 // waiting, so that every barrier is still met and the kernel ends.
 struct Waits {
@@ -216,23 +214,25 @@ struct Waits {
   }
 };
 
-// grid: one CTA per SM.  HPT: heads per softmax thread, 2 HPT >= n_q / n_kv.
-template <int HD, bool FP8, int HPT>
-__global__ void __launch_bounds__(kThreads, 1)
+// grid: one CTA per SM.  Softmax teams of NG groups of 4 warps; a group's threads hold HPT heads, NG HPT >= n_q / n_kv.
+template <int HD, bool FP8, int HPT, int NG>
+__global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ PagedAttnArgs a) {
   using C = PCfg<HD, FP8>;
-  extern __shared__ __align__(1024) uint8_t sm_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = ring + C::kRing;                     // [2][QTILE]
-  uint8_t* sP = sQ + 2 * C::QTILE;                  // [2][TERMS][PTILE]
+  constexpr int kTeam = NG * 128, kSoftWarps = 2 * NG * 4, kThreads = 2 * kTeam + 128, kWarps = kThreads / 32;
+  constexpr int kProducer = kSoftWarps, kScores = kProducer + 1, kItems = kProducer + 2, kPV = kProducer + 3;
+  extern __shared__ __align__(1024) uint8_t ring[];  // the swizzles' atoms; static shared memory is padded to it
+  uint8_t* sQ = ring + C::kRing;           // [2][QTILE]
+  uint8_t* sP = sQ + 2 * C::QTILE;         // [2][TERMS][PTILE], one per team
+  __shared__ Item s_item[4];
   __shared__ __align__(8) uint64_t kv_full[2][C::NS], kv_empty[2][C::NS], q_full[2], q_empty[2], s_full[2], s_empty[2],
-      p_full[2], p_empty[2], o_full[2], o_empty[2];
-  __shared__ long long s_part[kThreads / 32], s_off;
-  __shared__ float s_max[8][HPT], s_sum[8][HPT], q_pow[4][kN];
+      p_full[2], p_empty[2], o_full[2], o_empty[2], x_full[2], x_empty[2], i_full[4], i_empty[4];
+  __shared__ long long s_part[kWarps], s_base;  // s_base: units before request s_m, which holds the CTA's first one
+  __shared__ float s_max[kSoftWarps][HPT], s_sum[kSoftWarps][HPT], s_x[2][NG][2][HPT], q_pow[FP8 ? 4 : 1][kN];
   __shared__ uint32_t loaded[kMasks];                // 16-position groups of a chunk that were loaded, by bit
   __shared__ uint32_t s_tmem;
-  __shared__ int s_m, s_last[2];
+  __shared__ int s_last[2], s_m;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   auto B = [](const uint64_t& b) { return tc::smem_u32(&b); };
   if (tid == 0) {
@@ -244,22 +244,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(B(q_full[i]), 1);
       tc::mbar_init(B(q_empty[i]), 1);
       tc::mbar_init(B(s_full[i]), 2);  // the MMAs' commit, and the issuing thread's own arrival
-      tc::mbar_init(B(s_empty[i]), kSoft / 32);
-      tc::mbar_init(B(p_full[i]), kSoft / 32);
+      tc::mbar_init(B(s_empty[i]), 4 * NG);
+      tc::mbar_init(B(p_full[i]), 4 * NG);
       tc::mbar_init(B(p_empty[i]), 1);
       tc::mbar_init(B(o_full[i]), 1);
-      tc::mbar_init(B(o_empty[i]), kSoft / 32);
+      tc::mbar_init(B(o_empty[i]), 4 * NG);
+      tc::mbar_init(B(x_full[i]), NG);
+      tc::mbar_init(B(x_empty[i]), 4 * NG);
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(B(i_full[i]), 1);
+      tc::mbar_init(B(i_empty[i]), kSoftWarps + 3);
     }
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
-  for (int i = tid; i < 2 * C::TERMS * C::PTILE / 16; i += kThreads)  // P of heads that no thread holds stays 0
-    reinterpret_cast<uint4*>(sP)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
+  if (warp == kScores) tc::tmem_alloc(tc::smem_u32(&s_tmem), C::kCols);
   tc::griddep_launch_dependents();
   tc::griddep_wait();
   const int G = a.n_q / a.n_kv, nkvs = a.n_kv / a.t;
+
+  // The units: a sum over the requests, a contiguous run of them per thread.
+  const int per = (a.M + kThreads - 1) / kThreads, r0 = min(a.M, tid * per), r1 = min(a.M, r0 + per);
+  long long here = 0;
+  for (int m = r0; m < r1; ++m) here += (long long)units_of(span_of(a, m), C::kEnds) * a.n_kv;
+  long long base = here;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(kFull, base, o);
+    if (lane >= o) base += u;
+  }
+  if (lane == 31) s_part[warp] = base;
+  base -= here;
+  __syncthreads();
+  long long U = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) base += s_part[w];
+    U += s_part[w];
+  }
+  const int nct = (int)min((long long)gridDim.x, U / 2);
+  const long long u0 = nct == 0 ? 0 : split_at(U, nct, min((int)blockIdx.x, nct)),
+                  u1 = nct == 0 ? 0 : split_at(U, nct, min((int)blockIdx.x + 1, nct));
+  if (u0 < u1 && u0 >= base && u0 < base + here) {  // this thread's requests hold unit u0
+    int m = r0;
+    for (;; ++m) {
+      const long long n = (long long)units_of(span_of(a, m), C::kEnds) * a.n_kv;
+      if (u0 < base + n) break;
+      base += n;
+    }
+    s_m = m;
+    s_base = base;
+  }
 
   // rows without positions
   for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
@@ -270,505 +307,593 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.lse)
       for (int i = tid; i < a.n_q; i += kThreads) a.lse[(size_t)m * a.n_q + i] = -INFINITY;
   }
-
-  // the units: a sum over the requests, a contiguous run of them per thread
-  const int per = (a.M + kThreads - 1) / kThreads, r0 = min(a.M, tid * per), r1 = min(a.M, r0 + per);
-  long long here = 0;
-  for (int m = r0; m < r1; ++m) {
-    const Span s = span_of(a, m);
-    here += s.c1 - s.c0;
-  }
-  long long incl = here;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += u;
-  }
-  if (lane == 31) s_part[warp] = incl;
-  __syncthreads();
-  long long U = 0, before = incl - here;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_part[w];
-    U += s_part[w];
-  }
-  U *= a.n_kv;
-  const int nct = (int)min((long long)gridDim.x, U);
-  if ((int)blockIdx.x >= nct) return;
-  const long long u0 = split_at(U, nct, blockIdx.x), u1 = split_at(U, nct, blockIdx.x + 1);
-  if (u0 >= before * a.n_kv && u0 < (before + here) * a.n_kv) {  // this thread's requests hold unit u0
-    int m = r0;
-    long long off = u0 - before * a.n_kv;
-    for (;; ++m) {
-      const Span s = span_of(a, m);
-      const long long n = (long long)(s.c1 - s.c0) * a.n_kv;
-      if (off < n) break;
-      off -= n;
-    }
-    s_m = m;
-    s_off = off;
-  }
-  if (warp == 9) tc::tmem_alloc(tc::smem_u32(&s_tmem), C::kCols);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
   auto S_at = [&](int k, int term) { return tmem + ((k & 1) * C::QTERMS + term) * kN; };
-  auto O_at = [&](int seg, int nb, int term) {
-    return tmem + (2 * C::QTERMS + ((seg & 1) * C::NB + nb) * C::TERMS + term) * kN;
+  auto O_at = [&](int j, int team, int nb, int term) {
+    return tmem + (2 * C::QTERMS + (((j & 1) * 2 + team) * C::NB + nb) * C::TERMS + term) * kN;
   };
-  const int nu = (int)(u1 - u0);
-  Cursor cu;
-  cu.m = s_m;
-  cu.seg = 0;
-  cu.s = span_of(a, cu.m);
-  cu.gg = (int)(s_off / (cu.s.c1 - cu.s.c0));
-  cu.c = cu.s.c0 + (int)(s_off % (cu.s.c1 - cu.s.c0));
-
-  // pieces of a split (request, kv head): only this CTA's first or last can be one
-  int np_mine = 0, pm[2], pgg[2], pa[2], pb[2];
-  bool pst[2];  // the first of its CTAs starts with it
-  float* part = reinterpret_cast<float*>(a.ws + kPagedMaxCtas);
-  const int per_piece = (G * (HD + 2) + 3) / 4 * 4;
-
   constexpr uint32_t kLay = C::INB == 128 ? 2 : 4;  // swizzle of the cache's stages
   auto mma = [](uint32_t d, uint64_t x, uint64_t y, uint32_t id, bool acc) {
     if (FP8) tc::mma_e4m3(d, x, y, id, acc);
     else tc::mma_bf16(d, x, y, id, acc);
   };
+  // Item j as a role sees it: j counts the CTA's items, k its chunks (over all items) from here on.
+  auto next_item = [&](Waits& wait, int j, bool whole_warp) {
+    wait(B(i_full[j & 3]), (j >> 2) & 1);
+    const Item it = s_item[j & 3];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) tc::mbar_arrive(B(i_empty[j & 3]));
+    if (wait.failed) {  // nothing to go by: end
+      Item none = it;
+      none.m = -1;
+      return none;
+    }
+    return it;
+  };
 
-  if (warp == 8) {
-    // ---- producer: k of chunk c in stage 2 c, v in 2 c + 1 (modulo NS).  The barriers go by (k or v, chunk
-    // modulo NS), not by stage: each is then waited for phase by phase by one role (with an odd NS a
-    // stage holds k and v in turn, and the role that reads k would miss every other phase).
+  if (warp == kProducer) {
+    // ---- k of chunk c in stage 2 c, v in 2 c + 1 (modulo NS).  The barriers go by (k or v, chunk modulo NS), not
+    // by stage: each is then waited for phase by phase by one role (with an odd NS a stage holds k and v in
+    // turn, and the role that reads k would miss every other phase).
     Waits wait{a.err, 44u, false};
     const int box_rows = min(1 << a.page_shift, kP), nbp = kP / box_rows;  // boxes along the positions
     const int box = lane % nbp, side = lane / nbp;
     const uint64_t pol = tc::l2_evict_first();  // the cache streams through once
-    auto page_of = [&](const Cursor& x) {  // the page id of this lane's box, -1: nothing to load
-      const int p = x.c * kP + box * box_rows;
-      if (side >= C::NIB || p >= x.s.n || p + box_rows <= x.s.lo) return -1;
-      return a.table[(size_t)x.m * a.table_stride + (p >> a.page_shift)];
+    auto page_of = [&](const Item& it, int c) {  // the page id of this lane's box, -1: nothing to load
+      const int p = c * kP + box * box_rows;
+      return side < C::NIB && p < it.n && p + box_rows > it.lo
+                 ? a.table[(size_t)it.m * a.table_stride + (p >> a.page_shift)]
+                 : -1;
     };
-    int id = page_of(cu);
-    for (int k = 0; k < nu; ++k) {
-      Cursor nx = cu;
-      if (k + 1 < nu) advance(a, nx);
-      const int next_id = k + 1 < nu ? page_of(nx) : -1;  // in flight while the stages are waited for
-      const bool load = id >= 0 && id < a.n_pages;
-      const unsigned boxes = __ballot_sync(kFull, load);
-      const unsigned groups = __ballot_sync(kFull, lane < 8 && (boxes >> ((lane & 7) * 16 / box_rows) & 1));
-      const int p = cu.c * kP + box * box_rows;
-      const int row = ((((cu.gg / nkvs) * a.n_pages + id) * nkvs + cu.gg % nkvs) << a.page_shift) +
-                      (p & ((1 << a.page_shift) - 1));
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int i = 2 * k + kv, st = i % C::NS;
-        const int was = (i - C::NS) >> 1;  // the chunk whose k or v was in this stage
-        if (i >= C::NS) wait(B(kv_empty[(i - C::NS) & 1][was % C::NS]), (was / C::NS) & 1);
-        __syncwarp();
-        if (lane == 0) {
-          if (kv == 0) loaded[k % kMasks] = groups;
-          tc::mbar_arrive_expect_tx(B(kv_full[kv][k % C::NS]), __popc(boxes) * box_rows * C::INB);
+    int k = 0;
+    Item it = next_item(wait, 0, true);
+    int id = it.m < 0 ? -1 : page_of(it, it.c0);
+    for (int j = 0; it.m >= 0; ++j) {
+      const int base = (it.gg / nkvs) * a.n_pages, g = it.gg % nkvs;
+      Item nx;
+      for (int c = it.c0; c < it.c1; ++c, ++k) {
+        int next_id = -1;  // in flight while the stages are waited for
+        if (c + 1 < it.c1) {
+          next_id = page_of(it, c + 1);
+        } else {
+          nx = next_item(wait, j + 1, true);
+          if (nx.m >= 0) next_id = page_of(nx, nx.c0);
         }
-        __syncwarp();
-        if (load)
-          tc::tma_load_2d_hint(tc::smem_u32(ring + (size_t)st * C::STAGE) + (side * kP + box * box_rows) * C::INB,
-                               kv ? &tmV : &tmK, side * (C::INB / (FP8 ? 1 : 2)), row, B(kv_full[kv][k % C::NS]), pol);
+        const bool load = id >= 0 && id < a.n_pages;
+        const unsigned boxes = __ballot_sync(kFull, load);
+        const unsigned groups = __ballot_sync(kFull, lane < 8 && (boxes >> ((lane & 7) * 16 / box_rows) & 1));
+        const int row = (((base + id) * nkvs + g) << a.page_shift) +
+                        ((c * kP + box * box_rows) & ((1 << a.page_shift) - 1));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int i = 2 * k + kv, st = i % C::NS;
+          const int was = (i - C::NS) >> 1;  // the chunk whose k or v was in this stage
+          if (i >= C::NS) wait(B(kv_empty[(i - C::NS) & 1][was % C::NS]), (was / C::NS) & 1);
+          __syncwarp();
+          if (lane == 0) {
+            if (kv == 0) loaded[k % kMasks] = groups;
+            tc::mbar_arrive_expect_tx(B(kv_full[kv][k % C::NS]), __popc(boxes) * box_rows * C::INB);
+          }
+          __syncwarp();
+          if (load)
+            tc::tma_load_2d_hint(tc::smem_u32(ring + (size_t)st * C::STAGE) + (side * kP + box * box_rows) * C::INB,
+                                 kv ? &tmV : &tmK, side * (C::INB / (FP8 ? 1 : 2)), row, B(kv_full[kv][k % C::NS]), pol);
+        }
+        id = next_id;
       }
-      cu = nx;
-      id = next_id;
+      it = nx;
     }
-  } else if (warp == 9) {
+  } else if (warp == kScores) {
     // ---- scores: one thread issues
     if (lane == 0) {
       Waits wait{a.err, 45u, false};
       const uint32_t idesc = FP8 ? tc::idesc_e4m3(128, kN * C::QTERMS) : tc::idesc_bf16(128, kN * C::QTERMS);
-      for (int k = 0; k < nu; ++k) {
-        const int st = 2 * k % C::NS, qb = cu.seg & 1;
-        wait(B(q_full[qb]), (cu.seg >> 1) & 1);
-        wait(B(kv_full[0][k % C::NS]), (k / C::NS) & 1);
-        if (k >= 2) wait(B(s_empty[k & 1]), ((k >> 1) - 1) & 1);
-        tc::tc_fence_after();
-        const uint32_t kA = tc::smem_u32(ring + (size_t)st * C::STAGE);
-        const uint32_t qA = tc::smem_u32(sQ + (size_t)qb * C::QTILE);
+      int k = 0;
+      for (int j = 0;; ++j) {
+        const Item it = next_item(wait, j, false);
+        if (it.m < 0) break;
+        wait(B(q_full[j & 1]), (j >> 1) & 1);
+        const uint32_t qA = tc::smem_u32(sQ + (size_t)(j & 1) * C::QTILE);
+        for (int c = it.c0; c < it.c1; ++c, ++k) {
+          wait(B(kv_full[0][k % C::NS]), (k / C::NS) & 1);
+          if (k >= 2) wait(B(s_empty[k & 1]), ((k >> 1) - 1) & 1);
+          tc::tc_fence_after();
+          const uint32_t kA = tc::smem_u32(ring + (size_t)(2 * k % C::NS) * C::STAGE);
 #pragma unroll
-        for (int i = 0; i < C::ROWB / 32; ++i) {  // 32 bytes of a row per MMA
-          const uint32_t ka = kA + (32 * i) / C::INB * (kP * C::INB) + (32 * i) % C::INB;
-          const uint32_t qa = qA + i / 4 * C::QBOX + (i % 4) * 32;
-          mma(S_at(k, 0), smem_desc(ka, 16, 8 * C::INB, kLay), smem_desc(qa, 16, 1024, 2), idesc, i > 0);
+          for (int i = 0; i < C::ROWB / 32; ++i) {  // 32 bytes of a row per MMA
+            const uint32_t ka = kA + (32 * i) / C::INB * (kP * C::INB) + (32 * i) % C::INB;
+            const uint32_t qa = qA + i / 4 * C::QBOX + (i % 4) * 32;
+            mma(S_at(k, 0), smem_desc(ka, 16, 8 * C::INB, kLay), smem_desc(qa, 16, 1024, 2), idesc, i > 0);
+          }
+          tc::mma_commit(B(kv_empty[0][k % C::NS]));
+          tc::mma_commit(B(s_full[k & 1]));
+          tc::mbar_arrive(B(s_full[k & 1]));  // releases what this thread has seen: the chunk's mask, q's powers
         }
-        tc::mma_commit(B(kv_empty[0][k % C::NS]));
-        tc::mma_commit(B(s_full[k & 1]));
-        tc::mbar_arrive(B(s_full[k & 1]));  // releases what this thread has seen: the chunk's mask
-        if (k + 1 == nu || cu.ends()) tc::mma_commit(B(q_empty[qb]));
-        if (k + 1 < nu) advance(a, cu);
+        tc::mma_commit(B(q_empty[j & 1]));
       }
     }
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (warp == kPV) {
     // ---- P V: one thread issues
     if (lane == 0) {
       Waits wait{a.err, 48u, false};
       const uint32_t idesc =
           (FP8 ? tc::idesc_e4m3(128, kN * C::TERMS) : tc::idesc_bf16(128, kN * C::TERMS)) | kTransposed;
-      bool live = false;  // O of the (request, kv head) holds something
-      for (int k = 0; k < nu; ++k) {
-        const int st = (2 * k + 1) % C::NS, ob = cu.seg & 1;
-        if (k == 0 || cu.c == cu.s.c0) {
-          if (cu.seg >= 2) wait(B(o_empty[ob]), ((cu.seg >> 1) - 1) & 1);
-          live = false;
-        }
-        wait(B(p_full[k & 1]), (k >> 1) & 1);
-        wait(B(kv_full[1][k % C::NS]), (k / C::NS) & 1);
-        tc::tc_fence_after();
-        const uint32_t groups = group_bits(cu, loaded[k % kMasks]);
-        const uint32_t vA = tc::smem_u32(ring + (size_t)st * C::STAGE);
-        const uint32_t pA = tc::smem_u32(sP + (size_t)(k & 1) * C::TERMS * C::PTILE);
+      int k = 0;
+      for (int j = 0;; ++j) {
+        const Item it = next_item(wait, j, false);
+        if (it.m < 0) break;
+        if (j >= 2) wait(B(o_empty[j & 1]), ((j >> 1) - 1) & 1);
+        uint32_t live = 0;  // by team: its O holds something
+        for (int c = it.c0; c < it.c1; ++c, ++k) {
+          wait(B(p_full[k & 1]), (k >> 1) & 1);
+          wait(B(kv_full[1][k % C::NS]), (k / C::NS) & 1);
+          tc::tc_fence_after();
+          const uint32_t groups = group_bits(it, c, loaded[k % kMasks]);
+          const uint32_t vA = tc::smem_u32(ring + (size_t)((2 * k + 1) % C::NS) * C::STAGE);
+          const uint32_t pA = tc::smem_u32(sP + (size_t)(k & 1) * C::TERMS * C::PTILE);
 #pragma unroll
-        for (int i = 0; i < kP / C::KS; ++i) {
-          if (!(groups >> (i * C::KS / 16) & (FP8 ? 3u : 1u))) continue;
-          // P's codes are tiles one after another: the blocks of its columns
-          const uint32_t pt = pA + i * C::KS * C::PROW;
-          const uint64_t pd = FP8 ? smem_desc(pt, 128, C::PTILE, 0) : smem_desc(pt, C::PTILE, 256, 6);
+          for (int i = 0; i < kP / C::KS; ++i) {
+            if (!(groups >> (i * C::KS / 16) & (FP8 ? 3u : 1u))) continue;
+            // P's codes are tiles one after another: the blocks of its columns
+            const uint32_t pt = pA + i * C::KS * C::PROW;
+            const uint64_t pd = FP8 ? smem_desc(pt, 128, C::PTILE, 0) : smem_desc(pt, C::PTILE, 256, 6);
 #pragma unroll
-          for (int nb = 0; nb < C::NB; ++nb) {
-            // a head of 64 dims fills half of the 128 rows: the other half reads it again (lead 0)
-            const uint32_t va = vA + nb * (128 * (FP8 ? 1 : 2) / C::INB) * (kP * C::INB) + i * C::KS * C::INB;
-            mma(O_at(cu.seg, nb, 0), smem_desc(va, HD == 64 ? 0 : kP * C::INB, 8 * C::INB, kLay), pd, idesc, live);
+            for (int nb = 0; nb < C::NB; ++nb) {
+              // a head of 64 dims fills half of the 128 rows: the other half reads it again (lead 0)
+              const uint32_t va = vA + nb * (128 * (FP8 ? 1 : 2) / C::INB) * (kP * C::INB) + i * C::KS * C::INB;
+              mma(O_at(j, k & 1, nb, 0), smem_desc(va, HD == 64 ? 0 : kP * C::INB, 8 * C::INB, kLay), pd, idesc,
+                  live >> (k & 1) & 1);
+            }
+            live |= 1u << (k & 1);
           }
-          live = true;
+          tc::mma_commit(B(kv_empty[1][k % C::NS]));
+          tc::mma_commit(B(p_empty[k & 1]));
         }
-        tc::mma_commit(B(kv_empty[1][k % C::NS]));
-        tc::mma_commit(B(p_empty[k & 1]));
-        if (k + 1 == nu || cu.ends()) tc::mma_commit(B(o_full[ob]));
-        if (k + 1 < nu) advance(a, cu);
+        tc::mma_commit(B(o_full[j & 1]));
       }
     }
     __syncwarp();
-  } else if (warp == 10) {
-    // ---- q of each (request, kv head): G heads as 16 rows of 128-byte-swizzled pieces
+  } else if (warp == kItems) {
+    // ---- items, and the q of each: G heads as 16 rows of 128-byte-swizzled pieces
     Waits wait{a.err, 46u, false};
     constexpr int RP = HD / 8;       // 16-byte pieces of a row: 8, 16 or 32 neighbouring lanes
     constexpr int QV = 16 * RP / 32;
-    for (int k = 0; k < nu; ++k) {
-      if (k == 0 || cu.c == cu.s.c0) {
-        const __nv_bfloat16* qp = a.q + ((size_t)cu.m * a.n_q + (size_t)cu.gg * G) * HD;
-        uint4 qn[QV];
-#pragma unroll
-        for (int i = 0; i < QV; ++i) {
-          const int idx = lane + 32 * i, r = idx / RP, c8 = idx % RP;
-          qn[i] = r < G ? *reinterpret_cast<const uint4*>(qp + (size_t)r * HD + 8 * c8) : make_uint4(0, 0, 0, 0);
+    int m = u0 < u1 ? s_m : 0, gg = 0;
+    Span s = u0 < u1 ? span_of(a, m) : Span{0, 0, 0, 0};
+    long long at = u0 < u1 ? s_base : 0;  // the first unit of (m, gg)
+    int j = 0;
+    if (u0 < u1) {  // the head that holds u0
+      const int n = units_of(s, C::kEnds);
+      gg = (int)((u0 - at) / n);
+      at += (long long)gg * n;
+    }
+    for (;;) {
+      Item it{};
+      it.m = -1;
+      while (at < u1 && !wait.failed) {
+        const int n = units_of(s, C::kEnds), ch = s.c1 - s.c0;
+        if (n > 0) {
+          // chunk i begins at unit at + kEnds + 2 i
+          auto chunks_before = [&](long long u) {
+            return (int)min((long long)ch, max(0ll, (u - at - C::kEnds + 1) >> 1));
+          };
+          it.c0 = chunks_before(u0);
+          it.c1 = chunks_before(u1);
         }
-        const int qb = cu.seg & 1;
-        if (cu.seg >= 2) wait(B(q_empty[qb]), ((cu.seg >> 1) - 1) & 1);
-        uint8_t* dst = sQ + (size_t)qb * C::QTILE;
-#pragma unroll
-        for (int i = 0; i < QV; ++i) {
-          const int idx = lane + 32 * i, r = idx / RP, c8 = idx % RP;
-          if (FP8) {  // q / 2^e below 256, as two codes
-            const uint32_t w[4] = {qn[i].x, qn[i].y, qn[i].z, qn[i].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max((w[j] >> 7) & 0xffu, (w[j] >> 23) & 0xffu));
-#pragma unroll
-            for (int o = 1; o < RP; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-            // exponent field of the largest value, less 7 for 2^7 <= q / 2^e < 2^8; both factors stay normal
-            const int e = min(max((int)top, 8), 253) - 7;
-            const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float x = bf16_lo(w[j]) * inv, y = bf16_hi(w[j]) * inv;
-              const uint32_t h = e4m3x2(x, y);
-              const float2 b = e4m3x2_value(h);
-              hi[j >> 1] |= h << (16 * (j & 1));
-              lo[j >> 1] |= e4m3x2(x - b.x, y - b.y) << (16 * (j & 1));
-            }
-            uint8_t* at = dst + c8 / 16 * C::QBOX + r * 128 + (((c8 / 2 % 8) ^ (r & 7)) << 4) + (c8 & 1) * 8;
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(at + kN * 128) = make_uint2(lo[0], lo[1]);
-            if (c8 == 0) q_pow[cu.seg & 3][r] = __uint_as_float((uint32_t)e << 23);
-          } else {
-            *reinterpret_cast<uint4*>(dst + c8 / 8 * C::QBOX + r * 128 + (((c8 % 8) ^ (r & 7)) << 4)) = qn[i];
-          }
+        if (n > 0 && it.c0 < it.c1) {
+          it.m = m;
+          it.gg = gg;
+          const bool split = it.c0 > 0 || it.c1 < ch;
+          it.a = split ? owner(U, nct, at + C::kEnds) : 0;
+          it.b = split ? owner(U, nct, at + C::kEnds + 2 * (ch - 1)) : 0;
+          // whether it is the second item of CTA a, whose run then begins before it
+          it.second = split && split_at(U, nct, it.a) < at;
+          it.c0 += s.c0;
+          it.c1 += s.c0;
+          it.lo = s.lo;
+          it.n = s.n;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(B(q_full[qb]));
+        at += n;
+        if (++gg >= a.n_kv || n == 0) {
+          gg = 0;
+          if (++m >= a.M) at = u1;
+          else s = span_of(a, m);
+        }
+        if (it.m >= 0) break;
       }
-      if (k + 1 < nu) advance(a, cu);
+      if (j >= 4) wait(B(i_empty[j & 3]), ((j >> 2) - 1) & 1);
+      if (lane == 0) {
+        s_item[j & 3] = it;
+        tc::mbar_arrive(B(i_full[j & 3]));
+      }
+      if (it.m < 0) break;
+      const __nv_bfloat16* qp = a.q + ((size_t)it.m * a.n_q + (size_t)it.gg * G) * HD;
+      uint4 qn[QV];
+#pragma unroll
+      for (int i = 0; i < QV; ++i) {
+        const int idx = lane + 32 * i, r = idx / RP, c8 = idx % RP;
+        qn[i] = r < G ? *reinterpret_cast<const uint4*>(qp + (size_t)r * HD + 8 * c8) : make_uint4(0, 0, 0, 0);
+      }
+      if (j >= 2) wait(B(q_empty[j & 1]), ((j >> 1) - 1) & 1);
+      uint8_t* dst = sQ + (size_t)(j & 1) * C::QTILE;
+#pragma unroll
+      for (int i = 0; i < QV; ++i) {
+        const int idx = lane + 32 * i, r = idx / RP, c8 = idx % RP;
+        if (FP8) {  // q / 2^e below 256, as two codes
+          const uint32_t w[4] = {qn[i].x, qn[i].y, qn[i].z, qn[i].w};
+          uint32_t top = 0;
+#pragma unroll
+          for (int j2 = 0; j2 < 4; ++j2) top = max(top, max((w[j2] >> 7) & 0xffu, (w[j2] >> 23) & 0xffu));
+#pragma unroll
+          for (int o = 1; o < RP; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+          // exponent field of the largest value, less 7 for 2^7 <= q / 2^e < 2^8; both factors stay normal
+          const int e = min(max((int)top, 8), 253) - 7;
+          const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+          for (int j2 = 0; j2 < 4; ++j2) {
+            const float v = bf16_lo(w[j2]) * inv, y = bf16_hi(w[j2]) * inv;
+            const uint32_t h = e4m3x2(v, y);
+            const float2 b = e4m3x2_value(h);
+            hi[j2 >> 1] |= h << (16 * (j2 & 1));
+            lo[j2 >> 1] |= e4m3x2(v - b.x, y - b.y) << (16 * (j2 & 1));
+          }
+          uint8_t* at = dst + c8 / 16 * C::QBOX + r * 128 + (((c8 / 2 % 8) ^ (r & 7)) << 4) + (c8 & 1) * 8;
+          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(at + kN * 128) = make_uint2(lo[0], lo[1]);
+          if (c8 == 0) q_pow[j & 3][r] = __uint_as_float((uint32_t)e << 23);
+        } else {
+          *reinterpret_cast<uint4*>(dst + c8 / 8 * C::QBOX + r * 128 + (((c8 % 8) ^ (r & 7)) << 4)) = qn[i];
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(B(q_full[j & 1]));
+      ++j;
     }
   } else {
-    // ---- softmax: thread = position 32 (warp % 4) + lane and heads [h0, h0 + HPT); for O, dim and heads
+    // ---- softmax: thread = position 32 (warp % 4) + lane and heads [h0, h0 + HPT); for O, dim and heads.
+    // Team k % 2 takes chunk k.
     Waits wait{a.err, 47u, false};
-    const int quad = warp & 3, half = warp >> 2, h0 = half * HPT, row = 32 * quad + lane, bid = 1 + half;
+    const int team = warp / (4 * NG), grp = warp / 4 % NG, quad = warp & 3, h0 = grp * HPT, row = 32 * quad + lane;
+    const int bid = 1 + team * NG + grp, tt = tid - team * kTeam;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    float ref[HPT], l[HPT], sc[HPT];
-    int c_seg = cu.c;      // first chunk of the current piece
-    bool first_seg = true, fresh = true, live = false;  // fresh: at the piece's first chunk; live: O holds something
-    for (int k = 0; k < nu; ++k) {
-      wait(B(s_full[k & 1]), (k >> 1) & 1);
-      tc::tc_fence_after();
-      float s[HPT];
-      tmem_ld<HPT>(S_at(k, 0) + h0 + lanes, s);
-      if (C::QTERMS == 2) {
-        float lo[HPT];
-        tmem_ld<HPT>(S_at(k, 1) + h0 + lanes, lo);
-        landed(lo);
-        landed(s);
-#pragma unroll
-        for (int h = 0; h < HPT; ++h) s[h] += lo[h];
-      } else {
-        landed(s);
-      }
-      tc::tc_fence_before();
-      if (fresh) {
-#pragma unroll
-        for (int h = 0; h < HPT; ++h) {
-          sc[h] = a.scale * kLog2e;
-          if (FP8) sc[h] *= (a.k_scale ? a.k_scale[cu.gg] : 1.0f) * q_pow[cu.seg & 3][h0 + h];
-          ref[h] = -INFINITY;
-          l[h] = 0.f;
-        }
-        fresh = live = false;
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(B(s_empty[k & 1]));
-      const uint32_t groups = group_bits(cu, loaded[k % kMasks]);
-      const int p = cu.c * kP + row;
-      const bool counts = p >= cu.s.lo && p < cu.s.n && (groups >> (row >> 4) & 1);
-      bool above = false;
+    float* pieces = reinterpret_cast<float*>(a.ws + kWsHead);
+    const int per_piece = (G * (HD + 2) + 3) / 4 * 4;
+    int k0 = 0;  // chunks before the item
+    for (int j = 0;; ++j) {
+      const Item it = next_item(wait, j, true);
+      // a team ends together: a thread whose wait has run out would leave the others at a barrier
+      if (bar_any(5 + team, kTeam, it.m < 0)) break;
+      const int nch = it.c1 - it.c0;
+      float ref[HPT], l[HPT], sc[HPT];
 #pragma unroll
       for (int h = 0; h < HPT; ++h) {
-        s[h] = counts ? s[h] * sc[h] : -INFINITY;
-        above |= s[h] > ref[h] + C::kStep;
+        ref[h] = -INFINITY;
+        l[h] = 0.f;
+        sc[h] = a.scale * kLog2e * (FP8 && a.k_scale ? a.k_scale[it.gg] : 1.0f);
       }
-      if (bar_any(bid, kSoft / 2, above)) {  // a new reference: the maximum so far
-#pragma unroll
-        for (int h = 0; h < HPT; ++h) {
-          float x = s[h];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-          if (lane == 0) s_max[warp][h] = x;
-        }
-        bar_sync(bid, kSoft / 2);
-        float f[HPT];
-#pragma unroll
-        for (int h = 0; h < HPT; ++h) {
-          float x = ref[h];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) x = fmaxf(x, s_max[4 * half + w][h]);
-          f[h] = weight(ref[h], x);
-          l[h] *= f[h];
-          ref[h] = x;
-        }
-        if (live) {  // once the P V before has ended
-          wait(B(p_empty[(k - 1) & 1]), ((k - 1) >> 1) & 1);
-          tc::tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < C::NB * C::TERMS; ++i) {
-            const uint32_t at = O_at(cu.seg, i / C::TERMS, i % C::TERMS) + h0 + lanes;
-            float o[HPT];
-            tmem_ld<HPT>(at, o);
-            landed(o);
-#pragma unroll
-            for (int h = 0; h < HPT; ++h) o[h] *= f[h];
-            tmem_st<HPT>(at, o);
-          }
-          tc::tc_fence_before();
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < HPT; ++h) {  // a head without a score yet has reference -inf and weights 0
-        s[h] = ex2(s[h] - (ref[h] == -INFINITY ? 0.f : ref[h]));
-        l[h] += s[h];
-      }
-      if (k >= 2) wait(B(p_empty[k & 1]), ((k >> 1) - 1) & 1);
-      uint8_t* pt = sP + (size_t)(k & 1) * C::TERMS * C::PTILE;
-      if (FP8) {
-        float r[HPT];
-#pragma unroll
-        for (int h = 0; h < HPT; ++h) r[h] = s[h] * C::kPMul;
-#pragma unroll
-        for (int t = 0; t < C::TERMS; ++t) {
-          uint32_t w[HPT / 4];
-#pragma unroll
-          for (int i = 0; i < HPT / 4; ++i) {
-            const uint32_t c0 = e4m3x2(r[4 * i], r[4 * i + 1]), c1 = e4m3x2(r[4 * i + 2], r[4 * i + 3]);
-            w[i] = c0 | c1 << 16;
-            if (t + 1 < C::TERMS) {
-              const float2 x = e4m3x2_value(c0), y = e4m3x2_value(c1);
-              r[4 * i] = (r[4 * i] - x.x) * C::kNext;
-              r[4 * i + 1] = (r[4 * i + 1] - x.y) * C::kNext;
-              r[4 * i + 2] = (r[4 * i + 2] - y.x) * C::kNext;
-              r[4 * i + 3] = (r[4 * i + 3] - y.y) * C::kNext;
-            }
-          }
-          uint8_t* at = pt + t * C::PTILE + row * 16 + h0;
-          if constexpr (HPT == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-          else *reinterpret_cast<uint32_t*>(at) = w[0];
-        }
-      } else {
-        uint32_t hi[HPT / 2], lo[HPT / 2];
-#pragma unroll
-        for (int i = 0; i < HPT / 2; ++i) {
-          const float x = s[2 * i], y = s[2 * i + 1];
-          hi[i] = pack_bf16(x, y);
-          lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
-        }
-        // 32-byte rows, the two 16-byte pieces swapped in every other group of four rows
-        uint8_t* at = pt + row * 32 + (((h0 >> 3) ^ ((row >> 2) & 1)) << 4) + (h0 & 7) * 2;
-        if constexpr (HPT == 8) {
-          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(at + C::PTILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        } else {
-          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(at + C::PTILE) = make_uint2(lo[0], lo[1]);
-        }
-      }
-      // v rows that do not count may hold anything (NaN too): where their MMA step runs, P V must see 0
-      const bool step_runs = groups >> (row / C::KS * C::KS / 16) & (FP8 ? 3u : 1u);
-      if (__any_sync(kFull, step_runs && !counts)) {
-        const int st = (2 * k + 1) % C::NS;
-        wait(B(kv_full[1][k % C::NS]), (k / C::NS) & 1);
-        if (step_runs && !counts) {
-          constexpr int PB = C::INB / 16, NPC = C::ROWB / 16;  // a row's pieces stay within it under any swizzle
-          uint8_t* v = ring + (size_t)st * C::STAGE + row * C::INB;
-#pragma unroll
-          for (int j = 0; j < NPC / 2; ++j) {
-            const int q = half * (NPC / 2) + j;
-            *reinterpret_cast<uint4*>(v + q / PB * (kP * C::INB) + (q % PB) * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-      }
-      live |= groups != 0;
-      fence_proxy_async_smem();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(B(p_full[k & 1]));
-
-      const bool last = k + 1 == nu, end = last || cu.ends();
-      if (end) {  // the piece of (m, gg) in this CTA ends
-#pragma unroll
-        for (int h = 0; h < HPT; ++h) {
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(kFull, l[h], o);
-          if (lane == 0) s_sum[warp][h] = l[h];
-        }
-        bar_sync(bid, kSoft / 2);
-#pragma unroll
-        for (int h = 0; h < HPT; ++h)
-          l[h] = (s_sum[4 * half][h] + s_sum[4 * half + 1][h]) + (s_sum[4 * half + 2][h] + s_sum[4 * half + 3][h]);
-        const bool whole = c_seg == cu.s.c0 && cu.ends();
-        const size_t orow = (size_t)cu.m * a.n_q + (size_t)cu.gg * G;  // of o and lse
-        float* piece = part + (size_t)(2 * blockIdx.x + (first_seg ? 0 : 1)) * per_piece;
-        const float vs = (FP8 && a.v_scale ? a.v_scale[cu.gg] : 1.0f) / C::kPMul;
-        wait(B(o_full[cu.seg & 1]), (cu.seg >> 1) & 1);
+      bool live = false;  // O holds something
+      const int first = (k0 ^ team) & 1;
+      for (int i = first; i < nch; i += 2) {
+        const int k = k0 + i, c = it.c0 + i;
+        wait(B(s_full[team]), (k >> 1) & 1);
         tc::tc_fence_after();
-        float o[C::NB][HPT], ot[C::NB][C::TERMS][HPT];
+        float s[HPT];
+        tmem_ld<HPT>(S_at(k, 0) + h0 + lanes, s);
+        if (C::QTERMS == 2) {
+          float lo[HPT];
+          tmem_ld<HPT>(S_at(k, 1) + h0 + lanes, lo);
+          landed(lo);
+          landed(s);
 #pragma unroll
-        for (int i = 0; i < C::NB * C::TERMS; ++i)
-          tmem_ld<HPT>(O_at(cu.seg, i / C::TERMS, i % C::TERMS) + h0 + lanes, ot[i / C::TERMS][i % C::TERMS]);
+          for (int h = 0; h < HPT; ++h) s[h] += lo[h];
+        } else {
+          landed(s);
+        }
+        tc::tc_fence_before();
+        if (FP8 && i == first) {
 #pragma unroll
-        for (int i = 0; i < C::NB * C::TERMS; ++i) landed(ot[i / C::TERMS][i % C::TERMS]);
+          for (int h = 0; h < HPT; ++h) sc[h] *= q_pow[j & 3][h0 + h];
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(B(s_empty[team]));
+        const uint32_t groups = group_bits(it, c, loaded[k % kMasks]);
+        const int p = c * kP + row;
+        const bool counts = p >= it.lo && p < it.n && (groups >> (row >> 4) & 1);
+        bool above = false;
 #pragma unroll
-        for (int nb = 0; nb < C::NB; ++nb)
+        for (int h = 0; h < HPT; ++h) {
+          s[h] = counts ? s[h] * sc[h] : -INFINITY;
+          above |= s[h] > ref[h] + C::kStep;
+        }
+        const bool raise = bar_any(bid, 128, above);
+        if (k >= 2) wait(B(p_empty[team]), ((k >> 1) - 1) & 1);  // the team's P V before has ended
+        if (raise) {  // a new reference: the maximum so far
 #pragma unroll
           for (int h = 0; h < HPT; ++h) {
-            o[nb][h] = ot[nb][C::TERMS - 1][h];
+            float v = s[h];
 #pragma unroll
-            for (int t = C::TERMS - 2; t >= 0; --t) o[nb][h] = ot[nb][t][h] + o[nb][h] * (1.f / C::kNext);
+            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+            if (lane == 0) s_max[warp][h] = v;
           }
+          bar_sync(bid, 128);
+          float f[HPT];
+#pragma unroll
+          for (int h = 0; h < HPT; ++h) {
+            float v = ref[h];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) v = fmaxf(v, s_max[(warp & ~3) + w][h]);
+            f[h] = weight(ref[h], v);
+            l[h] *= f[h];
+            ref[h] = v;
+          }
+          if (live) {
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < C::NB * C::TERMS; ++q) {
+              const uint32_t at = O_at(j, team, q / C::TERMS, q % C::TERMS) + h0 + lanes;
+              float o[HPT];
+              tmem_ld<HPT>(at, o);
+              landed(o);
+#pragma unroll
+              for (int h = 0; h < HPT; ++h) o[h] *= f[h];
+              tmem_st<HPT>(at, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < HPT; ++h) {  // a head without a score yet has reference -inf and weights 0
+          s[h] = ex2(s[h] - (ref[h] == -INFINITY ? 0.f : ref[h]));
+          l[h] += s[h];
+        }
+        uint8_t* pt = sP + (size_t)team * C::TERMS * C::PTILE;
+        if (FP8) {
+          float r[HPT];
+#pragma unroll
+          for (int h = 0; h < HPT; ++h) r[h] = s[h] * C::kPMul;
+#pragma unroll
+          for (int t = 0; t < C::TERMS; ++t) {
+            uint32_t w[HPT / 4];
+#pragma unroll
+            for (int q = 0; q < HPT / 4; ++q) {
+              const uint32_t c0 = e4m3x2(r[4 * q], r[4 * q + 1]), c1 = e4m3x2(r[4 * q + 2], r[4 * q + 3]);
+              w[q] = c0 | c1 << 16;
+              if (t + 1 < C::TERMS) {
+                const float2 u = e4m3x2_value(c0), y = e4m3x2_value(c1);
+                r[4 * q] = (r[4 * q] - u.x) * C::kNext;
+                r[4 * q + 1] = (r[4 * q + 1] - u.y) * C::kNext;
+                r[4 * q + 2] = (r[4 * q + 2] - y.x) * C::kNext;
+                r[4 * q + 3] = (r[4 * q + 3] - y.y) * C::kNext;
+              }
+            }
+            uint8_t* at = pt + t * C::PTILE + row * 16 + h0;
+            if constexpr (HPT == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(at) = w[0];
+          }
+        } else {
+          uint32_t hi[HPT / 2], lo[HPT / 2];
+#pragma unroll
+          for (int q = 0; q < HPT / 2; ++q) {
+            const float u = s[2 * q], y = s[2 * q + 1];
+            hi[q] = pack_bf16(u, y);
+            lo[q] = pack_bf16(u - bf16_lo(hi[q]), y - bf16_hi(hi[q]));
+          }
+          // 32-byte rows, the two 16-byte pieces swapped in every other group of four rows
+          uint8_t* at = pt + row * 32 + (((h0 >> 3) ^ ((row >> 2) & 1)) << 4) + (h0 & 7) * 2;
+          if constexpr (HPT == 8) {
+            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + C::PTILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + C::PTILE) = make_uint2(lo[0], lo[1]);
+          }
+        }
+        // v rows that do not count may hold anything (NaN too): where their MMA step runs, P V must see 0
+        const bool step_runs = groups >> (row / C::KS * C::KS / 16) & (FP8 ? 3u : 1u);
+        if (__any_sync(kFull, step_runs && !counts)) {
+          wait(B(kv_full[1][k % C::NS]), (k / C::NS) & 1);
+          if (step_runs && !counts) {
+            constexpr int PB = C::INB / 16, NPC = C::ROWB / 16;  // a row's pieces stay within it under any swizzle
+            uint8_t* v = ring + (size_t)((2 * k + 1) % C::NS) * C::STAGE + row * C::INB;
+#pragma unroll
+            for (int q = grp; q < NPC; q += NG)
+              *reinterpret_cast<uint4*>(v + q / PB * (kP * C::INB) + (q % PB) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        live |= groups != 0;
+        fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(B(o_empty[cu.seg & 1]));
+        if (lane == 0) tc::mbar_arrive(B(p_full[team]));
+      }
+
+      // The item's end: the sums over the positions; the team of the first chunk brings the two together.
+#pragma unroll
+      for (int h = 0; h < HPT; ++h) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(kFull, l[h], o);
+        if (lane == 0) s_sum[warp][h] = l[h];
+      }
+      bar_sync(bid, 128);
+#pragma unroll
+      for (int h = 0; h < HPT; ++h) {
+        const float(*q)[HPT] = &s_sum[warp & ~3];
+        l[h] = (q[0][h] + q[1][h]) + (q[2][h] + q[3][h]);
+      }
+      k0 += nch;
+      if (first != 0) {
+        if (quad == 0 && lane == 0) {  // only who writes waits: another could come when the next phase has ended too
+          if (j >= 2) wait(B(x_empty[j & 1]), ((j >> 1) - 1) & 1);
+#pragma unroll
+          for (int h = 0; h < HPT; ++h) {
+            s_x[j & 1][grp][0][h] = ref[h];
+            s_x[j & 1][grp][1][h] = l[h];
+          }
+          tc::mbar_arrive(B(x_full[j & 1]));
+        }
+        __syncwarp();
+        continue;
+      }
+      wait(B(x_full[j & 1]), (j >> 1) & 1);
+      float f0[HPT], f1[HPT];
+#pragma unroll
+      for (int h = 0; h < HPT; ++h) {
+        const float xr = s_x[j & 1][grp][0][h], xl = s_x[j & 1][grp][1][h], v = fmaxf(ref[h], xr);
+        // a sum of 0: nothing counted, and its O may hold anything
+        f0[h] = l[h] == 0.f ? 0.f : weight(ref[h], v);
+        f1[h] = xl == 0.f ? 0.f : weight(xr, v);
+        l[h] = l[h] * f0[h] + xl * f1[h];
+        ref[h] = v;
+      }
+      wait(B(o_full[j & 1]), (j >> 1) & 1);
+      tc::tc_fence_after();
+      const bool whole = it.a == it.b;
+      auto slot_of = [&](int cta) { return 2 * cta + (cta == it.a ? it.second : 0); };
+      const size_t orow = (size_t)it.m * a.n_q + (size_t)it.gg * G;  // of o and lse
+      const float vs = (FP8 && a.v_scale ? a.v_scale[it.gg] : 1.0f) / C::kPMul;
+      float* piece = pieces + (size_t)slot_of(blockIdx.x) * per_piece;
+#pragma unroll 1
+      for (int nb = 0; nb < C::NB; ++nb) {
+        float ot[2][C::TERMS][HPT];
+#pragma unroll
+        for (int q = 0; q < 2 * C::TERMS; ++q)
+          tmem_ld<HPT>(O_at(j, team ^ (q / C::TERMS), nb, q % C::TERMS) + h0 + lanes, ot[q / C::TERMS][q % C::TERMS]);
+#pragma unroll
+        for (int q = 0; q < 2 * C::TERMS; ++q) landed(ot[q / C::TERMS][q % C::TERMS]);
+#pragma unroll
+        for (int h = 0; h < HPT; ++h) {
+          float v[2];
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            v[w] = ot[w][C::TERMS - 1][h];
+#pragma unroll
+            for (int t = C::TERMS - 2; t >= 0; --t) v[w] = ot[w][t][h] + v[w] * (1.f / C::kNext);
+          }
+          const float r = !whole ? vs : l[h] == 0.f ? 0.f : vs / l[h];
+          const float o = ((f0[h] == 0.f ? 0.f : v[0] * f0[h]) + (f1[h] == 0.f ? 0.f : v[1] * f1[h])) * r;
+          if (h0 + h < G && row < HD) {
+            const size_t at = (size_t)(h0 + h) * HD + 128 * nb + row;
+            if (whole) a.o[orow * HD + at] = __float2bfloat16_rn(o);
+            else piece[at] = o;
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(B(o_empty[j & 1]));
+        tc::mbar_arrive(B(x_empty[j & 1]));
+      }
+      if (row == 0) {
 #pragma unroll
         for (int h = 0; h < HPT; ++h) {
           if (h0 + h >= G) break;
-          // a sum of 0: nothing counted, and O may hold anything
-          const float r = l[h] == 0.f ? 0.f : whole ? vs / l[h] : vs;
-#pragma unroll
-          for (int nb = 0; nb < C::NB; ++nb) {
-            if (row >= HD) break;
-            const size_t at = (size_t)(h0 + h) * HD + 128 * nb + row;
-            const float v = l[h] == 0.f ? 0.f : o[nb][h] * r;
-            if (whole) a.o[orow * HD + at] = __float2bfloat16_rn(v);
-            else piece[at] = v;
-          }
-          if (row == 0) {
-            if (!whole) {
-              piece[G * HD + h0 + h] = ref[h];
-              piece[G * HD + G + h0 + h] = l[h];
-            } else if (a.lse) {
-              a.lse[orow + h0 + h] = (ref[h] + log2f(l[h])) * kLn2;  // -inf + log2(0) where nothing counts
-            }
+          if (!whole) {
+            piece[G * HD + h0 + h] = ref[h];
+            piece[G * HD + G + h0 + h] = l[h];
+          } else if (a.lse) {
+            a.lse[orow + h0 + h] = (ref[h] + log2f(l[h])) * kLn2;  // -inf + log2(0) where nothing counts
           }
         }
-        if (!whole) {
-          const long long ub = u0 + k - (cu.c - cu.s.c0);  // the unit of chunk c0 of (m, gg)
-          const int i = np_mine++ & 1;
-          pm[i] = cu.m;
-          pgg[i] = cu.gg;
-          pa[i] = owner(U, nct, ub);
-          pst[i] = split_at(U, nct, pa[i]) == ub;
-          pb[i] = owner(U, nct, ub + (cu.s.c1 - cu.s.c0) - 1);
-        }
-        first_seg = false;
-        fresh = true;
       }
-      if (!last) advance(a, cu);
-      if (end) c_seg = cu.c;
-    }
+      if (whole) continue;
 
-    // Split (request, kv head)s: count this CTA's pieces in; the CTA that brings the last one joins
-    // them all, in order, and leaves the counter at zero.
-    if (np_mine > 0) {
-      __threadfence();
-      bar_sync(3, kSoft);
-      if (tid == 0) {
-        for (int i = 0; i < np_mine; ++i) {
-          const bool is_last = atomicAdd(a.ws + pa[i], 1u) == (unsigned)(pb[i] - pa[i]);
-          if (is_last) a.ws[pa[i]] = 0u;
-          s_last[i] = is_last;
+      // A piece: count it in among kFan neighbours; who is last joins those pieces in order and counts in
+      // among the joined ones, whose last gives the result.  The counters are left at zero.
+      auto last_of = [&](unsigned* counter, int n) {  // whole team: its writes are seen by who is last
+        bar_sync(5 + team, kTeam);
+        if (tt == 0) {
+          __threadfence();
+          const bool is_last = atomicAdd(counter, 1u) + 1 == (unsigned)n;
+          if (is_last) *counter = 0u;
+          __threadfence();
+          s_last[team] = is_last;
         }
-        __threadfence();
-      }
-      bar_sync(3, kSoft);
-      for (int i = 0; i < np_mine; ++i) {
-        if (!s_last[i]) continue;
-        const size_t orow = (size_t)pm[i] * a.n_q + (size_t)pgg[i] * G;
-        // CTA j's piece is its first one (slot 2 j), but that of the CTA the (request, kv head) starts
-        // in only if that CTA's run starts with it
-        auto piece_of = [&](int j) { return part + (size_t)(2 * j + (j == pa[i] && !pst[i] ? 1 : 0)) * per_piece; };
-        for (int e = 4 * tid; e < G * HD; e += 4 * kSoft) {
-          const int hi = e / HD;
-          float Mx = -INFINITY, Lx = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int j = pa[i]; j <= pb[i]; ++j) Mx = fmaxf(Mx, __ldcg(piece_of(j) + G * HD + hi));
-#pragma unroll 8
-          for (int j = pa[i]; j <= pb[i]; ++j) {
-            const float* pc = piece_of(j);
-            const float f = weight(__ldcg(pc + G * HD + hi), Mx);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(pc + e));
-            Lx += __ldcg(pc + G * HD + G + hi) * f;
-            v.x += x.x * f;
-            v.y += x.y * f;
-            v.z += x.z * f;
-            v.w += x.w * f;
+        bar_sync(5 + team, kTeam);
+        return s_last[team] != 0;
+      };
+      // the pieces of CTAs first, first + step, ..: n of them, in order
+      auto join = [&](int e, int cta0, int step, int n, float& M, float& L, float4& v) {
+        const int hi = e / HD;
+        M = -INFINITY;
+        L = 0.f;
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = 0; b < n; b += kFan) {
+          float pm[kFan], pl[kFan];
+          float4 pv[kFan];
+          float Mb = M;
+#pragma unroll
+          for (int q = 0; q < kFan; ++q) {
+            const float* pc = pieces + (size_t)slot_of(cta0 + min(b + q, n - 1) * step) * per_piece;
+            pm[q] = __ldcg(pc + G * HD + hi);
+            pl[q] = __ldcg(pc + G * HD + G + hi);
+            pv[q] = __ldcg(reinterpret_cast<const float4*>(pc + e));
           }
-          const float r = Lx == 0.f ? 0.f : 1.0f / Lx;
-          *reinterpret_cast<uint2*>(a.o + orow * HD + e) =
-              make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
-          if (a.lse && e % HD == 0) a.lse[orow + hi] = (Mx + log2f(Lx)) * kLn2;
+#pragma unroll
+          for (int q = 0; q < kFan; ++q)
+            if (b + q < n) Mb = fmaxf(Mb, pm[q]);
+          const float g = weight(M, Mb);
+          L *= g;
+          v = make_float4(v.x * g, v.y * g, v.z * g, v.w * g);
+#pragma unroll
+          for (int q = 0; q < kFan; ++q) {
+            if (b + q >= n) break;
+            const float f = weight(pm[q], Mb);
+            L += pl[q] == 0.f ? 0.f : pl[q] * f;
+            v.x += pv[q].x * f;
+            v.y += pv[q].y * f;
+            v.z += pv[q].z * f;
+            v.w += pv[q].w * f;
+          }
+          M = Mb;
         }
+      };
+      const int all = it.b - it.a + 1, fan0 = it.a + ((int)blockIdx.x - it.a) / kFan * kFan;
+      const int nfan = min(kFan, it.b + 1 - fan0), nfans = (all + kFan - 1) / kFan;
+      if (!last_of(a.ws + slot_of(fan0), nfan)) continue;
+      constexpr int EV = (16 * HD / 4 + kTeam - 1) / kTeam;  // vectors of four values per thread
+      if (nfans > 1) {
+        float M[EV], L[EV];
+        float4 v[EV];
+#pragma unroll
+        for (int q = 0; q < EV; ++q) {
+          const int e = 4 * (tt + q * kTeam);
+          if (e < G * HD) join(e, fan0, 1, nfan, M[q], L[q], v[q]);
+        }
+        bar_sync(5 + team, kTeam);  // every piece is read before the first one's place is written
+        float* dst = pieces + (size_t)slot_of(fan0) * per_piece;
+#pragma unroll
+        for (int q = 0; q < EV; ++q) {
+          const int e = 4 * (tt + q * kTeam);
+          if (e >= G * HD) break;
+          *reinterpret_cast<float4*>(dst + e) = v[q];
+          if (e % HD == 0) {
+            dst[G * HD + e / HD] = M[q];
+            dst[G * HD + G + e / HD] = L[q];
+          }
+        }
+        if (!last_of(a.ws + kSlots + slot_of(it.a), nfans)) continue;
+      }
+      for (int e = 4 * tt; e < G * HD; e += 4 * kTeam) {
+        float M, L;
+        float4 v;
+        if (nfans > 1) join(e, it.a, kFan, nfans, M, L, v);
+        else join(e, it.a, 1, nfan, M, L, v);
+        const float r = L == 0.f ? 0.f : 1.0f / L;
+        *reinterpret_cast<uint2*>(a.o + orow * HD + e) =
+            make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
+        if (a.lse && e % HD == 0) a.lse[orow + e / HD] = (M + log2f(L)) * kLn2;
       }
     }
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kScores) {
     tc::tc_fence_after();
     tc::tmem_relinquish();
     tc::tmem_dealloc(tmem, C::kCols);
@@ -789,7 +914,7 @@ int sm_count() {  // of the current device, asked for once
   return n;
 }
 
-template <int HD, bool FP8, int HPT>
+template <int HD, bool FP8, int HPT, int NG>
 cudaError_t launch(const PagedAttnArgs& a, const void* k_pages, const void* v_pages, cudaStream_t st) {
   using C = PCfg<HD, FP8>;
   EncodeTiled enc = encode_fn();
@@ -806,11 +931,11 @@ cudaError_t launch(const PagedAttnArgs& a, const void* k_pages, const void* v_pa
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  auto kernel = paged_attn_kernel<HD, FP8, HPT>;
+  auto kernel = paged_attn_kernel<HD, FP8, HPT, NG>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
   const int grid = std::min(sm_count(), kPagedMaxCtas);
-  e = launch_dependent(kernel, dim3(grid), dim3(kThreads), C::SMEM, st, tm[0], tm[1], a);
+  e = launch_dependent(kernel, dim3(grid), dim3(2 * NG * 128 + 128), C::SMEM, st, tm[0], tm[1], a);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -818,17 +943,23 @@ cudaError_t launch(const PagedAttnArgs& a, const void* k_pages, const void* v_pa
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int G, int hd) {
-  return (kPagedMaxCtas + 2 * kPagedMaxCtas * piece_floats(G, hd)) * 4;
+  return (kWsHead + kSlots * piece_floats(G, hd)) * 4;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,
                               cudaStream_t st) {
   auto go = [&](auto fp8) {
     constexpr bool F = decltype(fp8)::value;
-    const bool few = a.n_q / a.n_kv <= 8;  // heads per kv head: 4 or 8 per softmax thread
-    if (hd == 64) return few ? launch<64, F, 4>(a, k_pages, v_pages, st) : launch<64, F, 8>(a, k_pages, v_pages, st);
-    if (hd == 128) return few ? launch<128, F, 4>(a, k_pages, v_pages, st) : launch<128, F, 8>(a, k_pages, v_pages, st);
-    return few ? launch<256, F, 4>(a, k_pages, v_pages, st) : launch<256, F, 8>(a, k_pages, v_pages, st);
+    auto sized = [&](auto hd_) {
+      constexpr int D = decltype(hd_)::value;
+      const int G = a.n_q / a.n_kv;  // heads of a kv head: 4 or 8 per softmax thread, in one or two groups
+      return G <= 4   ? launch<D, F, 4, 1>(a, k_pages, v_pages, st)
+             : G <= 8 ? launch<D, F, 4, 2>(a, k_pages, v_pages, st)
+                      : launch<D, F, 8, 2>(a, k_pages, v_pages, st);
+    };
+    if (hd == 64) return sized(std::integral_constant<int, 64>{});
+    if (hd == 128) return sized(std::integral_constant<int, 128>{});
+    return sized(std::integral_constant<int, 256>{});
   };
   return kv_dtype == TP_BF16 ? go(std::false_type{}) : go(std::true_type{});
 }

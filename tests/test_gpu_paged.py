@@ -390,7 +390,7 @@ class Case:
                 assert_within(got_l[m][fine], rl[fine], ps[fine] + 2.0 ** -21 * (1 + np.abs(rl[fine])), "lse")
             if not fine.any():
                 assert not got[m].any()
-        assert not self.ws[:1024].any()                                # the counters are left at zero
+        assert not self.ws[:4 * 1024].any()                            # the counters are left at zero
         return o, lse
 
 
