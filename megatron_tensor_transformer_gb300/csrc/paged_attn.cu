@@ -56,6 +56,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNoRef = -1e38f;           // a reference that any score is a step above
 constexpr int kP = 128;                    // positions per chunk: the rows of an MMA
 constexpr int kN = 16;                     // heads of an MMA (its columns)
 constexpr int kMasks = 32;                 // ring of the chunks' masks: above the chunks in flight
@@ -69,7 +70,6 @@ struct PCfg {
   static constexpr int INB = ROWB < 128 ? ROWB : 128;             // bytes of a box row
   static constexpr int NIB = ROWB / INB;                          // boxes side by side
   static constexpr int STAGE = kP * ROWB;                         // k or v of a chunk
-  static constexpr int NS = std::min(16, (192 * 1024) / STAGE);   // stages, k and v in turn
   static constexpr int NB = HD == 256 ? 2 : 1;                    // 128-dim blocks of O^T
   static constexpr int KS = FP8 ? 32 : 16;                        // k of an MMA
   static constexpr int TERMS = FP8 ? 3 : 2;                       // codes that P is split into
@@ -78,8 +78,9 @@ struct PCfg {
   static constexpr int QTERMS = FP8 ? 2 : 1;                      // codes of q, 16 rows each
   static constexpr int QBOX = QTERMS * kN * 128;                  // their rows' 128 bytes
   static constexpr int QTILE = (ROWB + 127) / 128 * QBOX;
+  static constexpr int NS = std::min(16, 192 * 1024 / STAGE);     // stages, k and v in turn
   static constexpr float kStep = FP8 ? 1.f : 8.f;                 // ref may be behind the maximum by this
-  static constexpr float kPMul = FP8 ? 128.f : 1.f;               // P is held times this: up to 256 in e4m3
+  static constexpr float kPLog = FP8 ? 7.f : 0.f;                 // weights are held times 2^this: up to 256 in e4m3
   static constexpr float kNext = FP8 ? 16.f : 1.f;                // each code of P after the first is held times this
   static constexpr int kUsed = 2 * kN * (QTERMS + 2 * NB * TERMS);  // TMEM: S [2][QTERMS][16], O [2][team][NB][TERMS][16]
   static constexpr uint32_t kCols = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
@@ -163,10 +164,10 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool p) {
 __device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
-  return __half22float2(__half2(h));
+__device__ __forceinline__ __half2 e4m3x2_half2(uint32_t v) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3));
 }
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t v) { return __half22float2(e4m3x2_half2(v)); }
 
 // The positions [lo, n) a request attends to, in chunks [c0, c1); c0 == c1 if there are none.
 struct Span {
@@ -342,31 +343,39 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     const int box_rows = min(1 << a.page_shift, kP), nbp = kP / box_rows;  // boxes along the positions
     const int box = lane % nbp, side = lane / nbp;
     const uint64_t pol = tc::l2_evict_first();  // the cache streams through once
-    auto page_of = [&](const Item& it, int c) {  // the page id of this lane's box, -1: nothing to load
-      const int p = c * kP + box * box_rows;
-      return side < C::NIB && p < it.n && p + box_rows > it.lo
-                 ? a.table[(size_t)it.m * a.table_stride + (p >> a.page_shift)]
-                 : -1;
+    // Page ids come 32 at a time, one per lane, the next 32 on their way (one chunk's at a time, a look-up
+    // took as long as a chunk of 32 KB).
+    auto first_page = [&](const Item& it) { return it.c0 * kP >> a.page_shift; };
+    auto ids_from = [&](const Item& it, int page) {  // the page id of page + lane, -1: not attended to
+      page += lane;
+      const long long p = (long long)page << a.page_shift;
+      return p < it.n && p + (1 << a.page_shift) > it.lo ? a.table[(size_t)it.m * a.table_stride + page] : -1;
     };
     int k = 0;
-    Item it = next_item(wait, 0, true);
-    int id = it.m < 0 ? -1 : page_of(it, it.c0);
+    Item it = next_item(wait, 0, true), nx = it;
+    int at = 0, ids = -1, ids_next = -1, ids_item = -1;  // lanes' ids from page `at` on; the 32 after; the next item's
+    if (it.m >= 0) {
+      at = first_page(it);
+      ids = ids_from(it, at);
+    }
     for (int j = 0; it.m >= 0; ++j) {
+      ids_next = ids_from(it, at + 32);
+      nx = next_item(wait, j + 1, true);
+      if (nx.m >= 0) ids_item = ids_from(nx, first_page(nx));
       const int base = (it.gg / nkvs) * a.n_pages, g = it.gg % nkvs;
-      Item nx;
       for (int c = it.c0; c < it.c1; ++c, ++k) {
-        int next_id = -1;  // in flight while the stages are waited for
-        if (c + 1 < it.c1) {
-          next_id = page_of(it, c + 1);
-        } else {
-          nx = next_item(wait, j + 1, true);
-          if (nx.m >= 0) next_id = page_of(nx, nx.c0);
+        const int pos = c * kP + box * box_rows, page = pos >> a.page_shift;
+        if (((c * kP + kP - 1) >> a.page_shift) >= at + 32) {  // a chunk's pages never straddle two batches
+          at += 32;
+          ids = ids_next;
+          ids_next = ids_from(it, at + 32);
         }
+        int id = __shfl_sync(kFull, ids, page - at);
+        if (side >= C::NIB || pos >= it.n || pos + box_rows <= it.lo) id = -1;
         const bool load = id >= 0 && id < a.n_pages;
         const unsigned boxes = __ballot_sync(kFull, load);
         const unsigned groups = __ballot_sync(kFull, lane < 8 && (boxes >> ((lane & 7) * 16 / box_rows) & 1));
-        const int row = (((base + id) * nkvs + g) << a.page_shift) +
-                        ((c * kP + box * box_rows) & ((1 << a.page_shift) - 1));
+        const int row = (((base + id) * nkvs + g) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int i = 2 * k + kv, st = i % C::NS;
@@ -382,9 +391,10 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
             tc::tma_load_2d_hint(tc::smem_u32(ring + (size_t)st * C::STAGE) + (side * kP + box * box_rows) * C::INB,
                                  kv ? &tmV : &tmK, side * (C::INB / (FP8 ? 1 : 2)), row, B(kv_full[kv][k % C::NS]), pol);
         }
-        id = next_id;
       }
       it = nx;
+      at = first_page(it);
+      ids = ids_item;
     }
   } else if (warp == kScores) {
     // ---- scores: one thread issues
@@ -570,13 +580,15 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       // a team ends together: a thread whose wait has run out would leave the others at a barrier
       if (bar_any(5 + team, kTeam, it.m < 0)) break;
       const int nch = it.c1 - it.c0;
-      float ref[HPT], l[HPT], sc[HPT];
+      // A weight is 2^(s sc - sub): sub = ref - kPLog, or kNoRef while there is no reference.
+      float sub[HPT], l[HPT], sc[HPT];
 #pragma unroll
       for (int h = 0; h < HPT; ++h) {
-        ref[h] = -INFINITY;
+        sub[h] = kNoRef;
         l[h] = 0.f;
         sc[h] = a.scale * kLog2e * (FP8 && a.k_scale ? a.k_scale[it.gg] : 1.0f);
       }
+      const float vs = FP8 && a.v_scale ? a.v_scale[it.gg] : 1.0f;
       bool live = false;  // O holds something
       const int first = (k0 ^ team) & 1;
       for (int i = first; i < nch; i += 2) {
@@ -605,18 +617,18 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         const uint32_t groups = group_bits(it, c, loaded[k % kMasks]);
         const int p = c * kP + row;
         const bool counts = p >= it.lo && p < it.n && (groups >> (row >> 4) & 1);
-        bool above = false;
+        float x[HPT], top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HPT; ++h) {
-          s[h] = counts ? s[h] * sc[h] : -INFINITY;
-          above |= s[h] > ref[h] + C::kStep;
+          x[h] = counts ? s[h] * sc[h] - sub[h] : -INFINITY;
+          top = fmaxf(top, x[h]);
         }
-        const bool raise = bar_any(bid, 128, above);
+        const bool raise = bar_any(bid, 128, top > C::kStep + C::kPLog);
         if (k >= 2) wait(B(p_empty[team]), ((k >> 1) - 1) & 1);  // the team's P V before has ended
         if (raise) {  // a new reference: the maximum so far
 #pragma unroll
           for (int h = 0; h < HPT; ++h) {
-            float v = s[h];
+            float v = counts ? s[h] * sc[h] : -INFINITY;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
             if (lane == 0) s_max[warp][h] = v;
@@ -625,12 +637,14 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
           float f[HPT];
 #pragma unroll
           for (int h = 0; h < HPT; ++h) {
-            float v = ref[h];
+            float v = -INFINITY;
 #pragma unroll
             for (int w = 0; w < 4; ++w) v = fmaxf(v, s_max[(warp & ~3) + w][h]);
-            f[h] = weight(ref[h], v);
+            const float to = fmaxf(sub[h], v - C::kPLog);  // kNoRef if there is still no score
+            f[h] = ex2(sub[h] - to);                       // from kNoRef: of a sum that is 0
             l[h] *= f[h];
-            ref[h] = v;
+            sub[h] = to;
+            x[h] = counts ? s[h] * sc[h] - sub[h] : -INFINITY;
           }
           if (live) {
             tc::tc_fence_after();
@@ -647,29 +661,24 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
           }
         }
 #pragma unroll
-        for (int h = 0; h < HPT; ++h) {  // a head without a score yet has reference -inf and weights 0
-          s[h] = ex2(s[h] - (ref[h] == -INFINITY ? 0.f : ref[h]));
+        for (int h = 0; h < HPT; ++h) {
+          s[h] = ex2(x[h]);
           l[h] += s[h];
         }
         uint8_t* pt = sP + (size_t)team * C::TERMS * C::PTILE;
         if (FP8) {
-          float r[HPT];
+          __half2 r[HPT / 2];  // fp16 holds 2^-12 of a weight, or 2^-32 of one that is 1
 #pragma unroll
-          for (int h = 0; h < HPT; ++h) r[h] = s[h] * C::kPMul;
+          for (int q = 0; q < HPT / 2; ++q) r[q] = __floats2half2_rn(s[2 * q], s[2 * q + 1]);
+          const __half2 next = __float2half2_rn(C::kNext);
 #pragma unroll
           for (int t = 0; t < C::TERMS; ++t) {
             uint32_t w[HPT / 4];
 #pragma unroll
-            for (int q = 0; q < HPT / 4; ++q) {
-              const uint32_t c0 = e4m3x2(r[4 * q], r[4 * q + 1]), c1 = e4m3x2(r[4 * q + 2], r[4 * q + 3]);
-              w[q] = c0 | c1 << 16;
-              if (t + 1 < C::TERMS) {
-                const float2 u = e4m3x2_value(c0), y = e4m3x2_value(c1);
-                r[4 * q] = (r[4 * q] - u.x) * C::kNext;
-                r[4 * q + 1] = (r[4 * q + 1] - u.y) * C::kNext;
-                r[4 * q + 2] = (r[4 * q + 2] - y.x) * C::kNext;
-                r[4 * q + 3] = (r[4 * q + 3] - y.y) * C::kNext;
-              }
+            for (int q = 0; q < HPT / 2; ++q) {
+              const uint32_t code = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(r[q]), __NV_SATFINITE, __NV_E4M3);
+              w[q >> 1] = q & 1 ? w[q >> 1] | code << 16 : code;
+              if (t + 1 < C::TERMS) r[q] = __hmul2(__hsub2(r[q], e4m3x2_half2(code)), next);  // exact
             }
             uint8_t* at = pt + t * C::PTILE + row * 16 + h0;
             if constexpr (HPT == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
@@ -731,7 +740,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
           if (j >= 2) wait(B(x_empty[j & 1]), ((j >> 1) - 1) & 1);
 #pragma unroll
           for (int h = 0; h < HPT; ++h) {
-            s_x[j & 1][grp][0][h] = ref[h];
+            s_x[j & 1][grp][0][h] = sub[h];
             s_x[j & 1][grp][1][h] = l[h];
           }
           tc::mbar_arrive(B(x_full[j & 1]));
@@ -743,19 +752,18 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       float f0[HPT], f1[HPT];
 #pragma unroll
       for (int h = 0; h < HPT; ++h) {
-        const float xr = s_x[j & 1][grp][0][h], xl = s_x[j & 1][grp][1][h], v = fmaxf(ref[h], xr);
+        const float xs = s_x[j & 1][grp][0][h], xl = s_x[j & 1][grp][1][h], v = fmaxf(sub[h], xs);
         // a sum of 0: nothing counted, and its O may hold anything
-        f0[h] = l[h] == 0.f ? 0.f : weight(ref[h], v);
-        f1[h] = xl == 0.f ? 0.f : weight(xr, v);
+        f0[h] = l[h] == 0.f ? 0.f : ex2(sub[h] - v);
+        f1[h] = xl == 0.f ? 0.f : ex2(xs - v);
         l[h] = l[h] * f0[h] + xl * f1[h];
-        ref[h] = v;
+        sub[h] = v;
       }
       wait(B(o_full[j & 1]), (j >> 1) & 1);
       tc::tc_fence_after();
       const bool whole = it.a == it.b;
       auto slot_of = [&](int cta) { return 2 * cta + (cta == it.a ? it.second : 0); };
       const size_t orow = (size_t)it.m * a.n_q + (size_t)it.gg * G;  // of o and lse
-      const float vs = (FP8 && a.v_scale ? a.v_scale[it.gg] : 1.0f) / C::kPMul;
       float* piece = pieces + (size_t)slot_of(blockIdx.x) * per_piece;
 #pragma unroll 1
       for (int nb = 0; nb < C::NB; ++nb) {
@@ -774,7 +782,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
 #pragma unroll
             for (int t = C::TERMS - 2; t >= 0; --t) v[w] = ot[w][t][h] + v[w] * (1.f / C::kNext);
           }
-          const float r = !whole ? vs : l[h] == 0.f ? 0.f : vs / l[h];
+          const float r = !whole ? vs : l[h] == 0.f ? 0.f : __fdividef(vs, l[h]);
           const float o = ((f0[h] == 0.f ? 0.f : v[0] * f0[h]) + (f1[h] == 0.f ? 0.f : v[1] * f1[h])) * r;
           if (h0 + h < G && row < HD) {
             const size_t at = (size_t)(h0 + h) * HD + 128 * nb + row;
@@ -794,10 +802,10 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         for (int h = 0; h < HPT; ++h) {
           if (h0 + h >= G) break;
           if (!whole) {
-            piece[G * HD + h0 + h] = ref[h];
+            piece[G * HD + h0 + h] = l[h] == 0.f ? -INFINITY : sub[h];
             piece[G * HD + G + h0 + h] = l[h];
           } else if (a.lse) {
-            a.lse[orow + h0 + h] = (ref[h] + log2f(l[h])) * kLn2;  // -inf + log2(0) where nothing counts
+            a.lse[orow + h0 + h] = l[h] == 0.f ? -INFINITY : (sub[h] + log2f(l[h])) * kLn2;
           }
         }
       }
