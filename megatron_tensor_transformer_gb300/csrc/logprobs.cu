@@ -10,12 +10,12 @@
 // rows there are; they join through distributed shared memory, so there is no workspace and one launch.
 //
 // Top alternatives: (logit, id) as one 64-bit key, the greater the further ahead, so ties go to the
-// lower id.  Each warp keeps its best keys, sorted across its lanes, and inserts new ones one by one, so
-// few must come that far: a value is a candidate only if it reaches the bar, the k-th largest of the 64
-// maxima that the CTA's groups of 8 threads have seen so far (k values reach it, so no smaller one is
-// among the k first).  The bar is taken anew after 1, 2, 4, 8, .. rounds, before the round's own values
-// are looked at; on average it lies near the k-th largest value so far, and about k ln(n / n_0) of a
-// CTA's n values pass it, whatever the number of warps.
+// lower id.  A value is a candidate only if it reaches the bar, the k-th largest of the maxima that 32 or 64 groups
+// of threads have seen so far: k values reach it, so no smaller one is among the k first.  The bar is
+// taken anew after 1, 6 and 32 rounds, before the round's own values are looked at; of random values
+// the 9 largest or so reach it for k = 8, the 31 largest for k = 20.  Each warp keeps its k best candidates, sorted across its
+// lanes, inserting one at a time; at the end those that reach the last bar are ranked against each other,
+// and the CTAs' k best in turn.  (Merging the warps' lists pairwise took longer than reading the row.)
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -75,18 +75,6 @@ __device__ __forceinline__ Part join(const Part& a, const Part& b) {
   return {m, a.S * fa + b.S * fb, (fa > 0.f ? (a.T + a.S * da) * fa : 0.f) + (fb > 0.f ? (b.T + b.S * db) * fb : 0.f)};
 }
 
-// The warp's keys, sorted, the best in lane 0: the 32 best of its own and v's (also sorted).
-__device__ __forceinline__ uint64_t merge_sorted(uint64_t mine, uint64_t v, int lane) {
-  const uint64_t r = __shfl_sync(kFull, v, 31 - lane);
-  uint64_t x = mine > r ? mine : r;  // bitonic, holds the 32 best
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t y = __shfl_xor_sync(kFull, x, o);
-    x = (lane & o) ? (x < y ? x : y) : (x > y ? x : y);
-  }
-  return x;
-}
-
 struct Shared {
   Part part;
   int ahead;
@@ -98,8 +86,10 @@ __global__ void __launch_bounds__(kNT, 2) logprobs_kernel(const LogprobsArgs a) 
   __shared__ Shared sh;
   __shared__ Part s_part[kNW];
   __shared__ int s_ahead[kNW];
-  __shared__ uint64_t s_top[kNW][32];
-  __shared__ float s_max[64], s_bar;  // maxima of groups of 8 threads; the bar
+  __shared__ uint64_t s_key[kNT];
+  __shared__ __align__(16) float s_max[64];  // the groups' maxima
+  __shared__ float s_bar;
+  __shared__ int s_n;
   tc::griddep_launch_dependents();
   tc::griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -132,65 +122,80 @@ __global__ void __launch_bounds__(kNT, 2) logprobs_kernel(const LogprobsArgs a) 
       }
     }
   };
+  // 32 groups of 16 threads for k <= 24, else 64 of 8 (1900 rows, k = 20: 214.7 and 234.5 us; k = 32: 284.5 and 251.9)
+  const bool small = k <= 24;
+  auto ahead_of = [&](float v, int n) {  // how many of the first n maxima are ahead of this thread's, ties by place
+    int r = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; i += 4) {
+      const float4 y4 = *reinterpret_cast<const float4*>(s_max + i);
+      const float y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r += y[j] > v || (y[j] == v && i + j < tid);
+    }
+    return r;
+  };
   auto raise_bar = [&](float seen) {  // whole CTA; seen: the thread's maximum so far
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) seen = fmaxf(seen, __shfl_xor_sync(kFull, seen, o));
-    if ((lane & 7) == 0) s_max[warp * 4 + (lane >> 3)] = seen;
+    if (small) {
+      seen = fmaxf(seen, __shfl_xor_sync(kFull, seen, 8));
+      if ((lane & 15) == 0) s_max[warp * 2 + (lane >> 4)] = seen;
+    } else if ((lane & 7) == 0) {
+      s_max[warp * 4 + (lane >> 3)] = seen;
+    }
     __syncthreads();
-    if (warp == 0) {  // the 32 largest of 64, sorted
-      float lo = s_max[lane], hi = s_max[32 + lane];
-#pragma unroll
-      for (int n = 2; n <= 32; n <<= 1) {
-#pragma unroll
-        for (int o = n >> 1; o > 0; o >>= 1) {
-          const float pl = __shfl_xor_sync(kFull, lo, o), ph = __shfl_xor_sync(kFull, hi, o);
-          const bool desc = (lane & n) == 0 || n == 32, first = (lane & o) == 0;
-          lo = desc == first ? fmaxf(lo, pl) : fminf(lo, pl);
-          hi = desc == first ? fmaxf(hi, ph) : fminf(hi, ph);
-        }
-      }
-      const float rev = __shfl_sync(kFull, hi, 31 - lane);
-      float x32 = fmaxf(lo, rev);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float y = __shfl_xor_sync(kFull, x32, o);
-        x32 = (lane & o) ? fminf(x32, y) : fmaxf(x32, y);
-      }
-      if (lane == k - 1) s_bar = x32;
+    if (warp == 0 || (warp == 1 && !small)) {
+      const float v = s_max[tid];
+      if ((small ? ahead_of(v, 32) : ahead_of(v, 64)) == k - 1) s_bar = v;
     }
     __syncthreads();
     bar = s_bar;
   };
+  // Ranks n keys of s_key, one per thread; the k first go to out, in order.
+  auto rank = [&](int n, uint64_t* out) {
+    if (tid < n) {
+      const uint64_t key = s_key[tid];
+      int r = 0;
+      for (int i = 0; i < n; ++i) r += s_key[i] > key;
+      if (r < k) out[r] = key;
+    }
+  };
   const int rounds = (v1 - v0 + kNT * kVec - 1) / (kNT * kVec);
+  float4 q[kVec];
+  auto load = [&](int r) {  // a vector that is not there holds -inf: no weight
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      const int i = v0 + (r * kVec + u) * kNT + tid;
+      q[u] = i < v1 ? __ldcs(xv + i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+  };
+  load(0);
   for (int r = 0; r < rounds; ++r) {
     const int i0 = v0 + r * kNT * kVec + tid;
     float v[kVec][4];
 #pragma unroll
-    for (int u = 0; u < kVec; ++u) {
-      const int i = i0 + u * kNT;
-      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (i < v1) q = __ldcs(xv + i);
-      v[u][0] = q.x, v[u][1] = q.y, v[u][2] = q.z, v[u][3] = q.w;
-    }
-    float mx[kVec], all = p.m;
+    for (int u = 0; u < kVec; ++u) v[u][0] = q[u].x, v[u][1] = q[u].y, v[u][2] = q[u].z, v[u][3] = q[u].w;
+    if (r + 1 < rounds) load(r + 1);  // in flight while these are summed
+    float mx[kVec], now = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
       mx[u] = fmaxf(fmaxf(v[u][0], v[u][1]), fmaxf(v[u][2], v[u][3]));
-      all = fmaxf(all, mx[u]);
+      now = fmaxf(now, mx[u]);
     }
-    if (all > p.m) {
+    if (now > p.m) {
       if (p.m != -INFINITY) {
-        const float d = p.m - all, f = ex2(d * kLog2e);
+        const float d = p.m - now, f = ex2(d * kLog2e);
         p.T = f > 0.f ? (p.T + p.S * d) * f : 0.f;  // as in join()
         p.S *= f;
       }
-      p.m = all;
+      p.m = now;
     }
     const float base = p.m == -INFINITY ? 0.f : p.m;  // only -inf so far: every weight is 0
 #pragma unroll
     for (int u = 0; u < kVec; ++u) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // a vector that is not there holds -inf: no weight
+      for (int j = 0; j < 4; ++j) {
         const float d = max_nan(v[u][j] - base, -1e4f), e = ex2(d * kLog2e);
         p.S += e;
         p.T += e * d;
@@ -202,13 +207,17 @@ __global__ void __launch_bounds__(kNT, 2) logprobs_kernel(const LogprobsArgs a) 
       }
     }
     if (k > 0) {
-      if ((r & (r + 1)) == 0) raise_bar(p.m);
+      if (r == 0 || r == 5 || r == 31) raise_bar(p.m);
+      if (__any_sync(kFull, now >= bar)) {
 #pragma unroll
-      for (int u = 0; u < kVec; ++u) {
-        const bool there = i0 + u * kNT < v1;
-        if (__any_sync(kFull, there && mx[u] >= bar)) {
+        for (int u = 0; u < kVec; ++u) {
+          const bool there = i0 + u * kNT < v1;
+          if (!__any_sync(kFull, there && mx[u] >= bar)) continue;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) insert(v[u][j], lead + 4 * (i0 + u * kNT) + j, there && v[u][j] >= bar);
+          for (int j = 0; j < 4; ++j) {
+            const bool in = there && v[u][j] >= bar;
+            if (__any_sync(kFull, in)) insert(v[u][j], lead + 4 * (i0 + u * kNT) + j, in);
+          }
         }
       }
     }
@@ -225,57 +234,66 @@ __global__ void __launch_bounds__(kNT, 2) logprobs_kernel(const LogprobsArgs a) 
   }
 
   // the warp's, the CTA's, the cluster's
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Part q{__shfl_xor_sync(kFull, p.m, o), __shfl_xor_sync(kFull, p.S, o), __shfl_xor_sync(kFull, p.T, o)};
-    p = join(p, q);
-    ahead += __shfl_xor_sync(kFull, ahead, o);
-  }
+  auto join_lanes = [&](int n) {
+    for (int o = n / 2; o > 0; o >>= 1) {
+      const Part q{__shfl_xor_sync(kFull, p.m, o), __shfl_xor_sync(kFull, p.S, o), __shfl_xor_sync(kFull, p.T, o)};
+      p = join(p, q);
+      ahead += __shfl_xor_sync(kFull, ahead, o);
+    }
+  };
+  join_lanes(32);
   if (lane == 0) {
     s_part[warp] = p;
     s_ahead[warp] = ahead;
   }
-  s_top[warp][lane] = top;
+  if (tid == 0) s_n = 0;
+  if (tid < 32) sh.top[tid] = 0;
   __syncthreads();
   if (k > 0) {
-#pragma unroll
-    for (int o = kNW / 2; o > 0; o >>= 1) {
-      if (warp < o) {
-        top = merge_sorted(top, s_top[warp + o][lane], lane);
-        s_top[warp][lane] = top;
-      }
-      __syncthreads();
-    }
+    const bool in = lane < k && top != 0 && key_logit(top) >= bar;
+    const unsigned who = __ballot_sync(kFull, in);
+    int at = lane == 0 && who ? atomicAdd(&s_n, __popc(who)) : 0;
+    at = __shfl_sync(kFull, at, 0) + __popc(who & ((1u << lane) - 1));
+    if (in) s_key[at] = top;
+    __syncthreads();
+    rank(s_n, sh.top);
+    __syncthreads();
   }
   if (warp == 0) {
-    p = Part{-INFINITY, 0.f, 0.f};
-    ahead = 0;
-    for (int w = 0; w < kNW; ++w) {
-      p = join(p, s_part[w]);
-      ahead += s_ahead[w];
-    }
-    if (C > 1) {
-      if (lane == 0) {
-        sh.part = p;
-        sh.ahead = ahead;
-      }
-      sh.top[lane] = top;
+    p = s_part[lane % kNW];
+    ahead = s_ahead[lane % kNW];
+    join_lanes(kNW);
+    if (lane == 0) {
+      sh.part = p;
+      sh.ahead = ahead;
     }
   }
   if (C > 1) {
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
-    if (c == 0 && warp == 0) {
-      for (int r = 1; r < C; ++r) {
-        const Shared* o = cl.map_shared_rank(&sh, r);
-        p = join(p, o->part);
-        ahead += o->ahead;
-        if (k > 0) top = merge_sorted(top, o->top[lane], lane);
+    if (c == 0 && warp < C) {  // warp r brings CTA r's
+      const Shared* o = cl.map_shared_rank(&sh, warp);
+      if (lane < k) s_key[warp * k + lane] = o->top[lane];
+      if (lane == 0) {
+        s_part[warp] = o->part;
+        s_ahead[warp] = o->ahead;
       }
     }
     cl.sync();  // the others' shared memory is read until here
+    if (c != 0) return;
+    __syncthreads();
+    if (k > 0) {
+      rank(C * k, sh.top);
+      __syncthreads();
+    }
+    if (warp == 0) {
+      p = s_part[lane % C];
+      ahead = s_ahead[lane % C];
+      join_lanes(C);
+    }
   }
-  if (c != 0 || warp != 0) return;
+  if (warp != 0) return;
+  if (lane < k) top = sh.top[lane];
   const bool none = !(p.S > 0.f);
   const float lnS = logf(p.S);
   if (lane == 0) {

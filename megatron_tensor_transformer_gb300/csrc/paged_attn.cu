@@ -60,7 +60,7 @@ constexpr float kNoRef = -1e38f;           // a reference that any score is a st
 constexpr int kP = 128;                    // positions per chunk: the rows of an MMA
 constexpr int kN = 16;                     // heads of an MMA (its columns)
 constexpr int kMasks = 32;                 // ring of the chunks' masks: above the chunks in flight
-constexpr int kFan = 8;                    // pieces joined at once
+constexpr int kFan = 5;                    // pieces joined at once (131071 tokens: 87.4 us with 5, 89.2 with 8, 90.0 with 24)
 constexpr int kSlots = 2 * kPagedMaxCtas;  // pieces: a split (request, kv head) is a CTA's first item or its last
 constexpr int kWsHead = 2 * kSlots;        // counters: by the slot of the first of kFan pieces, then of the first of all
 
@@ -84,9 +84,6 @@ struct PCfg {
   static constexpr float kNext = FP8 ? 16.f : 1.f;                // each code of P after the first is held times this
   static constexpr int kUsed = 2 * kN * (QTERMS + 2 * NB * TERMS);  // TMEM: S [2][QTERMS][16], O [2][team][NB][TERMS][16]
   static constexpr uint32_t kCols = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
-  // A chunk is two units of work, and a (request, kv head)'s beginning and end about 1 us: one unit where a
-  // chunk's 64 KB or more take 1.4 us or more at an SM's share of the HBM, else three.
-  static constexpr int kEnds = STAGE >= 32 * 1024 ? 1 : 3;
   static constexpr size_t kRing = (size_t)NS * STAGE;
   static constexpr size_t SMEM = kRing + 2 * TERMS * PTILE + 2 * QTILE;
   static_assert(NS >= 3, "a chunk's k and v and the next one's k");
@@ -222,6 +219,9 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
                       const __grid_constant__ PagedAttnArgs a) {
   using C = PCfg<HD, FP8>;
   constexpr int kTeam = NG * 128, kSoftWarps = 2 * NG * 4, kThreads = 2 * kTeam + 128, kWarps = kThreads / 32;
+  // A chunk is two units of work.  The beginning and end of a (request, kv head) come to about 0.7 us for bf16,
+  // half a chunk of 64 KB at an SM's share of the HBM, and 2 and 4 us for e4m3 with 4 and 8 heads a thread.
+  constexpr int kEnds = FP8 ? (HPT == 8 ? 10 : 6) : C::STAGE >= 32 * 1024 ? 1 : 3;
   constexpr int kProducer = kSoftWarps, kScores = kProducer + 1, kItems = kProducer + 2, kPV = kProducer + 3;
   extern __shared__ __align__(1024) uint8_t ring[];  // the swizzles' atoms; static shared memory is padded to it
   uint8_t* sQ = ring + C::kRing;           // [2][QTILE]
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   // The units: a sum over the requests, a contiguous run of them per thread.
   const int per = (a.M + kThreads - 1) / kThreads, r0 = min(a.M, tid * per), r1 = min(a.M, r0 + per);
   long long here = 0;
-  for (int m = r0; m < r1; ++m) here += (long long)units_of(span_of(a, m), C::kEnds) * a.n_kv;
+  for (int m = r0; m < r1; ++m) here += (long long)units_of(span_of(a, m), kEnds) * a.n_kv;
   long long base = here;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   if (u0 < u1 && u0 >= base && u0 < base + here) {  // this thread's requests hold unit u0
     int m = r0;
     for (;; ++m) {
-      const long long n = (long long)units_of(span_of(a, m), C::kEnds) * a.n_kv;
+      const long long n = (long long)units_of(span_of(a, m), kEnds) * a.n_kv;
       if (u0 < base + n) break;
       base += n;
     }
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     long long at = u0 < u1 ? s_base : 0;  // the first unit of (m, gg)
     int j = 0;
     if (u0 < u1) {  // the head that holds u0
-      const int n = units_of(s, C::kEnds);
+      const int n = units_of(s, kEnds);
       gg = (int)((u0 - at) / n);
       at += (long long)gg * n;
     }
@@ -485,11 +485,11 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       Item it{};
       it.m = -1;
       while (at < u1 && !wait.failed) {
-        const int n = units_of(s, C::kEnds), ch = s.c1 - s.c0;
+        const int n = units_of(s, kEnds), ch = s.c1 - s.c0;
         if (n > 0) {
           // chunk i begins at unit at + kEnds + 2 i
           auto chunks_before = [&](long long u) {
-            return (int)min((long long)ch, max(0ll, (u - at - C::kEnds + 1) >> 1));
+            return (int)min((long long)ch, max(0ll, (u - at - kEnds + 1) >> 1));
           };
           it.c0 = chunks_before(u0);
           it.c1 = chunks_before(u1);
@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
           it.m = m;
           it.gg = gg;
           const bool split = it.c0 > 0 || it.c1 < ch;
-          it.a = split ? owner(U, nct, at + C::kEnds) : 0;
-          it.b = split ? owner(U, nct, at + C::kEnds + 2 * (ch - 1)) : 0;
+          it.a = split ? owner(U, nct, at + kEnds) : 0;
+          it.b = split ? owner(U, nct, at + kEnds + 2 * (ch - 1)) : 0;
           // whether it is the second item of CTA a, whose run then begins before it
           it.second = split && split_at(U, nct, it.a) < at;
           it.c0 += s.c0;
@@ -816,10 +816,10 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       auto last_of = [&](unsigned* counter, int n) {  // whole team: its writes are seen by who is last
         bar_sync(5 + team, kTeam);
         if (tt == 0) {
-          __threadfence();
-          const bool is_last = atomicAdd(counter, 1u) + 1 == (unsigned)n;
+          unsigned before;  // releases the team's writes, and acquires those of who counted in before
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+          const bool is_last = before + 1 == (unsigned)n;
           if (is_last) *counter = 0u;
-          __threadfence();
           s_last[team] = is_last;
         }
         bar_sync(5 + team, kTeam);
