@@ -183,9 +183,12 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& a, int m) {
 __device__ __forceinline__ int units_of(const Span& s, int ends) { return s.c0 == s.c1 ? 0 : ends + 2 * (s.c1 - s.c0); }
 // CTA i of nct takes units [U i / nct, U (i + 1) / nct), nct at most U / 2; a chunk belongs to the CTA of its
 // first unit, which is owner(u).
-__device__ __forceinline__ long long split_at(long long U, int nct, int i) { return U * i / nct; }
+__device__ __forceinline__ long long quot(long long x, long long y) {  // x / y, both >= 0: a 64-bit division only if it must be
+  return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+}
+__device__ __forceinline__ long long split_at(long long U, int nct, int i) { return quot(U * i, nct); }
 __device__ __forceinline__ int owner(long long U, int nct, long long u) {
-  return (int)(((u + 1) * nct + U - 1) / U) - 1;
+  return (int)quot((u + 1) * nct + U - 1, U) - 1;
 }
 
 // Chunks [c0, c1) of (m, gg), whose request attends to [lo, n): the piece of CTA blockIdx.x of those that CTAs
@@ -360,8 +363,11 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     }
     for (int j = 0; it.m >= 0; ++j) {
       ids_next = ids_from(it, at + 32);
-      nx = next_item(wait, j + 1, true);
-      if (nx.m >= 0) ids_item = ids_from(nx, first_page(nx));
+      auto look_ahead = [&]() {
+        nx = next_item(wait, j + 1, true);
+        if (nx.m >= 0) ids_item = ids_from(nx, first_page(nx));
+      };
+      if (j > 0) look_ahead();  // (the first item's copies do not wait for the second item)
       const int base = (it.gg / nkvs) * a.n_pages, g = it.gg % nkvs;
       for (int c = it.c0; c < it.c1; ++c, ++k) {
         const int pos = c * kP + box * box_rows, page = pos >> a.page_shift;
@@ -391,6 +397,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
             tc::tma_load_2d_hint(tc::smem_u32(ring + (size_t)st * C::STAGE) + (side * kP + box * box_rows) * C::INB,
                                  kv ? &tmV : &tmK, side * (C::INB / (FP8 ? 1 : 2)), row, B(kv_full[kv][k % C::NS]), pol);
         }
+        if (j == 0 && c == it.c0) look_ahead();
       }
       it = nx;
       at = first_page(it);
@@ -478,7 +485,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     int j = 0;
     if (u0 < u1) {  // the head that holds u0
       const int n = units_of(s, kEnds);
-      gg = (int)((u0 - at) / n);
+      gg = (int)quot(u0 - at, n);
       at += (long long)gg * n;
     }
     for (;;) {

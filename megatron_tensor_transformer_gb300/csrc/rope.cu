@@ -52,7 +52,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
 
 // grid (token groups, head groups), block (hd / 16, heads a pass)
 template <int SINK>
-__global__ void __launch_bounds__(256, 6) rope_kernel(const __grid_constant__ RopeArgs a, int toks, int heads) {
+__global__ void __launch_bounds__(256, SINK == SINK_E4M3 ? 4 : 6) rope_kernel(const __grid_constant__ RopeArgs a, int toks, int heads) {
   __shared__ __align__(16) float cs[kTok][2][128];
   tc::griddep_launch_dependents();
   tc::griddep_wait();
@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(256, 6) rope_kernel(const __grid_constant__ Ro
   }
   __syncthreads();
   const int hd = a.hd, per = (a.n_q + 2 * a.n_kv) / a.t, nqs = a.n_q / a.t, nkvs = a.n_kv / a.t, all = per * a.t;
+  const unsigned per_inv = 0xffffffffu / per + 1;  // h / per as a high product (per is at least 3)
   const int i = threadIdx.x;
   const bool turned = 8 * i < half;
   // the thread's two vectors within the head
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(256, 6) rope_kernel(const __grid_constant__ Ro
       kept = slot >= 0 && (slot >> a.page_shift) < a.n_pages;
     }
     for (int h = blockIdx.y * heads + threadIdx.y; h < h1; h += blockDim.y) {
-      const int sh = h / per, l = h % per;
+      const int sh = (int)__umulhi((unsigned)h, per_inv), l = h - sh * per;
       const bool is_q = l < nqs, is_v = l >= nqs + nkvs;
       if (SINK == SINK_QKV && is_v && a.q_out == a.qkv) continue;  // in place
       if (SINK != SINK_QKV && !is_q && !kept) continue;
