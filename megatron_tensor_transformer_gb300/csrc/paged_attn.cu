@@ -97,6 +97,28 @@ __device__ __forceinline__ float ex2(float x) {
 // what a sum taken under reference m counts under the reference mx (0 where nothing was summed)
 __device__ __forceinline__ float weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
 
+// the warp's largest value (a NaN is passed over)
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The sums of v[0 .. N) over the warp: lane l gets that of v[l >> (5 - log2 N)].
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1, o >>= 1) {  // the upper half of the lanes takes the upper half of the sums
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = lane & o ? v[i + n] : v[i], give = lane & o ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor_sync(kFull, give, o);
+    }
+  }
+  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(kFull, v[0], o);
+  return v[0];
+}
+
 // 32 lanes x N consecutive 32-bit columns of tensor memory; the values are there after landed()
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[N]) {
@@ -636,8 +658,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
 #pragma unroll
           for (int h = 0; h < HPT; ++h) {
             float v = counts ? s[h] * sc[h] : -INFINITY;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+            v = warp_max(v);
             if (lane == 0) s_max[warp][h] = v;
           }
           bar_sync(bid, 128);
@@ -729,12 +750,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       }
 
       // The item's end: the sums over the positions; the team of the first chunk brings the two together.
-#pragma unroll
-      for (int h = 0; h < HPT; ++h) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(kFull, l[h], o);
-        if (lane == 0) s_sum[warp][h] = l[h];
-      }
+      s_sum[warp][lane / (32 / HPT)] = warp_sums(l, lane);  // (the same sum from each lane that has it)
       bar_sync(bid, 128);
 #pragma unroll
       for (int h = 0; h < HPT; ++h) {
@@ -833,7 +849,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         return s_last[team] != 0;
       };
       // the pieces of CTAs first, first + step, ..: n of them, in order
-      auto join = [&](int e, int cta0, int step, int n, float& M, float& L, float4& v) {
+      auto join = [&](int e, size_t from, int cta0, int step, int n, float& M, float& L, float4& v) {
         const int hi = e / HD;
         M = -INFINITY;
         L = 0.f;
@@ -844,7 +860,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
           float Mb = M;
 #pragma unroll
           for (int q = 0; q < kFan; ++q) {
-            const float* pc = pieces + (size_t)slot_of(cta0 + min(b + q, n - 1) * step) * per_piece;
+            const float* pc = pieces + (from + slot_of(cta0 + min(b + q, n - 1) * step)) * per_piece;
             pm[q] = __ldcg(pc + G * HD + hi);
             pl[q] = __ldcg(pc + G * HD + G + hi);
             pv[q] = __ldcg(reinterpret_cast<const float4*>(pc + e));
@@ -871,38 +887,33 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       const int all = it.b - it.a + 1, fan0 = it.a + ((int)blockIdx.x - it.a) / kFan * kFan;
       const int nfan = min(kFan, it.b + 1 - fan0), nfans = (all + kFan - 1) / kFan;
       if (!last_of(a.ws + slot_of(fan0), nfan)) continue;
-      constexpr int EV = (16 * HD / 4 + kTeam - 1) / kTeam;  // vectors of four values per thread
-      if (nfans > 1) {
-        float M[EV], L[EV];
-        float4 v[EV];
-#pragma unroll
-        for (int q = 0; q < EV; ++q) {
-          const int e = 4 * (tt + q * kTeam);
-          if (e < G * HD) join(e, fan0, 1, nfan, M[q], L[q], v[q]);
-        }
-        bar_sync(5 + team, kTeam);  // every piece is read before the first one's place is written
-        float* dst = pieces + (size_t)slot_of(fan0) * per_piece;
-#pragma unroll
-        for (int q = 0; q < EV; ++q) {
-          const int e = 4 * (tt + q * kTeam);
-          if (e >= G * HD) break;
-          *reinterpret_cast<float4*>(dst + e) = v[q];
-          if (e % HD == 0) {
-            dst[G * HD + e / HD] = M[q];
-            dst[G * HD + G + e / HD] = L[q];
+      int cta0 = fan0, step = 1, n = nfan;
+      size_t from = 0;  // joined pieces lie kSlots behind the slot of their first
+      for (bool final = nfans == 1;; final = true) {
+#pragma unroll 1
+        for (int e = 4 * tt; e < G * HD; e += 4 * kTeam) {
+          float M, L;
+          float4 v;
+          join(e, from, cta0, step, n, M, L, v);
+          if (!final) {
+            float* dst = pieces + (kSlots + (size_t)slot_of(fan0)) * per_piece;
+            *reinterpret_cast<float4*>(dst + e) = v;
+            if (e % HD == 0) {
+              dst[G * HD + e / HD] = M;
+              dst[G * HD + G + e / HD] = L;
+            }
+            continue;
           }
+          const float r = L == 0.f ? 0.f : 1.0f / L;
+          *reinterpret_cast<uint2*>(a.o + orow * HD + e) =
+              make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
+          if (a.lse && e % HD == 0) a.lse[orow + e / HD] = (M + log2f(L)) * kLn2;
         }
-        if (!last_of(a.ws + kSlots + slot_of(it.a), nfans)) continue;
-      }
-      for (int e = 4 * tt; e < G * HD; e += 4 * kTeam) {
-        float M, L;
-        float4 v;
-        if (nfans > 1) join(e, it.a, kFan, nfans, M, L, v);
-        else join(e, it.a, 1, nfan, M, L, v);
-        const float r = L == 0.f ? 0.f : 1.0f / L;
-        *reinterpret_cast<uint2*>(a.o + orow * HD + e) =
-            make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
-        if (a.lse && e % HD == 0) a.lse[orow + e / HD] = (M + log2f(L)) * kLn2;
+        if (final || !last_of(a.ws + kSlots + slot_of(it.a), nfans)) break;
+        cta0 = it.a;
+        step = kFan;
+        n = nfans;
+        from = kSlots;
       }
     }
   }
@@ -958,7 +969,7 @@ cudaError_t launch(const PagedAttnArgs& a, const void* k_pages, const void* v_pa
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int G, int hd) {
-  return (kWsHead + kSlots * piece_floats(G, hd)) * 4;
+  return (kWsHead + 2 * kSlots * piece_floats(G, hd)) * 4;  // the pieces, and the joined ones
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,
