@@ -463,6 +463,27 @@ tp_status tp_paged_attn_decode(const tp_shape* shape /* host */, const tp_pages*
 tp_status tp_lm_head_forward(const tp_packed_desc* desc /* host */, const void* w, const void* x, int32_t M,
                              float* logits, void* ws, size_t ws_bytes, uint32_t flags, void* stream);
 
+/* The attention block of a decode step over a paged cache, in one call, one row per request:
+ *   qkv_out = x . Wqkv                          column-parallel, shard-major (tp_colpar_forward)
+ *   q_out = rotated q; the pages' slots[m] = rotated k, v       (tp_rope_append; rope NULL: not rotated)
+ *   o_in = attention of request m over its lens[m] positions, the new one included (tp_paged_attn_decode,
+ *          scale 1 / sqrt(hd))
+ *   y = residual + o_in . Wo                     row-parallel, shards folded in order (tp_rowpar_forward)
+ * The weights and flags as for tp_attn_block_forward, the other arguments as for the calls named;
+ * the same bits as these calls.  qkv_out [M, (n_q + 2 n_kv) hd], q_out and o_in [M, n_q hd]: the caller's
+ * bf16 buffers; y must not alias x or residual.  ws: tp_paged_attn_block_workspace_bytes(shape, M, flags)
+ * bytes, zero-filled once before first use.  Errors as for the calls, all checked before the first
+ * launch.  M == 0 is a no-op. */
+size_t tp_paged_attn_block_workspace_bytes(const tp_shape* shape /* host */, int32_t M, uint32_t flags);
+tp_status tp_paged_attn_block_forward(const tp_packed_desc* qkv /* host */, const void* qkv_w,
+                                      const tp_packed_desc* o /* host */, const void* o_w, const void* x,
+                                      const void* residual, int32_t M, const tp_rope* rope /* host */,
+                                      const tp_pages* pages /* host */, const int32_t* positions,
+                                      const int32_t* slots, void* k_pages, void* v_pages, const float* k_scale,
+                                      const float* v_scale, const int32_t* block_table, const int32_t* lens,
+                                      int32_t window, void* y, void* qkv_out, void* q_out, void* o_in, void* ws,
+                                      size_t ws_bytes, uint32_t flags, void* stream);
+
 /* Log probabilities over logits [M, vocab] fp32 (rows ldl apart, ldl >= vocab; tp_lm_head_forward's output),
  * with P = softmax of the row, in one pass over it:
  *   logprob[m] = ln P(ids[m]); 0 for an id outside [0, vocab), which asks for no token

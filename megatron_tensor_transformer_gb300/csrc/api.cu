@@ -215,6 +215,58 @@ RopeArgs rope_args(const tp_shape* sh, const tp_rope* rope, const void* qkv, con
   return a;
 }
 
+// The checks of tp_rope_append and tp_paged_attn_decode after those of the shape and the pages; both
+// fill *out unless M is 0.
+tp_status append_args(const tp_shape* sh, const tp_rope* rope, const tp_pages* pages, const void* qkv,
+                      const int32_t* positions, const int32_t* slots, int32_t M, void* q_out, void* k_pages,
+                      void* v_pages, const float* k_scale, const float* v_scale, RopeArgs* out) {
+  if (M < 0) return TP_ERR_INVALID_ARG;
+  const tp_status st = check_rope(rope, sh->head_dim);
+  if (st != TP_OK) return st;
+  if (pages->kv_dtype == TP_BF16 && (k_scale || v_scale)) return TP_ERR_INVALID_ARG;
+  if (M == 0) return TP_OK;
+  if (!qkv || (rope && !positions) || !slots || !q_out || !k_pages || !v_pages) return TP_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned4(positions) ||
+      !aligned4(slots) || !aligned4(k_scale) || !aligned4(v_scale))
+    return TP_ERR_ALIGN;
+  const size_t nq = (size_t)M * sh->n_q_heads * sh->head_dim * 2;
+  if (overlap(q_out, nq, qkv, nq + (size_t)M * 2 * sh->n_kv_heads * sh->head_dim * 2)) return TP_ERR_INVALID_ARG;
+  *out = rope_args(sh, rope, qkv, positions, M, q_out);
+  out->slots = slots;
+  out->k_pages = k_pages;
+  out->v_pages = v_pages;
+  out->k_scale = k_scale;
+  out->v_scale = v_scale;
+  out->page_shift = page_shift(pages);
+  out->n_pages = pages->n_pages;
+  return TP_OK;
+}
+tp_status attn_args(const tp_shape* sh, const tp_pages* pages, const void* q, const void* k_pages, const void* v_pages,
+                    const float* k_scale, const float* v_scale, const int32_t* block_table, const int32_t* lens,
+                    int32_t M, float scale, int32_t window, void* o_in, float* lse, void* ws, size_t ws_bytes,
+                    PagedAttnArgs* out) {
+  if (M < 0 || window < 0 || !std::isfinite(scale)) return TP_ERR_INVALID_ARG;
+  if (pages->kv_dtype == TP_BF16 && (k_scale || v_scale)) return TP_ERR_INVALID_ARG;
+  if (!attn_supported(sh->head_dim, sh->n_q_heads / sh->n_kv_heads)) return TP_ERR_UNSUPPORTED;
+  if (((int64_t)sh->n_kv_heads * pages->n_pages << page_shift(pages)) >= (int64_t(1) << 31)) return TP_ERR_UNSUPPORTED;
+  if (M == 0) return TP_OK;
+  if (!q || !k_pages || !v_pages || !block_table || !lens || !o_in) return TP_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o_in) || !aligned4(block_table) ||
+      !aligned4(lens) || !aligned4(lse) || !aligned4(k_scale) || !aligned4(v_scale))
+    return TP_ERR_ALIGN;
+  if (!ws || ws_bytes < tp_paged_attn_workspace_bytes(sh)) return TP_ERR_WORKSPACE;
+  if (!aligned16(ws)) return TP_ERR_ALIGN;
+  const size_t n = (size_t)M * sh->n_q_heads * sh->head_dim * 2;
+  if (overlap(q, n, o_in, n)) return TP_ERR_INVALID_ARG;  // a request's q is read by several CTAs
+  unsigned* err = tc_error_word();
+  if (!err) return TP_ERR_CUDA;
+  *out = PagedAttnArgs{static_cast<const __nv_bfloat16*>(q), k_scale, v_scale, block_table, lens,
+                       static_cast<__nv_bfloat16*>(o_in), lse, static_cast<unsigned*>(ws), err, M, sh->t, sh->n_q_heads,
+                       sh->n_kv_heads, window, page_shift(pages), pages->n_pages, pages->max_pages, pages->table_stride,
+                       scale == 0.f ? 1.0f / sqrtf((float)sh->head_dim) : scale};
+  return TP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1125,25 +1177,9 @@ tp_status tp_rope_append(const tp_shape* sh, const tp_rope* rope, const tp_pages
   tp_status st = check_shape(sh, TP_W_QKV);
   if (st == TP_OK) st = check_pages(pages);
   if (st != TP_OK) return st;
-  if (M < 0) return TP_ERR_INVALID_ARG;
-  st = check_rope(rope, sh->head_dim);
-  if (st != TP_OK) return st;
-  if (pages->kv_dtype == TP_BF16 && (k_scale || v_scale)) return TP_ERR_INVALID_ARG;
-  if (M == 0) return TP_OK;
-  if (!qkv || (rope && !positions) || !slots || !q_out || !k_pages || !v_pages) return TP_ERR_INVALID_ARG;
-  if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned4(positions) ||
-      !aligned4(slots) || !aligned4(k_scale) || !aligned4(v_scale))
-    return TP_ERR_ALIGN;
-  const size_t nq = (size_t)M * sh->n_q_heads * sh->head_dim * 2;
-  if (overlap(q_out, nq, qkv, nq + (size_t)M * 2 * sh->n_kv_heads * sh->head_dim * 2)) return TP_ERR_INVALID_ARG;
-  RopeArgs a = rope_args(sh, rope, qkv, positions, M, q_out);
-  a.slots = slots;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.page_shift = page_shift(pages);
-  a.n_pages = pages->n_pages;
+  RopeArgs a;
+  st = append_args(sh, rope, pages, qkv, positions, slots, M, q_out, k_pages, v_pages, k_scale, v_scale, &a);
+  if (st != TP_OK || M == 0) return st;
   return cuda_status(launch_rope_append(a, pages->kv_dtype, S(stream)));
 }
 
@@ -1159,26 +1195,54 @@ tp_status tp_paged_attn_decode(const tp_shape* sh, const tp_pages* pages, const 
   tp_status st = check_shape(sh, TP_W_QKV);
   if (st == TP_OK) st = check_pages(pages);
   if (st != TP_OK) return st;
-  if (M < 0 || window < 0 || !std::isfinite(scale)) return TP_ERR_INVALID_ARG;
-  if (pages->kv_dtype == TP_BF16 && (k_scale || v_scale)) return TP_ERR_INVALID_ARG;
-  if (!attn_supported(sh->head_dim, sh->n_q_heads / sh->n_kv_heads)) return TP_ERR_UNSUPPORTED;
-  if (((int64_t)sh->n_kv_heads * pages->n_pages << page_shift(pages)) >= (int64_t(1) << 31)) return TP_ERR_UNSUPPORTED;
-  if (M == 0) return TP_OK;
-  if (!q || !k_pages || !v_pages || !block_table || !lens || !o_in) return TP_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o_in) || !aligned4(block_table) ||
-      !aligned4(lens) || !aligned4(lse) || !aligned4(k_scale) || !aligned4(v_scale))
-    return TP_ERR_ALIGN;
-  if (!ws || ws_bytes < tp_paged_attn_workspace_bytes(sh)) return TP_ERR_WORKSPACE;
-  if (!aligned16(ws)) return TP_ERR_ALIGN;
-  const size_t n = (size_t)M * sh->n_q_heads * sh->head_dim * 2;
-  if (overlap(q, n, o_in, n)) return TP_ERR_INVALID_ARG;  // a request's q is read by several CTAs
-  unsigned* err = tc_error_word();
-  if (!err) return TP_ERR_CUDA;
-  PagedAttnArgs a{static_cast<const bf16*>(q), k_scale, v_scale, block_table, lens, static_cast<bf16*>(o_in), lse,
-                  static_cast<unsigned*>(ws), err, M, sh->t, sh->n_q_heads, sh->n_kv_heads, window,
-                  page_shift(pages), pages->n_pages, pages->max_pages, pages->table_stride,
-                  scale == 0.f ? 1.0f / sqrtf((float)sh->head_dim) : scale};
+  PagedAttnArgs a;
+  st = attn_args(sh, pages, q, k_pages, v_pages, k_scale, v_scale, block_table, lens, M, scale, window, o_in, lse, ws,
+                 ws_bytes, &a);
+  if (st != TP_OK || M == 0) return st;
   return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
+}
+
+size_t tp_paged_attn_block_workspace_bytes(const tp_shape* sh, int32_t M, uint32_t flags) {
+  if (!sh || M < 0) return 0;
+  const size_t proj = tp_workspace_bytes(sh, M, flags), attn = tp_paged_attn_workspace_bytes(sh);
+  return proj == 0 || attn == 0 ? 0 : (size_t)align_up(proj) + attn;
+}
+
+tp_status tp_paged_attn_block_forward(const tp_packed_desc* qkv, const void* qkv_w, const tp_packed_desc* o,
+                                      const void* o_w, const void* x, const void* residual, int32_t M,
+                                      const tp_rope* rope, const tp_pages* pages, const int32_t* positions,
+                                      const int32_t* slots, void* k_pages, void* v_pages, const float* k_scale,
+                                      const float* v_scale, const int32_t* block_table, const int32_t* lens,
+                                      int32_t window, void* y, void* qkv_out, void* q_out, void* o_in, void* ws,
+                                      size_t ws_bytes, uint32_t flags, void* stream) {
+  tp_status st = check_desc(qkv, TP_W_QKV, qkv_w);
+  if (st == TP_OK) st = check_desc(o, TP_W_O, o_w);
+  if (st == TP_OK) st = check_pages(pages);
+  if (st != TP_OK) return st;
+  if (!same_block(qkv->shape, o->shape, false)) return TP_ERR_LAYOUT_MISMATCH;
+  if ((flags & ~kFwdFlags) || bad_kernel_flags(flags)) return TP_ERR_INVALID_ARG;
+  const tp_shape& sh = qkv->shape;
+  if (M < 0 || (M > 0 && (!x || !y))) return TP_ERR_INVALID_ARG;
+  if (M > 0 && (!aligned16(x) || !aligned16(y) || (residual && !aligned16(residual)))) return TP_ERR_ALIGN;
+  const size_t proj = align_up(tp_workspace_bytes(&sh, M, flags));
+  if (M > 0 && (!ws || ws_bytes < tp_paged_attn_block_workspace_bytes(&sh, M, flags))) {
+    // a shape that the attention does not take has no workspace size; it is refused as such below
+    if (tp_paged_attn_workspace_bytes(&sh) != 0) return TP_ERR_WORKSPACE;
+  }
+  RopeArgs ra;
+  PagedAttnArgs aa;
+  st = append_args(&sh, rope, pages, qkv_out, positions, slots, M, q_out, k_pages, v_pages, k_scale, v_scale, &ra);
+  if (st == TP_OK)
+    st = attn_args(&sh, pages, q_out, k_pages, v_pages, k_scale, v_scale, block_table, lens, M, 0.f, window, o_in,
+                   nullptr, static_cast<uint8_t*>(ws) + proj, ws_bytes - proj, &aa);
+  if (st != TP_OK || M == 0) return st;
+  cudaStream_t s = S(stream);
+  st = run_colpar(qkv, qkv_w, static_cast<const bf16*>(x), M, qkv_out, COLPAR_BF16, s, flags, ws, proj);
+  if (st == TP_OK) st = cuda_status(launch_rope_append(ra, pages->kv_dtype, s));
+  if (st == TP_OK) st = cuda_status(launch_paged_attn(aa, pages->kv_dtype, sh.head_dim, k_pages, v_pages, s));
+  if (st != TP_OK) return st;
+  return run_rowpar(o, o_w, static_cast<const bf16*>(o_in), M, static_cast<const bf16*>(residual),
+                    static_cast<bf16*>(y), nullptr, ws, proj, flags, s);
 }
 
 tp_status tp_token_logprobs(const float* logits, int64_t ldl, int32_t M, int32_t vocab, const int32_t* ids, int32_t k,

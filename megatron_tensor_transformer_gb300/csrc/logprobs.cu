@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(kNT, 2) logprobs_kernel(const LogprobsArgs a) 
   __shared__ __align__(16) float s_max[64];  // the groups' maxima
   __shared__ float s_bar;
   __shared__ int s_n;
-  tc::griddep_launch_dependents();
   tc::griddep_wait();
+  tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int m = blockIdx.x / C, c = blockIdx.x % C, V = a.vocab, k = a.k;
   const float* x = a.logits + (int64_t)m * a.ldl;

@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     tc::tma_prefetch_desc(&tmV);
   }
   if (warp == kScores) tc::tmem_alloc(tc::smem_u32(&s_tmem), C::kCols);
-  tc::griddep_launch_dependents();
   tc::griddep_wait();
+  tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
   const int G = a.n_q / a.n_kv, nkvs = a.n_kv / a.t;
 
   // The units: a sum over the requests, a contiguous run of them per thread.

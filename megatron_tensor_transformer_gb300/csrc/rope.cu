@@ -54,8 +54,8 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
 template <int SINK>
 __global__ void __launch_bounds__(256, SINK == SINK_E4M3 ? 4 : 6) rope_kernel(const __grid_constant__ RopeArgs a, int toks, int heads) {
   __shared__ __align__(16) float cs[kTok][2][128];
-  tc::griddep_launch_dependents();
   tc::griddep_wait();
+  tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
   const int m0 = blockIdx.x * toks, nt = min(toks, a.M - m0), half = a.rope.rot_dim / 2;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
   for (int j = tid; j < nt * half; j += nthr) {

@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(NT) tables_kernel(const TablesArgs a) {
   __shared__ int mark[NT], wmax[NT / 32];
   __shared__ int s_m[NT], s_len[NT];
   __shared__ long long s_first[NT], s_base[NT];  // the request's first row; its first page in the free list, -1: refused
-  tc::griddep_launch_dependents();
   tc::griddep_wait();
+  tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.M + NT - 1) / NT, m0 = min(a.M, tid * per), m1 = min(a.M, m0 + per);
   const long long head = a.head ? *a.head : 0;

@@ -32,7 +32,8 @@ EXPORTS = ["tp_packed_bytes", "tp_describe", "tp_partition_weights", "tp_workspa
            "tp_lm_head_forward", "tp_embed_lookup", "tp_attn_workspace_bytes", "tp_attn_decode",
            "tp_attn_block_workspace_bytes", "tp_attn_block_forward", "tp_quantize_fp8_per_token",
            "tp_paged_tables", "tp_rope_describe", "tp_rope_forward", "tp_rope_append",
-           "tp_paged_attn_workspace_bytes", "tp_paged_attn_decode", "tp_token_logprobs"]
+           "tp_paged_attn_workspace_bytes", "tp_paged_attn_decode", "tp_paged_attn_block_workspace_bytes",
+           "tp_paged_attn_block_forward", "tp_token_logprobs"]
 
 
 class TpxError(RuntimeError):
@@ -122,6 +123,9 @@ def lib():
             "tp_paged_attn_workspace_bytes": (SZ, [P(Shape)]),
             "tp_paged_attn_decode": (I32, [P(Shape), P(Pages), V, V, V, V, V, V, V, I32, ctypes.c_float, I32, V, V, V,
                                            SZ, V]),
+            "tp_paged_attn_block_workspace_bytes": (SZ, [P(Shape), I32, U32]),
+            "tp_paged_attn_block_forward": (I32, [P(PackedDesc), V, P(PackedDesc), V, V, V, I32, P(Rope), P(Pages), V, V,
+                                                  V, V, V, V, V, V, I32, V, V, V, V, V, SZ, U32, V]),
             "tp_token_logprobs": (I32, [V, ctypes.c_int64, I32, I32, V, I32, V, V, V, V, V, V]),
         }
         for name, (res, args) in sig.items():
@@ -397,6 +401,29 @@ def tp_paged_attn_decode(shape, pages, q, k_pages, v_pages, block_table, lens, o
                                       window, _ptr(o_in), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
            "tp_paged_attn_decode")
     return o_in
+
+
+def tp_paged_attn_block_workspace_bytes(shape, M, flags=0):
+    return lib().tp_paged_attn_block_workspace_bytes(ctypes.byref(shape), M, flags)
+
+
+def new_paged_attn_block_workspace(shape, M, device, flags=0):
+    """Zero-filled workspace of tp_paged_attn_block_forward (its counters start at zero)."""
+    return torch.zeros(max(1, tp_paged_attn_block_workspace_bytes(shape, M, flags)), dtype=torch.uint8, device=device)
+
+
+def tp_paged_attn_block_forward(qkv, qkv_w, o, o_w, x, residual, rope, pages, positions, slots, k_pages, v_pages,
+                                block_table, lens, y, qkv_out, q_out, o_in, ws, window=0, k_scale=None, v_scale=None,
+                                flags=0, stream=None):
+    """x, residual (or None), y: [M, d] bf16; qkv_out [M, (n_q + 2 n_kv) hd], q_out and o_in [M, n_q hd] bf16; the
+    cache as for tp_rope_append and tp_paged_attn_decode; lens counts the new token."""
+    _check(lib().tp_paged_attn_block_forward(ctypes.byref(qkv), _ptr(qkv_w), ctypes.byref(o), _ptr(o_w), _ptr(x),
+                                             _ptr(residual), x.shape[0], None if rope is None else ctypes.byref(rope),
+                                             ctypes.byref(pages), _ptr(positions), _ptr(slots), _ptr(k_pages),
+                                             _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(lens),
+                                             window, _ptr(y), _ptr(qkv_out), _ptr(q_out), _ptr(o_in), _ptr(ws),
+                                             ws.numel(), flags, _stream(stream)), "tp_paged_attn_block_forward")
+    return y
 
 
 def tp_token_logprobs(logits, ids, logprob, entropy, rank, top_logprob=None, top_id=None, stream=None):

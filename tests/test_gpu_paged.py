@@ -9,7 +9,7 @@ import torch
 from megatron_tensor_transformer_gb300 import inputs, tpx
 from oracle import paged_oracle as PO
 from oracle import tp_oracle as O
-from tests.test_gpu_parity import bits
+from tests.test_gpu_parity import bits, check_close
 
 pytestmark = pytest.mark.gpu
 
@@ -622,3 +622,62 @@ def test_paged_equals_contiguous_attention(dev):
             assert torch.equal(flat.contiguous().view(torch.int16), c[:, m, :, :150].contiguous().view(torch.int16))
     a, b = O.as_f64(bits(oc)), O.as_f64(bits(op))
     assert O.rel_frobenius(bits(op), a) <= 5e-3 and np.abs(a - b).max() <= 2e-2 * np.sqrt((a * a).mean())
+
+
+@pytest.mark.parametrize("wtype,kv", [(tpx.TP_BF16, tpx.TP_BF16), (tpx.TP_FP8_E4M3, tpx.TP_FP8_E4M3),
+                                      (tpx.TP_BF16, tpx.TP_FP8_E4M3)])
+@pytest.mark.parametrize("M", [1, 5, 70])
+def test_paged_attention_block_decode_steps(dev, wtype, kv, M):
+    """Decode steps as a server makes them: tables, the block in one call, the lm_head and the log probabilities.
+    The block equals its four calls bit for bit, and the last step's y equals the oracle on the cache it left."""
+    d, n_q, n_kv, hd, t, page, P, V = 1024, 8, 4, 128, 2, 16, 6, 1000
+    x, wqkv, wo = inputs.proj_inputs(d, n_q, n_kv, hd, M, seed=13, device=dev)
+    sh = tpx.make_shape(d, n_q=n_q, n_kv=n_kv, hd=hd, t=t, wtype=wtype)
+    q_w, qd = tpx.tp_partition_weights(sh, tpx.TP_W_QKV, wqkv)
+    o_w, od = tpx.tp_partition_weights(sh, tpx.TP_W_O, wo)
+    vsh = tpx.make_shape(d, t=t, vocab=V)
+    v_w, vd = tpx.tp_partition_weights(vsh, tpx.TP_W_VOCAB, inputs.normal_bf16((d, V), 0.02, 13, 98, dev))
+    pages, rope = tpx.make_pages(page, M * P, P, kv), tpx.make_rope(64, 500000.0)
+    ks, vs = scales(dev, n_kv, kv, 13)
+    free = i32(np.random.default_rng(13).permutation(M * P), dev)
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device=dev)
+    b16 = lambda *s: torch.full(s, float("nan"), dtype=torch.bfloat16, device=dev)
+    raw = torch.bfloat16 if kv == tpx.TP_BF16 else torch.float8_e4m3fn
+    caches = [[z(t, M * P, n_kv // t, page, hd, dt=raw) for _ in range(2)] for _ in range(2)]
+    table, lens, counts = z(M, P) - 1, [z(M), z(M)], [z(3), z(3)]
+    cu, pos, slots, add = z(M + 1), z(M), z(M), i32(np.ones(M), dev)
+    ws, ws2 = tpx.new_paged_attn_block_workspace(sh, M, dev), tpx.new_workspace(sh, M, dev)
+    aws = tpx.new_paged_attn_workspace(sh, dev)
+    Q = (n_q + 2 * n_kv) * hd
+    out = [dict(y=b16(M, d), qkv=b16(M, Q), q=b16(M, n_q * hd), o=b16(M, n_q * hd)) for _ in range(2)]
+    for step in range(35):
+        xs = inputs.normal_bf16((M, d), 1.0, 14 + step, 99, dev)
+        tpx.tp_paged_tables(pages, lens[0], add, free, table, lens[1], cu, pos, slots, counts[1], head=counts[0])
+        a, b = out
+        tpx.tp_paged_attn_block_forward(qd, q_w, od, o_w, xs, xs, rope, pages, pos, slots, *caches[0], table, lens[1],
+                                        a["y"], a["qkv"], a["q"], a["o"], ws, window=20, k_scale=ks, v_scale=vs)
+        tpx.tp_colpar_forward(qd, q_w, xs, b["qkv"], ws=ws2)
+        tpx.tp_rope_append(sh, rope, pages, b["qkv"], pos, slots, b["q"], *caches[1], ks, vs)
+        tpx.tp_paged_attn_decode(sh, pages, b["q"], *caches[1], table, lens[1], b["o"], aws, window=20, k_scale=ks,
+                                 v_scale=vs)
+        tpx.tp_rowpar_forward(od, o_w, b["o"], xs, b["y"], ws2)
+        lens.reverse()
+        counts.reverse()
+    sync()
+    for key in out[0]:
+        assert torch.equal(out[0][key].view(torch.int16), out[1][key].view(torch.int16)), key
+    for u, v in zip(*caches):
+        assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+    assert lens[0].tolist() == [35] * M and counts[0].tolist() == [M * 3, M, 0]
+    wo_ref = O.as_f64(bits(wo))
+    if wtype == tpx.TP_FP8_E4M3:
+        wo_ref = O.dequantize_fp8(*O.quantize_fp8_per_channel(wo_ref))
+    y_ref = O.as_f64(bits(out[0]["o"])) @ wo_ref + O.as_f64(bits(xs))
+    check_close(bits(out[0]["y"]), y_ref, what="y of the last step")
+    logits = torch.empty((M, V), dtype=torch.float32, device=dev)
+    tpx.tp_lm_head_forward(vd, v_w, out[0]["y"], logits)
+    lp, ent, rank = (torch.zeros(M, dtype=dt, device=dev) for dt in (torch.float32, torch.float32, torch.int32))
+    tl, ti = torch.zeros((M, 3), device=dev), z(M, 3)
+    tpx.tp_token_logprobs(logits, logits.argmax(1).to(torch.int32), lp, ent, rank, tl, ti)
+    sync()
+    assert (rank == 1).all() and torch.equal(lp, tl[:, 0]) and torch.equal(ti[:, 0].long(), logits.argmax(1))

@@ -136,6 +136,31 @@ def test_logprobs_refusals():
     assert logprobs(M=0) == tpx.TP_OK
 
 
+def test_block_refusals():
+    E = tpx.TP_ERR_INVALID_ARG
+    sh = tpx.make_shape(1024, n_q=8, n_kv=4, hd=128, t=2)
+    q, o = tpx.tp_describe(sh, tpx.TP_W_QKV), tpx.tp_describe(sh, tpx.TP_W_O)
+    BUF = [ctypes.c_void_p((1 << 34) + (i << 28)) for i in range(6)]
+
+    def block(qd=q, od=o, x=FAKE, M=4, rope=None, pages=PG, pos=FAKE, slots=FAKE, k=FAKE3, v=FAKE3, ks=None, table=FAKE,
+              lens=FAKE, window=0, y=BUF[0], qkv=BUF[1], qo=BUF[2], oi=BUF[3], ws=BUF[4], n=1 << 27, flags=0):
+        return tpx.lib().tp_paged_attn_block_forward(
+            ctypes.byref(qd), FAKE, ctypes.byref(od), FAKE, x, None, M, rope, ctypes.byref(pages), pos, slots, k, v, ks, None,
+            table, lens, window, y, qkv, qo, oi, ws, n, flags, None)
+    other = tpx.tp_describe(tpx.make_shape(1024, n_q=8, n_kv=4, hd=128, t=4), tpx.TP_W_O)
+    assert block(od=other) == tpx.TP_ERR_LAYOUT_MISMATCH and block(qd=o) == tpx.TP_ERR_LAYOUT_MISMATCH
+    assert block(pages=tpx.make_pages(8, 4, 4)) == tpx.TP_ERR_SHAPE
+    for kw in (dict(x=None), dict(M=-1), dict(slots=None), dict(k=None), dict(v=None), dict(ks=FAKE), dict(table=None),
+               dict(lens=None), dict(window=-1), dict(y=None), dict(qkv=None), dict(qo=None), dict(oi=None),
+               dict(flags=0x1000), dict(oi=BUF[2]), dict(qo=BUF[1])):
+        assert block(**kw) == E, kw
+    for kw in (dict(x=ODD), dict(y=ODD), dict(qkv=ODD), dict(qo=ODD), dict(oi=ODD), dict(slots=ODD), dict(lens=ODD)):
+        assert block(**kw) == tpx.TP_ERR_ALIGN, kw
+    need = tpx.tp_paged_attn_block_workspace_bytes(sh, 4)
+    assert need > tpx.tp_workspace_bytes(sh, 4) and block(ws=None) == block(n=need - 1) == tpx.TP_ERR_WORKSPACE
+    assert block(M=0, x=None, ws=None, n=0) == tpx.TP_OK
+
+
 @pytest.mark.parametrize("scaling", ["none", "linear", "wavelength", "yarn"])
 @pytest.mark.parametrize("rot,theta,factor", [(128, 500000.0, 8.0), (64, 10000.0, 1.0), (32, 1e6, 40.0), (256, 2.0, 0.1)])
 def test_described_rotation(scaling, rot, theta, factor):
