@@ -225,15 +225,19 @@ __device__ __forceinline__ uint32_t group_bits(const Item& it, int c, uint32_t l
 }
 // A role's bounded waits: one that runs out sets the error word, and the role goes on without
 // waiting, so that every barrier is still met and the kernel ends.
+// (The loop is a function of its own: inlined at every wait it made the roles' code together larger than the
+// SM's instruction cache, and the kernel's time depend on where the compiler put what, by up to a quarter.)
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
+  const bool ok = tc::mbar_wait(bar, parity);
+  if (!ok) atomicExch(err, code);
+  return !ok;
+}
 struct Waits {
   unsigned* err;
   unsigned code;
   bool failed;
   __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) {
-    if (!failed && !tc::mbar_wait(bar, parity)) {
-      atomicExch(err, code);
-      failed = true;
-    }
+    if (!tc::mbar_try_wait(bar, parity) && !failed) failed = wait_long(bar, parity, err, code);
   }
 };
 
@@ -245,8 +249,8 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   using C = PCfg<HD, FP8>;
   constexpr int kTeam = NG * 128, kSoftWarps = 2 * NG * 4, kThreads = 2 * kTeam + 128, kWarps = kThreads / 32;
   // A chunk is two units of work.  The beginning and end of a (request, kv head) come to about 0.7 us for bf16,
-  // half a chunk of 64 KB at an SM's share of the HBM, and 2 and 4 us for e4m3 with 4 and 8 heads a thread.
-  constexpr int kEnds = FP8 ? (HPT == 8 ? 10 : 6) : C::STAGE >= 32 * 1024 ? 1 : 3;
+  // half a chunk of 64 KB at an SM's share of the HBM, and 2 and 3 us for e4m3 with 4 and 8 heads a thread.
+  constexpr int kEnds = FP8 ? (HPT == 8 ? 8 : 6) : C::STAGE >= 32 * 1024 ? 1 : 4;
   constexpr int kProducer = kSoftWarps, kScores = kProducer + 1, kItems = kProducer + 2, kPV = kProducer + 3;
   extern __shared__ __align__(1024) uint8_t ring[];  // the swizzles' atoms; static shared memory is padded to it
   uint8_t* sQ = ring + C::kRing;           // [2][QTILE]
@@ -324,15 +328,6 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     s_base = base;
   }
 
-  // rows without positions
-  for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
-    const Span s = span_of(a, m);
-    if (s.c0 != s.c1) continue;
-    uint4* o = reinterpret_cast<uint4*>(a.o + (size_t)m * a.n_q * HD);
-    for (int i = tid; i < a.n_q * HD / 8; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int i = tid; i < a.n_q; i += kThreads) a.lse[(size_t)m * a.n_q + i] = -INFINITY;
-  }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -456,7 +451,15 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     }
     __syncwarp();
   } else if (warp == kPV) {
-    // ---- P V: one thread issues
+    // ---- P V: one thread issues.  The warp writes the rows without positions first, while the others begin.
+    for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
+      const Span s = span_of(a, m);
+      if (s.c0 != s.c1) continue;
+      uint4* o = reinterpret_cast<uint4*>(a.o + (size_t)m * a.n_q * HD);
+      for (int i = lane; i < a.n_q * HD / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = lane; i < a.n_q; i += 32) a.lse[(size_t)m * a.n_q + i] = -INFINITY;
+    }
     if (lane == 0) {
       Waits wait{a.err, 48u, false};
       const uint32_t idesc =
