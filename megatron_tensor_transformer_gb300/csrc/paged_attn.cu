@@ -237,7 +237,8 @@ struct Waits {
   unsigned code;
   bool failed;
   __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) {
-    if (!tc::mbar_try_wait(bar, parity) && !failed) failed = wait_long(bar, parity, err, code);
+    if (!tc::mbar_try_wait(bar, parity) && !tc::mbar_try_wait(bar, parity) && !failed)
+      failed = wait_long(bar, parity, err, code);
   }
 };
 

@@ -10,6 +10,7 @@
 // whole pairs as two 16-byte vectors (dims 8i.. and rot/2 + 8i.. for the half layout, 16i.. and
 // 16i + 8.. for the interleaved one); the block is (hd / 16) x heads.  The cos and sin of a token
 // are computed once per CTA, into shared memory, and shared by its heads.
+#include "attn_mma.cuh"
 #include "common.cuh"
 #include "paged.h"
 #include "tc_ptx.cuh"
@@ -35,7 +36,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = (uint32_t)f2bf(x[2 * j]) | ((uint32_t)f2bf(x[2 * j + 1]) << 16);
+  for (int j = 0; j < 4; ++j) w[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // e4m3 codes of x / s, RNE satfinite (a NaN stays one)
