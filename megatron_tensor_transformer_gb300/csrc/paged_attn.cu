@@ -30,7 +30,7 @@
 // are added when tensor memory is read: an MMA costs the 128-row operand's way out of shared memory,
 // whatever N is, so a code more costs nothing and an MMA more does (62 cycles alone, 150 beside TMA's
 // writes; one MMA per code took 120.8 us for 131071 tokens of the 70B heads).
-// Warps: the softmax teams; a TMA producer (lane i looks up the page of box i and copies it: 16 to 128
+// Warps: the softmax teams; a TMA producer (lane i looks up the page of box i and copies it: 16 to 64
 // positions by 128 bytes); one issuing the scores' MMAs and one those of P V, each as soon as its operands are
 // there (one thread for both made every chunk wait for the one before: 107.1 us instead of 95.5 for 131071
 // tokens); one that walks the CTA's items (its part of a (request, kv head)) and brings their q.
@@ -69,6 +69,9 @@ struct PCfg {
   static constexpr int ROWB = HD * (FP8 ? 1 : 2);                 // bytes of a position
   static constexpr int INB = ROWB < 128 ? ROWB : 128;             // bytes of a box row
   static constexpr int NIB = ROWB / INB;                          // boxes side by side
+  // Positions of a TMA box at most (a page's, if it has fewer): what lies outside the positions attended to is not
+  // read beyond a box.  bf16 chunks of 32-position boxes came as fast as of 128, e4m3 ones only from 64 on.
+  static constexpr int BOX = FP8 ? 64 : 32;
   static constexpr int STAGE = kP * ROWB;                         // k or v of a chunk
   static constexpr int NB = HD == 256 ? 2 : 1;                    // 128-dim blocks of O^T
   static constexpr int KS = FP8 ? 32 : 16;                        // k of an MMA
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     // by stage: each is then waited for phase by phase by one role (with an odd NS a stage holds k and v in
     // turn, and the role that reads k would miss every other phase).
     Waits wait{a.err, 44u, false};
-    const int box_rows = min(1 << a.page_shift, kP), nbp = kP / box_rows;  // boxes along the positions
+    const int box_rows = min(1 << a.page_shift, C::BOX), nbp = kP / box_rows;  // boxes along the positions
     const int box = lane % nbp, side = lane / nbp;
     const uint64_t pol = tc::l2_evict_first();  // the cache streams through once
     // Page ids come 32 at a time, one per lane, the next 32 on their way (one chunk's at a time, a look-up
@@ -954,7 +957,7 @@ cudaError_t launch(const PagedAttnArgs& a, const void* k_pages, const void* v_pa
   for (int i = 0; i < 2; ++i) {  // the pages as rows of positions
     const cuuint64_t dims[2] = {(cuuint64_t)HD, (cuuint64_t)a.t * a.n_pages * (a.n_kv / a.t) * page};
     const cuuint64_t strides[1] = {(cuuint64_t)C::ROWB};
-    const cuuint32_t box[2] = {(cuuint32_t)(C::INB / (FP8 ? 1 : 2)), (cuuint32_t)std::min(page, kP)}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)(C::INB / (FP8 ? 1 : 2)), (cuuint32_t)std::min(page, C::BOX)}, es[2] = {1, 1};
     if (enc(&tm[i], FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             const_cast<void*>(i ? v_pages : k_pages), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             C::INB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
