@@ -393,7 +393,7 @@ typedef struct {
   int32_t rot_dim; /* a multiple of 16, 16 .. 256 */
   int32_t layout, scaling;
   int32_t original_len;                                 /* WAVELENGTH, YARN */
-  double theta, factor;                                 /* theta > 1; factor > 0 (not used by NONE) */
+  double theta, factor; /* theta > 1; factor > 0 and its reciprocal finite (not used by NONE) */
   double low_freq_factor, high_freq_factor;             /* WAVELENGTH: 0 < low < high */
   double beta_fast, beta_slow;                          /* YARN: both > 0 */
 } tp_rope_params;
@@ -416,8 +416,9 @@ tp_status tp_rope_describe(const tp_rope_params* params, tp_rope* rope);
  * tp_colpar_forward's QKV output) at positions[m] (int32, device, any value) into qkv_out in the same
  * order; v is copied.  qkv_out may be qkv itself (in place, v not touched); any other overlap is not
  * allowed.  fp32 products and sums, one rounding to bf16.  For the contiguous cache: the rotated qkv is
- * what tp_attn_decode takes.  head_dim a multiple of 16 up to 256 (TP_ERR_UNSUPPORTED otherwise),
- * rot_dim at most head_dim (TP_ERR_SHAPE).  One kernel launch.  M == 0 is a no-op. */
+ * what tp_attn_decode takes.  head_dim a multiple of 16 up to 256 and n_q + 2 n_kv below
+ * 2^16 (TP_ERR_UNSUPPORTED otherwise), rot_dim at most head_dim (TP_ERR_SHAPE).  One kernel launch.  M == 0 is a
+ * no-op. */
 tp_status tp_rope_forward(const tp_shape* shape /* host */, const tp_rope* rope /* host */, const void* qkv,
                           const int32_t* positions, int32_t M, void* qkv_out, void* stream);
 
@@ -442,7 +443,9 @@ tp_status tp_rope_append(const tp_shape* shape /* host */, const tp_rope* rope /
  * 1 / sqrt(hd).  fp32 scores, softmax and accumulation.  A request with lens[m] outside
  * [1, max_pages * page_size] gets a zero row and lse -inf.  Positions of a page whose id is outside
  * [0, n_pages) are left out as if masked; a row left without positions is zero with lse -inf.  Cache
- * rows outside the positions attended to never enter the result, whatever they hold.
+ * rows outside the positions attended to never enter the result, whatever they hold.  A score of -inf counts
+ * as masked; a NaN, and an infinite q or v that is used, gives NaN (an infinite q at the latest where a score
+ * of it is not -inf; over e4m3 pages always).
  * head_dim 64, 128 or 256, n_q / n_kv at most 16, t * n_pages * (n_kv / t) * page_size below 2^31
  * (TP_ERR_UNSUPPORTED otherwise); q, the pages, o_in and ws 16-byte aligned.
  * ws: tp_paged_attn_workspace_bytes(shape) bytes, whatever M and the lengths are; zero-filled once

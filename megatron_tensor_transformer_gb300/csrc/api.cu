@@ -193,8 +193,10 @@ tp_status check_pages(const tp_pages* p) {
   if ((int64_t)p->n_pages * ps >= (int64_t(1) << 31)) return TP_ERR_UNSUPPORTED;  // slots are int32
   return TP_OK;
 }
-tp_status check_rope(const tp_rope* r, int hd) {
+tp_status check_rope(const tp_rope* r, const tp_shape* sh) {
+  const int hd = sh->head_dim;
   if (hd % 16 || hd > 256) return TP_ERR_UNSUPPORTED;
+  if ((int64_t)sh->n_q_heads + 2LL * sh->n_kv_heads >= (1 << 16)) return TP_ERR_UNSUPPORTED;
   if (!r) return TP_OK;
   if (r->magic != TP_ROPE_MAGIC) return TP_ERR_LAYOUT_MISMATCH;
   if (r->layout != TP_ROPE_HALF && r->layout != TP_ROPE_INTERLEAVED) return TP_ERR_INVALID_ARG;
@@ -221,7 +223,7 @@ tp_status append_args(const tp_shape* sh, const tp_rope* rope, const tp_pages* p
                       const int32_t* positions, const int32_t* slots, int32_t M, void* q_out, void* k_pages,
                       void* v_pages, const float* k_scale, const float* v_scale, RopeArgs* out) {
   if (M < 0) return TP_ERR_INVALID_ARG;
-  const tp_status st = check_rope(rope, sh->head_dim);
+  const tp_status st = check_rope(rope, sh);
   if (st != TP_OK) return st;
   if (pages->kv_dtype == TP_BF16 && (k_scale || v_scale)) return TP_ERR_INVALID_ARG;
   if (M == 0) return TP_OK;
@@ -1117,7 +1119,7 @@ tp_status tp_rope_describe(const tp_rope_params* p, tp_rope* rope) {
   if (p->rot_dim < 16 || p->rot_dim > 256 || p->rot_dim % 16) return TP_ERR_SHAPE;
   auto positive = [](double v) { return v > 0.0 && std::isfinite(v); };
   if (!(p->theta > 1.0) || !std::isfinite(p->theta)) return TP_ERR_INVALID_ARG;
-  if (p->scaling != TP_ROPE_NONE && !positive(p->factor)) return TP_ERR_INVALID_ARG;
+  if (p->scaling != TP_ROPE_NONE && !(positive(p->factor) && std::isfinite(1.0 / p->factor))) return TP_ERR_INVALID_ARG;
   if (p->scaling >= TP_ROPE_WAVELENGTH && p->original_len <= 0) return TP_ERR_INVALID_ARG;
   if (p->scaling == TP_ROPE_WAVELENGTH &&
       !(positive(p->low_freq_factor) && positive(p->high_freq_factor) && p->low_freq_factor < p->high_freq_factor))
@@ -1160,7 +1162,7 @@ tp_status tp_rope_forward(const tp_shape* sh, const tp_rope* rope, const void* q
   tp_status st = check_shape(sh, TP_W_QKV);
   if (st != TP_OK) return st;
   if (!rope || M < 0) return TP_ERR_INVALID_ARG;
-  st = check_rope(rope, sh->head_dim);
+  st = check_rope(rope, sh);
   if (st != TP_OK) return st;
   if (M == 0) return TP_OK;
   if (!qkv || !positions || !qkv_out) return TP_ERR_INVALID_ARG;

@@ -13,9 +13,14 @@
 // lower id.  A value is a candidate only if it reaches the bar, the k-th largest of the maxima that 32 or 64 groups
 // of threads have seen so far: k values reach it, so no smaller one is among the k first.  The bar is
 // taken anew after 1, 6 and 32 rounds, before the round's own values are looked at; of random values
-// the 9 largest or so reach it for k = 8, the 31 largest for k = 20.  Each warp keeps its k best candidates, sorted across its
-// lanes, inserting one at a time; at the end those that reach the last bar are ranked against each other,
-// and the CTAs' k best in turn.  (Merging the warps' lists pairwise took longer than reading the row.)
+// the 9 largest or so reach it for k = 8, the 31 largest for k = 20.  Each warp keeps its k best
+// candidates, sorted across its lanes, inserting one at a time; at the end those that reach the last bar
+// are ranked against each other, and the CTAs' k best in turn.  (Merging the warps' lists pairwise cost
+// 32 rows 9 us, more than reading them.)
+//
+// Measured on one GB300, 128256 logits a row: 1900 rows 156 us without alternatives (92% of the measured
+// copy's 6792 GB/s), 182 with one, 218 with 20 (66%: instructions issue in 75% of the cycles); 32 rows 7.2
+// us without, 10.9 with 8.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -10,6 +10,9 @@
 // whole pairs as two 16-byte vectors (dims 8i.. and rot/2 + 8i.. for the half layout, 16i.. and
 // 16i + 8.. for the interleaved one); the block is (hd / 16) x heads.  The cos and sin of a token
 // are computed once per CTA, into shared memory, and shared by its heads.
+// Measured on one GB300: 8192 rows of 64 q and 8 kv heads of 128 into bf16 pages 61.5 us, 5.46 TB/s (a plain
+// copy of as many bytes 50.7 us, the append without turning 54.5); 1003 rows of 32 and 8 heads into e4m3 pages
+// 6.8 us; 32 rows of 64 and 8 heads 2.7 us.  Bound by HBM and, beside it, by the angles and the turning.
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "paged.h"
@@ -74,7 +77,7 @@ __global__ void __launch_bounds__(256, SINK == SINK_E4M3 ? 4 : 6) rope_kernel(co
   }
   __syncthreads();
   const int hd = a.hd, per = (a.n_q + 2 * a.n_kv) / a.t, nqs = a.n_q / a.t, nkvs = a.n_kv / a.t, all = per * a.t;
-  const unsigned per_inv = 0xffffffffu / per + 1;  // h / per as a high product (per is at least 3)
+  const unsigned per_inv = 0xffffffffu / per + 1;  // h / per as a high product: exact while all * per < 2^32
   const int i = threadIdx.x;
   const bool turned = 8 * i < half;
   // the thread's two vectors within the head
@@ -159,10 +162,11 @@ __global__ void __launch_bounds__(256, SINK == SINK_E4M3 ? 4 : 6) rope_kernel(co
 template <int SINK>
 cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
   const int tx = a.hd / 16, ty = 256 / tx, all = a.n_q + 2 * a.n_kv;
-  // Few tokens: one token and one pass of heads per CTA, to fill the SMs; many: kTok tokens, all heads.
+  // Few tokens: one token and one pass of heads per CTA, to fill the SMs; many: kTok tokens, all heads (with 1, 2 and
+  // 4 per CTA 8192 rows into bf16 pages took 63.6, 61.5 and 67.6 us, 1003 rows into e4m3 pages 7.5, 6.8 and 8.9).
   const bool many = (int64_t)a.M * ((all + ty - 1) / ty) > 4 * 152;
   const int toks = many ? kTok : 1, heads = many ? all : ty;
-  const cudaError_t e = launch_dependent(rope_kernel<SINK>, dim3((a.M + toks - 1) / toks, (all + heads - 1) / heads),
+  const cudaError_t e = launch_dependent(rope_kernel<SINK>, dim3(a.M / toks + (a.M % toks != 0), (all + heads - 1) / heads),
                                          dim3(tx, ty), 0, st, a, toks, heads);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -504,6 +504,50 @@ def test_paged_attention_infinite_scores(dev):
     assert not o[3].float().any() and torch.isneginf(lse[3]).all()
 
 
+@pytest.mark.parametrize("kv", [tpx.TP_BF16, tpx.TP_FP8_E4M3])
+def test_paged_attention_infinite_q(dev, kv):
+    """An infinity in q makes its head's row NaN over pages of either type, and no other row another one."""
+    c = Case(dev, 2, 8, 4, 128, 32, [200, 77, 1500], kv, seed=21)
+    want, want_l = c.launch()
+    c.q[0, 5 * 128 + 3] = float("inf")
+    c.q[2, 1 * 128 + 100] = float("-inf")
+    o, lse = c.launch()
+    hit = torch.zeros((3, 8), dtype=torch.bool, device=dev)
+    hit[0, 5] = hit[2, 1] = True
+    o, want = o.view(3, 8, 128), want.view(3, 8, 128)
+    assert torch.isnan(o[hit].float()).all() and torch.isfinite(want.float()).all()
+    assert torch.equal(o[~hit].view(torch.int16), want[~hit].view(torch.int16))
+    assert torch.equal(lse[~hit], want_l[~hit]) and not torch.isfinite(lse[hit]).any()
+
+
+@pytest.mark.parametrize("kv", [tpx.TP_BF16, tpx.TP_FP8_E4M3])
+def test_paged_attention_requests_that_share_pages(dev, kv):
+    """Requests with a common beginning name the same pages, one of them a page twice."""
+    c = Case(dev, 1, 8, 2, 64, 16, [400, 333, 96, 400], kv, seed=22, poison=False)
+    c.table[1, :20] = c.table[0, :20]
+    c.table[2, :6] = c.table[0, :6]
+    c.table[3, 7:9] = c.table[3, 3]
+    c.check()
+    c.check(window=90)
+
+
+def test_two_attention_calls_at_once(dev):
+    """Calls on two streams with a workspace each, over the same pages and in any overlap, give the bits of
+    calls one after the other."""
+    a = Case(dev, 1, 32, 8, 128, 64, [9000, 1, 777], seed=23)
+    b = Case(dev, 1, 8, 4, 256, 16, [50, 0, 3100, 640, 12], seed=24)
+    want = [x.launch()[0].clone() for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(w) for _ in range(20)] for w in want]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for x, s, o in zip((a, b), streams, outs):
+            x.call(o[i], None, stream=s)
+    sync()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w.view(torch.int16), y.view(torch.int16)) for y in o)
+
+
 def test_paged_attention_and_append_past_4_gib(dev):
     """Pages whose byte offsets pass 32 bits (a pool of 5 GiB per side)."""
     n_kv, hd, page, n_pages = 8, 128, 256, 10400

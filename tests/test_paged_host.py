@@ -80,6 +80,7 @@ def test_rope_refusals():
     assert status(layout=2) == status(scaling=4) == status(theta=1.0) == status(theta=math.inf) == E
     assert status(scaling=tpx.TP_ROPE_LINEAR, factor=0.0) == E
     assert status(scaling=tpx.TP_ROPE_LINEAR, factor=math.nan) == E
+    assert status(scaling=tpx.TP_ROPE_LINEAR, factor=5e-324) == E                     # 1 / factor is infinite
     assert status(scaling=tpx.TP_ROPE_WAVELENGTH, factor=8.0) == E                   # no original length
     assert status(scaling=tpx.TP_ROPE_WAVELENGTH, factor=8.0, original_len=4096, low_freq_factor=4.0) == E
     assert status(scaling=tpx.TP_ROPE_YARN, factor=8.0, original_len=4096, beta_fast=0.0) == E
@@ -91,6 +92,7 @@ def test_rope_refusals():
     assert append(sh=tpx.make_shape(1024, n_q=8, n_kv=4, hd=72, t=2), rope=rope) == tpx.TP_ERR_UNSUPPORTED
     assert append(sh=tpx.make_shape(1024, n_q=8, n_kv=4, hd=512, t=2), rope=rope) == tpx.TP_ERR_UNSUPPORTED
     assert append(sh=tpx.make_shape(1024, n_q=8, n_kv=2, hd=128, t=4), rope=rope) == tpx.TP_ERR_SHAPE
+    assert append(sh=tpx.make_shape(1024, n_q=65536, n_kv=4, hd=128, t=2), rope=rope) == tpx.TP_ERR_UNSUPPORTED
     for kw in (dict(qkv=None), dict(pos=None), dict(slots=None), dict(q=None), dict(k=None), dict(v=None), dict(M=-1),
                dict(ks=FAKE), dict(vs=FAKE), dict(q=FAKE), dict(q=ctypes.c_void_p((1 << 20) + 4 * 2048 * 2 - 16))):
         assert append(rope=rope, **kw) == E, kw
