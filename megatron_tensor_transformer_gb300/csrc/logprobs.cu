@@ -334,9 +334,12 @@ cudaError_t launch(const LogprobsArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobsArgs& a, cudaStream_t st) {
-  // CTAs per row: two per SM over all rows, while each still has 4 vectors per thread
+  // CTAs per row: two if that is at most one per SM over all rows, four and eight up to 256 in all, while each
+  // still has 4 vectors per thread.  With 1, 2, 4, 8 CTAs and 8 alternatives of 128256 logits, 32 rows take 21.0,
+  // 16.2, 11.5, 10.8 us, 64 rows 21.9, 16.9, 15.7, 20.8, 76 rows 22.2, 17.1, 22.5, 27.7, 128 rows 22.4, 23.9, 29.3,
+  // 39.4: a second CTA on some SMs takes them nearly as long again.
   int c = 1;
-  while (c < kMaxC && (int64_t)a.M * c < 152 * 2 && a.vocab / (2 * c) >= 4 * 4 * kNT) c *= 2;
+  while (c < kMaxC && (int64_t)a.M * 2 * c <= (c == 1 ? 152 : 256) && a.vocab / (2 * c) >= 4 * 4 * kNT) c *= 2;
   return c == 1 ? launch<1>(a, st) : c == 2 ? launch<2>(a, st) : c == 4 ? launch<4>(a, st) : launch<8>(a, st);
 }
 
