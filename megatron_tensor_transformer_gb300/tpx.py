@@ -148,15 +148,20 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = _device = None
+
+
 def _stream(stream):
+    global _raw_stream, _device
     if stream is not None:
         return stream.cuda_stream
-    if not torch.cuda.is_initialized():
+    if _raw_stream is None:
         if not torch.cuda.is_available():
             return None
         torch.cuda.init()
+        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     # the current stream's handle, without a Stream object: a decode step makes many short calls
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw_stream(_device())
 
 
 def make_shape(d, ffn=0, n_q=0, n_kv=0, hd=0, t=1, wtype=TP_BF16, vocab=0):
