@@ -10,9 +10,11 @@
 // whole pairs as two 16-byte vectors (dims 8i.. and rot/2 + 8i.. for the half layout, 16i.. and
 // 16i + 8.. for the interleaved one); the block is (hd / 16) x heads.  The cos and sin of a token
 // are computed once per CTA, into shared memory, and shared by its heads.
-// Measured on one GB300: 8192 rows of 64 q and 8 kv heads of 128 into bf16 pages 61.5 us, 5.46 TB/s (a plain
-// copy of as many bytes 50.7 us, the append without turning 54.5); 1003 rows of 32 and 8 heads into e4m3 pages
-// 6.8 us; 32 rows of 64 and 8 heads 2.7 us.  Bound by HBM and, beside it, by the angles and the turning.
+// The heads of both tokens of a CTA are dealt to its threads at once (token by token, 80 heads took
+// three passes of 32, the last one half empty: 61.5 us).
+// Measured on one GB300: 8192 rows of 64 q and 8 kv heads of 128 into bf16 pages 56.5 us, 5.94 TB/s (a plain
+// copy of as many bytes 50.0 us, the append without turning 52.9); 1003 rows of 32 and 8 heads into e4m3 pages
+// 6.2 us; 32 rows of 64 and 8 heads 2.6 us.  Bound by HBM and, beside it, by the angles and the turning.
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "paged.h"
@@ -83,77 +85,79 @@ __global__ void __launch_bounds__(256, SINK == SINK_E4M3 ? 4 : 6) rope_kernel(co
   // the thread's two vectors within the head
   const bool split = turned && a.rope.layout == TP_ROPE_HALF;
   const int d0 = split ? 8 * i : 16 * i, d1 = split ? half + 8 * i : 16 * i + 8;
-  const int h1 = min(all, (int)(blockIdx.y + 1) * heads);
-  for (int k = 0; k < nt; ++k) {
-    const int m = m0 + k;
+  const int h0 = blockIdx.y * heads, nh = min(all - h0, heads);
+  int slots[kTok] = {};
+  if (SINK != SINK_QKV)
+    for (int k = 0; k < nt; ++k) slots[k] = a.slots[m0 + k];
+  for (int e = threadIdx.y; e < nt * nh; e += blockDim.y) {
+    static_assert(kTok == 2, "k is 0 or 1");
+    const int k = e >= nh, h = h0 + e - (k ? nh : 0), m = m0 + k;
     const __nv_bfloat16* row = a.qkv + (size_t)m * all * hd;
     int slot = 0;
     bool kept = true;
     if (SINK != SINK_QKV) {
-      slot = a.slots[m];
+      slot = k ? slots[1] : slots[0];
       kept = slot >= 0 && (slot >> a.page_shift) < a.n_pages;
     }
-    for (int h = blockIdx.y * heads + threadIdx.y; h < h1; h += blockDim.y) {
-      const int sh = (int)__umulhi((unsigned)h, per_inv), l = h - sh * per;
-      const bool is_q = l < nqs, is_v = l >= nqs + nkvs;
-      if (SINK == SINK_QKV && is_v && a.q_out == a.qkv) continue;  // in place
-      if (SINK != SINK_QKV && !is_q && !kept) continue;
-      const uint4 u0 = *reinterpret_cast<const uint4*>(row + (size_t)h * hd + d0);
-      const uint4 u1 = *reinterpret_cast<const uint4*>(row + (size_t)h * hd + d1);
-      float x[8], y[8];
-      uint4 o0 = u0, o1 = u1;
-      const bool turn_it = turned && !is_v;
-      unpack8(u0, x);
-      unpack8(u1, y);
-      if (turn_it) {
-        float c[8], s[8];
+    const int sh = (int)__umulhi((unsigned)h, per_inv), l = h - sh * per;
+    const bool is_q = l < nqs, is_v = l >= nqs + nkvs;
+    if (SINK == SINK_QKV && is_v && a.q_out == a.qkv) continue;  // in place
+    if (SINK != SINK_QKV && !is_q && !kept) continue;
+    const uint4 u0 = *reinterpret_cast<const uint4*>(row + (size_t)h * hd + d0);
+    const uint4 u1 = *reinterpret_cast<const uint4*>(row + (size_t)h * hd + d1);
+    float x[8], y[8];
+    uint4 o0 = u0, o1 = u1;
+    const bool turn_it = turned && !is_v;
+    unpack8(u0, x);
+    unpack8(u1, y);
+    if (turn_it) {
+      float c[8], s[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 cv = *reinterpret_cast<const float4*>(&cs[k][0][8 * i + 4 * j]);
-          const float4 sv = *reinterpret_cast<const float4*>(&cs[k][1][8 * i + 4 * j]);
-          c[4 * j] = cv.x, c[4 * j + 1] = cv.y, c[4 * j + 2] = cv.z, c[4 * j + 3] = cv.w;
-          s[4 * j] = sv.x, s[4 * j + 1] = sv.y, s[4 * j + 2] = sv.z, s[4 * j + 3] = sv.w;
-        }
-        if (split) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float p = x[j], q = y[j];
-            x[j] = p * c[j] - q * s[j];
-            y[j] = q * c[j] + p * s[j];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p = x[2 * j], q = x[2 * j + 1], u = y[2 * j], v = y[2 * j + 1];
-            x[2 * j] = p * c[j] - q * s[j];
-            x[2 * j + 1] = q * c[j] + p * s[j];
-            y[2 * j] = u * c[4 + j] - v * s[4 + j];
-            y[2 * j + 1] = v * c[4 + j] + u * s[4 + j];
-          }
-        }
-        o0 = pack8(x);
-        o1 = pack8(y);
+      for (int j = 0; j < 2; ++j) {
+        const float4 cv = *reinterpret_cast<const float4*>(&cs[k][0][8 * i + 4 * j]);
+        const float4 sv = *reinterpret_cast<const float4*>(&cs[k][1][8 * i + 4 * j]);
+        c[4 * j] = cv.x, c[4 * j + 1] = cv.y, c[4 * j + 2] = cv.z, c[4 * j + 3] = cv.w;
+        s[4 * j] = sv.x, s[4 * j + 1] = sv.y, s[4 * j + 2] = sv.z, s[4 * j + 3] = sv.w;
       }
-      if (SINK == SINK_QKV || is_q) {
-        __nv_bfloat16* out = SINK == SINK_QKV ? a.q_out + ((size_t)m * all + h) * hd
-                                              : a.q_out + ((size_t)m * a.n_q + sh * nqs + l) * hd;
+      if (split) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float p = x[j], q = y[j];
+          x[j] = p * c[j] - q * s[j];
+          y[j] = q * c[j] + p * s[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = x[2 * j], q = x[2 * j + 1], u = y[2 * j], v = y[2 * j + 1];
+          x[2 * j] = p * c[j] - q * s[j];
+          x[2 * j + 1] = q * c[j] + p * s[j];
+          y[2 * j] = u * c[4 + j] - v * s[4 + j];
+          y[2 * j + 1] = v * c[4 + j] + u * s[4 + j];
+        }
+      }
+      o0 = pack8(x);
+      o1 = pack8(y);
+    }
+    if (SINK == SINK_QKV || is_q) {
+      __nv_bfloat16* out = SINK == SINK_QKV ? a.q_out + ((size_t)m * all + h) * hd
+                                            : a.q_out + ((size_t)m * a.n_q + sh * nqs + l) * hd;
+      *reinterpret_cast<uint4*>(out + d0) = o0;
+      *reinterpret_cast<uint4*>(out + d1) = o1;
+    } else {
+      const int g = is_v ? l - nqs - nkvs : l - nqs;  // kv head within the shard
+      const size_t page = (size_t)sh * a.n_pages + (slot >> a.page_shift);
+      const size_t at = (((page * nkvs + g) << a.page_shift) + (slot & ((1 << a.page_shift) - 1))) * hd;
+      if (SINK == SINK_BF16) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_v ? a.v_pages : a.k_pages) + at;
         *reinterpret_cast<uint4*>(out + d0) = o0;
         *reinterpret_cast<uint4*>(out + d1) = o1;
       } else {
-        const int g = is_v ? l - nqs - nkvs : l - nqs;  // kv head within the shard
-        const size_t page = (size_t)sh * a.n_pages + (slot >> a.page_shift);
-        const size_t at = (((page * nkvs + g) << a.page_shift) + (slot & ((1 << a.page_shift) - 1))) * hd;
-        if (SINK == SINK_BF16) {
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_v ? a.v_pages : a.k_pages) + at;
-          *reinterpret_cast<uint4*>(out + d0) = o0;
-          *reinterpret_cast<uint4*>(out + d1) = o1;
-        } else {
-          const float* scale = is_v ? a.v_scale : a.k_scale;
-          const float sc = scale ? scale[sh * nkvs + g] : 1.0f;
-          uint8_t* out = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + at;
-          *reinterpret_cast<uint2*>(out + d0) = codes8(x, sc);
-          *reinterpret_cast<uint2*>(out + d1) = codes8(y, sc);
-        }
+        const float* scale = is_v ? a.v_scale : a.k_scale;
+        const float sc = scale ? scale[sh * nkvs + g] : 1.0f;
+        uint8_t* out = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + at;
+        *reinterpret_cast<uint2*>(out + d0) = codes8(x, sc);
+        *reinterpret_cast<uint2*>(out + d1) = codes8(y, sc);
       }
     }
   }
@@ -162,8 +166,9 @@ __global__ void __launch_bounds__(256, SINK == SINK_E4M3 ? 4 : 6) rope_kernel(co
 template <int SINK>
 cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
   const int tx = a.hd / 16, ty = 256 / tx, all = a.n_q + 2 * a.n_kv;
-  // Few tokens: one token and one pass of heads per CTA, to fill the SMs; many: kTok tokens, all heads (with 1, 2 and
-  // 4 per CTA 8192 rows into bf16 pages took 63.6, 61.5 and 67.6 us, 1003 rows into e4m3 pages 7.5, 6.8 and 8.9).
+  // Few tokens: one token and one pass of heads per CTA, to fill the SMs; many: kTok tokens, all heads (with 1 and
+  // 2 per CTA 8192 rows into bf16 pages took 59.5 and 56.5 us, 1003 rows into e4m3 pages 7.3 and 6.2; 3 and 4,
+  // which take a division per head, 57.7 and 61.6, 8.1 and 6.8).
   const bool many = (int64_t)a.M * ((all + ty - 1) / ty) > 4 * 152;
   const int toks = many ? kTok : 1, heads = many ? all : ty;
   const cudaError_t e = launch_dependent(rope_kernel<SINK>, dim3(a.M / toks + (a.M % toks != 0), (all + heads - 1) / heads),
