@@ -278,6 +278,34 @@ def test_rope_append(dev, kv, layout, scaling, hd, rot, n_q, n_kv, t, page, M):
         assert np.array_equal(got[~touched], old[~touched])           # the rest of the pool
 
 
+@pytest.mark.parametrize("kv", [tpx.TP_BF16, tpx.TP_FP8_E4M3])
+@pytest.mark.parametrize("M,hd,rot,n_q,n_kv,t,layout", [(1303, 128, 128, 64, 8, 8, "half"), (701, 64, 32, 12, 4, 2, "half"),
+                                                        (612, 256, 256, 3, 1, 1, "interleaved"),
+                                                        (905, 16, 16, 300, 4, 4, "interleaved")])
+def test_rope_many_rows_equal_few(dev, kv, M, hd, rot, n_q, n_kv, t, layout):
+    """A call of many rows (two to a CTA, odd numbers of rows and heads too) gives the bits of calls of few."""
+    pos, rope, _, _ = rope_case(M, hd, rot, layout, "yarn", M)
+    sh = tpx.make_shape(1024, n_q=n_q, n_kv=n_kv, hd=hd, t=t)
+    n_pages = M // 32 + 2
+    pages = tpx.make_pages(32, n_pages, 4, kv)
+    slots = np.random.default_rng(M).permutation(n_pages * 32)[:M]
+    slots[[5, M - 1]] = -1
+    qkv, pos, slots = make_qkv(dev, M, n_q, n_kv, hd, 13), i32(pos, dev), i32(slots, dev)
+    ks, vs = scales(dev, n_kv, kv, 3)
+    outs = []
+    for step in (M, 3):
+        kp, vp = (pool(dev, t, n_pages, n_kv, 32, hd, kv, 3, s) for s in (91, 92))
+        q = torch.zeros((M, n_q * hd), dtype=torch.bfloat16, device=dev)
+        turned = torch.zeros_like(qkv)
+        for m in range(0, M, step):
+            rows = slice(m, min(M, m + step))
+            tpx.tp_rope_append(sh, rope, pages, qkv[rows], pos[rows].clone(), slots[rows].clone(), q[rows], kp, vp, ks, vs)
+            tpx.tp_rope_forward(sh, rope, qkv[rows], pos[rows].clone(), turned[rows])
+        sync()
+        outs.append([x.view(torch.uint8) for x in (q, kp, vp, turned)])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 def test_append_codes_exactly_without_turning(dev):
     """rope None: bf16 pages hold the bits, e4m3 pages the nearest codes; overflow saturates, NaN stays."""
     M, n_q, n_kv, hd, page = 5, 4, 2, 64, 16
