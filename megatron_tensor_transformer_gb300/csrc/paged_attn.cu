@@ -47,7 +47,8 @@
 //   1 request of 519 tokens, 32 q and 8 kv heads, pages of 16                         9.9 us (latency)
 // What is left: about 3 us before the first products (launch, the lengths' sum, the page look-up, the first
 // copies) and 2.5 us of counting in and joining; the ends of short requests and the SMs' unequal shares of the
-// HBM; and over e4m3 with 16 heads per kv head the softmax itself, 1 us a chunk of 32 KB.
+// HBM; and over e4m3 each (request, kv head)'s beginning and end, 2.4 us beside 0.7 us a chunk, with 16 heads
+// per kv head 4.4 beside 0.78 (0.74 at the copy's rate).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -262,9 +263,11 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
                       const __grid_constant__ PagedAttnArgs a) {
   using C = PCfg<HD, FP8>;
   constexpr int kTeam = NG * 128, kSoftWarps = 2 * NG * 4, kThreads = 2 * kTeam + 128, kWarps = kThreads / 32;
-  // A chunk is two units of work.  The beginning and end of a (request, kv head) come to about 0.7 us for bf16,
-  // half a chunk of 64 KB at an SM's share of the HBM, and 2 and 3 us for e4m3 with 4 and 8 heads a thread.
-  constexpr int kEnds = FP8 ? (HPT == 8 ? 8 : 6) : C::STAGE >= 32 * 1024 ? 1 : 4;
+  // A chunk is two units of work, the beginning and end of a (request, kv head) kEnds.  bf16, 128 dims, with 1, 2, 3
+  // and 4: 32 requests up to 4096 take 52.9, 53.1, 53.3 and 54.3 us, 100 up to 2000 74.9, 68.3, 68.6 and 69.2, 256
+  // up to 700 91.6, 88.1, 84.6 and 84.4; 256 dims: 256 up to 700 63.7, 63.8, 64.8 and 66.3.  e4m3, 8 heads a thread,
+  // with 8, 10 and 12: 48 up to 8192 79.7, 80.7 and 82.0, 100 up to 2000 80.9, 78.5 and 77.9.
+  constexpr int kEnds = FP8 ? (HPT == 8 ? 8 : 6) : C::STAGE >= 64 * 1024 ? 1 : C::STAGE >= 32 * 1024 ? 3 : 4;
   constexpr int kProducer = kSoftWarps, kScores = kProducer + 1, kItems = kProducer + 2, kPV = kProducer + 3;
   extern __shared__ __align__(1024) uint8_t ring[];  // the swizzles' atoms; static shared memory is padded to it
   uint8_t* sQ = ring + C::kRing;           // [2][QTILE]
