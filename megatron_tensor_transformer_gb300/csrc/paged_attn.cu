@@ -40,10 +40,10 @@
 // joining 19 pieces took 10 us).  Every sum's order follows from the lengths and the SM count: runs repeat
 // bit for bit.
 // Measured on one GB300 (GPU time of a call among others, fractions of the measured copy's 6792 GB/s):
-//   1 request of 131071 tokens, 64 q and 8 kv heads of 128, bf16, pages of 64        86.5 us, 91%
-//   32 ragged requests up to 4096, the same heads, pages of 16                       52.7 us, 81%
+//   1 request of 131071 tokens, 64 q and 8 kv heads of 128, bf16, pages of 64        87.7 us, 90%
+//   32 ragged requests up to 4096, the same heads, pages of 16                       53.1 us, 80%
 //   48 ragged requests up to 8192, 128 q and 8 kv heads, e4m3, pages of 32           79.9 us, 67%
-//   61 ragged requests, a window of 1024, 8 q and 4 kv heads of 256, pages of 128    42.2 us, 80%
+//   61 ragged requests, a window of 1024, 8 q and 4 kv heads of 256, pages of 128    43.1 us, 78%
 //   1 request of 519 tokens, 32 q and 8 kv heads, pages of 16                         9.9 us (latency)
 // What is left: about 3 us before the first products (launch, the lengths' sum, the page look-up, the first
 // copies) and 2.5 us of counting in and joining; the ends of short requests and the SMs' unequal shares of the
