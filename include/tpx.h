@@ -475,8 +475,10 @@ tp_status tp_lm_head_forward(const tp_packed_desc* desc /* host */, const void* 
  * The weights and flags as for tp_attn_block_forward, the other arguments as for the calls named;
  * the same bits as these calls.  qkv_out [M, (n_q + 2 n_kv) hd], q_out and o_in [M, n_q hd]: the caller's
  * bf16 buffers, which overlap neither one another nor y; y must not alias x or residual.
- * ws: tp_paged_attn_block_workspace_bytes(shape, M, flags) bytes, zero-filled once before first use.  Errors as for the calls, all checked before the first
- * launch.  M == 0 is a no-op. */
+ * ws: tp_paged_attn_block_workspace_bytes(shape, M, flags) bytes, zero-filled once before first use (and after a
+ * TP_ERR_DEVICE_TIMEOUT).  One that is large enough serves calls of every M in any order, and between them the
+ * shape's calls that take a workspace of tp_workspace_bytes; not tp_paged_attn_decode, whose counters lie at its front.
+ * Errors as for the calls, all checked before the first launch.  M == 0 is a no-op. */
 size_t tp_paged_attn_block_workspace_bytes(const tp_shape* shape /* host */, int32_t M, uint32_t flags);
 tp_status tp_paged_attn_block_forward(const tp_packed_desc* qkv /* host */, const void* qkv_w,
                                       const tp_packed_desc* o /* host */, const void* o_w, const void* x,

@@ -1204,6 +1204,8 @@ tp_status tp_paged_attn_decode(const tp_shape* sh, const tp_pages* pages, const 
   return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
 }
 
+// Workspace of the block: [projections][paged attention].  The attention's part begins where M and the flags end the
+// projections', so a call of another M may have left anything there: the append of the same call zeroes its counters.
 size_t tp_paged_attn_block_workspace_bytes(const tp_shape* sh, int32_t M, uint32_t flags) {
   if (!sh || M < 0) return 0;
   const size_t proj = tp_workspace_bytes(sh, M, flags), attn = tp_paged_attn_workspace_bytes(sh);
@@ -1238,6 +1240,7 @@ tp_status tp_paged_attn_block_forward(const tp_packed_desc* qkv, const void* qkv
     st = attn_args(&sh, pages, q_out, k_pages, v_pages, k_scale, v_scale, block_table, lens, M, 0.f, window, o_in,
                    nullptr, static_cast<uint8_t*>(ws) + proj, ws_bytes - proj, &aa);
   if (st != TP_OK || M == 0) return st;
+  ra.counters = aa.ws;
   cudaStream_t s = S(stream);
   st = run_colpar(qkv, qkv_w, static_cast<const bf16*>(x), M, qkv_out, COLPAR_BF16, s, flags, ws, proj);
   if (st == TP_OK) st = cuda_status(launch_rope_append(ra, pages->kv_dtype, s));

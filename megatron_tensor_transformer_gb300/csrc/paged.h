@@ -26,6 +26,7 @@ struct RopeArgs {
   void *k_pages, *v_pages;
   int32_t M, t, n_q, n_kv, hd;
   int32_t page_shift, n_pages;
+  unsigned* counters;  // launch_rope_append: the attention workspace's, to be zeroed, or nullptr
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
 cudaError_t launch_rope_append(const RopeArgs& a, int kv_dtype, cudaStream_t st);
@@ -44,6 +45,8 @@ struct PagedAttnArgs {
 };
 // the largest grid
 constexpr int kPagedMaxCtas = 256;
+// counter words at the front of the workspace, zero between calls
+constexpr int kPagedCounters = 4 * kPagedMaxCtas;
 size_t paged_attn_workspace_bytes(int G, int hd);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,
                               cudaStream_t st);

@@ -73,7 +73,8 @@ constexpr int kN = 16;                     // heads of an MMA (its columns)
 constexpr int kMasks = 32;                 // ring of the chunks' masks: above the chunks in flight
 constexpr int kFan = 5;                    // pieces joined at once (131071 tokens: 87.4 us with 5, 89.2 with 8, 90.0 with 24)
 constexpr int kSlots = 2 * kPagedMaxCtas;  // pieces: a split (request, kv head) is a CTA's first item or its last
-constexpr int kWsHead = 2 * kSlots;        // counters: by the slot of the first of kFan pieces, then of the first of all
+constexpr int kWsHead = kPagedCounters;    // counters: by the slot of the first of kFan pieces, then of the first of all
+static_assert(kWsHead == 2 * kSlots, "two counters per slot");
 
 template <int HD, bool FP8>
 struct PCfg {

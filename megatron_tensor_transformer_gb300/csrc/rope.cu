@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(256, SINK == SINK_E4M3 ? 4 : 6) rope_kernel(co
   tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
   const int m0 = blockIdx.x * toks, nt = min(toks, a.M - m0), half = a.rope.rot_dim / 2;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
+  if (SINK != SINK_QKV && a.counters && blockIdx.x == 0 && blockIdx.y == 0)
+    for (int j = tid; j < kPagedCounters; j += nthr) a.counters[j] = 0u;
   for (int j = tid; j < nt * half; j += nthr) {
     const int k = j / half, i = j % half;
     const uint64_t turn = (uint64_t)(int64_t)a.positions[m0 + k] * a.rope.step[i];

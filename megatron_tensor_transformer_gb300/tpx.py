@@ -413,7 +413,7 @@ def tp_paged_attn_block_workspace_bytes(shape, M, flags=0):
 
 
 def new_paged_attn_block_workspace(shape, M, device, flags=0):
-    """Zero-filled workspace of tp_paged_attn_block_forward (its counters start at zero)."""
+    """Zero-filled workspace of tp_paged_attn_block_forward, for calls of up to M rows in any order."""
     return torch.zeros(max(1, tp_paged_attn_block_workspace_bytes(shape, M, flags)), dtype=torch.uint8, device=device)
 
 

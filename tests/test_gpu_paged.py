@@ -753,3 +753,44 @@ def test_paged_attention_block_decode_steps(dev, wtype, kv, M):
     tpx.tp_token_logprobs(logits, logits.argmax(1).to(torch.int32), lp, ent, rank, tl, ti)
     sync()
     assert (rank == 1).all() and torch.equal(lp, tl[:, 0]) and torch.equal(ti[:, 0].long(), logits.argmax(1))
+
+
+@pytest.mark.parametrize("wtype,kv", [(tpx.TP_BF16, tpx.TP_BF16), (tpx.TP_FP8_E4M3, tpx.TP_FP8_E4M3)])
+def test_paged_attention_block_shares_a_workspace_over_m(dev, wtype, kv):
+    """One workspace of the largest M, zero-filled once, serves steps of any M in any order, with the shape's other
+    calls between them: the bits of the four calls, whose attention has a workspace of its own.  The requests are
+    long enough to be split over CTAs, so each step counts pieces."""
+    d, n_q, n_kv, hd, t, page, L = 1024, 8, 4, 128, 2, 16, 2600
+    big = 70
+    _, wqkv, wo = inputs.proj_inputs(d, n_q, n_kv, hd, 1, seed=15, device=dev)
+    sh = tpx.make_shape(d, n_q=n_q, n_kv=n_kv, hd=hd, t=t, wtype=wtype)
+    q_w, qd = tpx.tp_partition_weights(sh, tpx.TP_W_QKV, wqkv)
+    o_w, od = tpx.tp_partition_weights(sh, tpx.TP_W_O, wo)
+    held = L // page + 1
+    n_pages = 3 * held
+    pages, rope = tpx.make_pages(page, n_pages, held, kv), tpx.make_rope(hd, 500000.0)
+    ks, vs = scales(dev, n_kv, kv, 15)
+    cache = [pool(dev, t, n_pages, n_kv, page, hd, kv, 15, s) for s in (101, 102)]
+    order = np.random.default_rng(15).permutation(n_pages).reshape(3, held)
+    table = i32([order[m % 3] for m in range(big)], dev)                # requests share pages; none is appended to
+    slots = i32([-1] * big, dev)
+    lens = i32([L - 37 * m if m % 5 else 0 for m in range(1, big + 1)], dev)
+    pos = lens - 1
+    xs = inputs.normal_bf16((big, d), 1.0, 16, 99, dev)
+    ws, ws2 = tpx.new_paged_attn_block_workspace(sh, big, dev), tpx.new_workspace(sh, big, dev)
+    aws = tpx.new_paged_attn_workspace(sh, dev)
+    b16 = lambda *s: torch.full(s, float("nan"), dtype=torch.bfloat16, device=dev)
+    for M in (70, 32, 31, 1, 8, 64, 4, 5, 1, 33, 70, 2):
+        a, b = [dict(y=b16(M, d), qkv=b16(M, (n_q + 2 * n_kv) * hd), q=b16(M, n_q * hd), o=b16(M, n_q * hd))
+                for _ in range(2)]
+        x = xs[:M]
+        tpx.tp_paged_attn_block_forward(qd, q_w, od, o_w, x, x, rope, pages, pos, slots, *cache, table, lens, a["y"],
+                                        a["qkv"], a["q"], a["o"], ws, k_scale=ks, v_scale=vs)
+        tpx.tp_colpar_forward(qd, q_w, x, b["qkv"], ws=ws2)
+        tpx.tp_rope_append(sh, rope, pages, b["qkv"], pos, slots, b["q"], *cache, ks, vs)
+        tpx.tp_paged_attn_decode(sh, pages, b["q"], *cache, table, lens, b["o"], aws, k_scale=ks, v_scale=vs)
+        tpx.tp_rowpar_forward(od, o_w, b["o"], x, b["y"], ws2)
+        sync()
+        for key in a:
+            assert torch.equal(a[key].view(torch.int16), b[key].view(torch.int16)), (M, key)
+        tpx.tp_rowpar_forward(od, o_w, xs[:, :n_q * hd].contiguous(), None, b16(big, d), ws)  # scratch over the counters
