@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(NT) tables_kernel(const TablesArgs a) {
   __shared__ long long part[NT / 32];
   __shared__ int mark[NT], wmax[NT / 32];
   __shared__ int s_m[NT], s_len[NT];
-  __shared__ long long s_first[NT], s_base[NT];  // the request's first row; its first page in the free list, -1: refused
+  __shared__ long long s_first[NT], s_base[NT];  // the request's first row; its first page in the free list
+  __shared__ bool s_in[NT];                      // whether it is served (it may be without pages left: s_base is then unused)
   tc::griddep_wait();
   tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -126,7 +127,8 @@ __global__ void __launch_bounds__(NT) tables_kernel(const TablesArgs a) {
           s_m[i] = m;
           s_len[i] = r.len;
           s_first[i] = first;
-          s_base[i] = r.ok && (r.need == 0 || need + r.need <= left) ? head + need : -1;
+          s_base[i] = head + need;
+          s_in[i] = r.ok && (r.need == 0 || need + r.need <= left);
         }
         need += r.need;
         first += r.rows;
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(NT) tables_kernel(const TablesArgs a) {
         const int m = s_m[i], len = s_len[i];
         const long long base = s_base[i];
         pos = (int)((unsigned)len + (unsigned)(row - s_first[i]));
-        if (base >= 0) {
+        if (s_in[i]) {
           const int pg = pos >> a.page_shift, fresh = pg - (int)(((long long)len + pmask) >> a.page_shift);
           int* entry = a.table + (size_t)m * a.table_stride + pg;
           const int id = fresh >= 0 ? a.free_pages[base + fresh] : *entry;

@@ -103,6 +103,16 @@ def test_tables_refusals_on_the_device(dev):
     run_tables(dev, [3, 3], [40, 40], 16, 8, 9, bad=[(1, -5), (3, 10 ** 6)])   # the list names no page
 
 
+@pytest.mark.parametrize("head", [-1, -(2 ** 31), 4, 2 ** 31 - 1])
+def test_tables_growth_within_a_page_with_no_page_left(dev, head):
+    """With *head outside the free list no page is left, but a request that grows within a page it holds needs none:
+    it is served and its rows have slots, whatever refused requests are before it."""
+    w = run_tables(dev, [5], [1], 16, 8, 3, head=head)
+    assert w[1].tolist() == [6] and w[4][0] >= 0 and w[5].tolist() == [head, 1, 0]
+    w = run_tables(dev, [5, 16, 30, 0, 47, 0, 1], [3, 1, 2, 40, 1, 0, 15], 16, 8, 3, head=head, rows=70)
+    assert w[5].tolist() == [head, 62, 2] and (w[4] >= 0).sum() == 21
+
+
 def test_tables_sums_past_32_bits(dev):
     big = 2 ** 31 - 1
     lens, add = [0, 0, 0, 4], [big, big, big, 3]
