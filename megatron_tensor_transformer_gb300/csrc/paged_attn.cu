@@ -668,10 +668,13 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         const uint32_t groups = group_bits(it, c, loaded[k % kMasks]);
         const int p = c * kP + row;
         const bool counts = p >= it.lo && p < it.n && (groups >> (row >> 4) & 1);
+        // The product is rounded by itself: the reference is such a product, and a fused difference from it would hold
+        // its rounding, which passes every step once the scores' spacing does (from 2^25 on).
         float x[HPT], top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HPT; ++h) {
-          x[h] = counts ? s[h] * sc[h] - sub[h] : -INFINITY;
+          s[h] = __fmul_rn(s[h], sc[h]);
+          x[h] = counts ? s[h] - sub[h] : -INFINITY;
           top = fmaxf(top, x[h]);
         }
         const bool raise = bar_any(bid, 128, top > C::kStep + C::kPLog);
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         if (raise) {  // a new reference: the maximum so far
 #pragma unroll
           for (int h = 0; h < HPT; ++h) {
-            float v = counts ? s[h] * sc[h] : -INFINITY;
+            float v = counts ? s[h] : -INFINITY;
             v = warp_max(v);
             if (lane == 0) s_max[warp][h] = v;
           }
@@ -694,7 +697,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
             f[h] = ex2(sub[h] - to);                       // from kNoRef: of a sum that is 0
             l[h] *= f[h];
             sub[h] = to;
-            x[h] = counts ? s[h] * sc[h] - sub[h] : -INFINITY;
+            x[h] = counts ? s[h] - sub[h] : -INFINITY;
           }
           if (live) {
             tc::tc_fence_after();

@@ -519,6 +519,42 @@ def test_paged_attention_scale_and_peaky_scores(dev, kv):
     c.check()
 
 
+@pytest.mark.parametrize("kv", [tpx.TP_BF16, tpx.TP_FP8_E4M3])
+@pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 26, 2.0 ** 28, 2.0 ** 32, 2.0 ** 60, -(2.0 ** 28), -(2.0 ** 32)])
+@pytest.mark.parametrize("n_q", [4, 32])
+def test_paged_attention_scores_with_a_spacing_above_one(dev, kv, scale, n_q):
+    """Scores whose neighbouring fp32 values are far apart: q is (1, 0, ..), k (1, 3 or 5, 0, ..), so the scores are
+    exact, equal ones are equal in any rounding, and only the largest weigh: o is the mean of their v, lse their score
+    and the logarithm of their number."""
+    c = Case(dev, 1, n_q, 2, 64, 16, [40, 3000, 17, 1], kv, seed=31, poison=False)
+    c.q.zero_()
+    c.q.view(4, n_q, 64)[:, :, 0] = 1.0
+    c.k.copy_(torch.zeros(c.k.shape, device=dev).to(c.k.dtype))
+    if kv == tpx.TP_FP8_E4M3:
+        c.ks.fill_(1.0)
+    rng = np.random.default_rng(31)
+    keys = rng.choice([1.0, 3.0, 5.0], size=(c.n_pages, 2, 16), p=[0.4, 0.3, 0.3])
+    keys[c.table[0, :3]] = np.minimum(keys[c.table[0, :3]], 3.0)         # the first request's largest score is another
+    c.k[0, :, :, :, 0] = torch.tensor(keys, dtype=torch.float32, device=dev).to(c.k.dtype)
+    o, lse = c.launch(scale=scale)
+    got, got_l, v = O.as_f64(bits(o)).reshape(4, n_q, 64), lse.cpu().numpy().astype(np.float64), values(c.v)
+    vs = np.ones(2) if c.vs is None else c.vs.cpu().numpy().astype(np.float64)
+    for m, n in enumerate(c.lens):
+        at, off = c.table[m, np.arange(n) // 16], np.arange(n) % 16
+        for h in range(n_q):
+            g = h // (n_q // 2)
+            s = keys[at, g, off] * scale
+            rows = v[0][at, g, off][s == s.max()] * vs[g]
+            ref, A = rows.mean(0), np.abs(rows).mean(0)
+            # the weights of equal scores are equal; ex2 of them and the sums as in Case.check, without the scores' error
+            e = A * (2 * (2.0 ** -21 + (n / 16 + 300) * 2.0 ** -24) + 2.0 ** -11)
+            if kv == tpx.TP_FP8_E4M3:
+                e = e + n * 2.0 ** -25 * np.abs(rows).max()
+            assert_within(got[m, h], ref, e + HALF * (np.abs(ref) + e), f"o of request {m}")
+            want = s.max() + math.log(len(rows))
+            assert abs(got_l[m, h] - want) <= 2.0 ** -20 * (1 + abs(want)), (m, h)
+
+
 def test_paged_attention_infinite_scores(dev):
     """A key of -inf in the scores weighs nothing; where all do, or one is +inf or NaN, the row says so."""
     c = Case(dev, 1, 2, 2, 64, 16, [40, 40, 40, 1], seed=9, poison=False)
