@@ -67,7 +67,8 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNoRef = -1e38f;           // a reference that any score is a step above
+constexpr float kNoRef = -3.402823466e38f;  // no reference yet: fp32's lowest, which every finite score reaches (one
+                                            // that only reaches it is rightly a weight of 1 under it)
 constexpr int kP = 128;                    // positions per chunk: the rows of an MMA
 constexpr int kN = 16;                     // heads of an MMA (its columns)
 constexpr int kMasks = 32;                 // ring of the chunks' masks: above the chunks in flight

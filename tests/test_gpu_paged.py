@@ -555,6 +555,34 @@ def test_paged_attention_scores_with_a_spacing_above_one(dev, kv, scale, n_q):
             assert abs(got_l[m, h] - want) <= 2.0 ** -20 * (1 + abs(want)), (m, h)
 
 
+@pytest.mark.parametrize("kv", [tpx.TP_BF16, tpx.TP_FP8_E4M3])
+@pytest.mark.parametrize("n_q", [4, 32])
+def test_paged_attention_scores_near_the_lowest(dev, kv, n_q):
+    """Scores near fp32's lowest value are scores, not masks: -2^126 everywhere (times log2 e it is below -1e38) gives
+    the mean of v and lse -2^126."""
+    c = Case(dev, 1, n_q, 2, 64, 16, [40, 3000, 0, 1], kv, seed=32, poison=False)
+    c.q.fill_(2.0 ** 60)
+    c.k.copy_(torch.full(c.k.shape, -(2.0 ** 60) if kv == tpx.TP_BF16 else -256.0, device=dev).to(c.k.dtype))
+    if kv == tpx.TP_FP8_E4M3:
+        c.ks.fill_(2.0 ** 52)
+    o, lse = c.launch(scale=1.0)
+    got, got_l, v = O.as_f64(bits(o)).reshape(4, n_q, 64), lse.cpu().numpy().astype(np.float64), values(c.v)
+    vs = np.ones(2) if c.vs is None else c.vs.cpu().numpy().astype(np.float64)
+    for m, n in enumerate(c.lens):
+        for h in range(n_q):
+            g = h // (n_q // 2)
+            if n == 0:
+                assert not got[m, h].any() and np.isneginf(got_l[m, h])
+                continue
+            rows = v[0][c.table[m, np.arange(n) // 16], g, np.arange(n) % 16] * vs[g]
+            ref, A = rows.mean(0), np.abs(rows).mean(0)
+            e = A * (2 * (2.0 ** -21 + (n / 16 + 300) * 2.0 ** -24) + 2.0 ** -11)   # as for scores far apart
+            if kv == tpx.TP_FP8_E4M3:
+                e = e + n * 2.0 ** -25 * np.abs(rows).max()
+            assert_within(got[m, h], ref, e + HALF * (np.abs(ref) + e), f"o of request {m}")
+            assert abs(got_l[m, h] + 2.0 ** 126) <= 2.0 ** (126 - 20), (m, h)
+
+
 def test_paged_attention_infinite_scores(dev):
     """A key of -inf in the scores weighs nothing; where all do, or one is +inf or NaN, the row says so."""
     c = Case(dev, 1, 2, 2, 64, 16, [40, 40, 40, 1], seed=9, poison=False)
