@@ -432,8 +432,13 @@ def tp_paged_attn_block_forward(qkv, qkv_w, o, o_w, x, residual, rope, pages, po
 
 
 def tp_token_logprobs(logits, ids, logprob, entropy, rank, top_logprob=None, top_id=None, stream=None):
-    """logits: [M, vocab] fp32, rows logits.stride(0) apart; ids, rank: [M] int32; logprob, entropy: [M] fp32;
-    top_logprob, top_id: [M, k] or None (all on the device; ids, logprob, entropy and rank may be None)."""
+    """logits: [M, vocab] fp32, rows logits.stride(0) apart, a row's logits next to one another; ids, rank: [M] int32;
+    logprob, entropy: [M] fp32; top_logprob, top_id: [M, k], both or neither (all on the device; ids, logprob, entropy
+    and rank may be None)."""
+    if logits.shape[1] > 1 and logits.stride(1) != 1:
+        raise TpxError(TP_ERR_INVALID_ARG, "tp_token_logprobs: logits' stride along the vocabulary")
+    if (top_logprob is None) != (top_id is None) or (top_id is not None and top_logprob.shape != top_id.shape):
+        raise TpxError(TP_ERR_INVALID_ARG, "tp_token_logprobs: top_logprob and top_id")
     k = 0 if top_id is None else top_id.shape[1]
     ldl = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
     _check(lib().tp_token_logprobs(_ptr(logits), ldl, logits.shape[0], logits.shape[1], _ptr(ids), k, _ptr(logprob),

@@ -6,6 +6,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 from megatron_tensor_transformer_gb300 import tpx
 from oracle import paged_oracle as PO
@@ -136,6 +137,19 @@ def test_logprobs_refusals():
     for kw in (dict(logits=ODD), dict(ids=ODD), dict(lp=ODD), dict(rank=ODD), dict(ent=ODD), dict(tl=ODD), dict(ti=ODD)):
         assert logprobs(**kw) == tpx.TP_ERR_ALIGN, kw
     assert logprobs(M=0) == tpx.TP_OK
+
+
+def test_logprobs_binding_refusals():
+    """What the C call cannot see: logits that are not next to one another, one half of the alternatives alone."""
+    x = torch.zeros((4, 100))
+    f, n = torch.zeros(4), torch.zeros(4, dtype=torch.int32)
+    tl, ti = torch.zeros((4, 3)), torch.zeros((4, 3), dtype=torch.int32)
+    for args in ((torch.zeros((100, 4)).t(), n, f, f, n), (torch.zeros((4, 200))[:, ::2], n, f, f, n),
+                 (torch.zeros((1, 200))[:, ::2], n, f, f, n),
+                 (x, n, f, f, n, tl, None), (x, n, f, f, n, None, ti), (x, n, f, f, n, tl, ti[:, :2])):
+        with pytest.raises(tpx.TpxError) as e:
+            tpx.tp_token_logprobs(*args)
+        assert e.value.status == tpx.TP_ERR_INVALID_ARG
 
 
 def test_block_refusals():
