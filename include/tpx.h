@@ -364,7 +364,9 @@ typedef struct {
  * page is left.  The outputs must not overlap the inputs (checked for lens_out against lens and add
  * and for counts against head): steps alternate between two sets, one call's lens_out and counts
  * being the next one's lens and head, with nothing read by the host.  int32 arrays on the device, 4-byte aligned.  One kernel
- * launch.  M == 0 is a no-op. */
+ * launch.  M == 0 is a no-op that writes nothing, counts and the rows' slots included: after it the two sets are not
+ * exchanged (the next step's head is the counts written last; the other set's are a step older, and its pages would go
+ * out twice). */
 tp_status tp_paged_tables(const tp_pages* pages /* host */, const int32_t* lens, const int32_t* add, int32_t M,
                           const int32_t* free_pages, int32_t n_free, const int32_t* head, int32_t* block_table,
                           int32_t* lens_out, int32_t* cu_rows, int32_t* positions, int32_t* slots, int32_t rows,

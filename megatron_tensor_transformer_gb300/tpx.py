@@ -363,7 +363,8 @@ def make_rope(rot_dim, theta=10000.0, layout=TP_ROPE_HALF, scaling=TP_ROPE_NONE,
 def tp_paged_tables(pages, lens, add, free_pages, block_table, lens_out, cu_rows, positions, slots, counts, head=None,
                     stream=None):
     """All int32 on the device: lens, add, lens_out [M]; free_pages [n_free]; block_table [M, table_stride]; cu_rows
-    [M + 1]; positions, slots [rows]; counts [3]; head: one element or None.  Returns slots."""
+    [M + 1]; positions, slots [rows]; counts [3]; head: one element or None.  Returns slots.  With no requests nothing
+    is written, counts included: keep the set written last as the next step's lens and head."""
     _check(lib().tp_paged_tables(ctypes.byref(pages), _ptr(lens), _ptr(add), lens.shape[0], _ptr(free_pages),
                                  free_pages.shape[0], _ptr(head), _ptr(block_table), _ptr(lens_out), _ptr(cu_rows),
                                  _ptr(positions), _ptr(slots), slots.shape[0], _ptr(counts), _stream(stream)),

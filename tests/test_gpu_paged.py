@@ -151,6 +151,26 @@ def test_tables_step_after_step_without_the_host(dev):
         assert np.array_equal(got[p], t[:, p // page] * page + p % page)
 
 
+def test_tables_a_step_without_requests_writes_nothing(dev):
+    """The chain goes on from the counts written last, and every page goes out once."""
+    page, P = 16, 4
+    pages = tpx.make_pages(page, 40, P)
+    free = i32(np.random.default_rng(6).permutation(40), dev)
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+    head, given = z(3), []
+    for M, rows in ((2, 6), (0, 6), (3, 6), (0, 0), (1, 6)):
+        counts, table = torch.full((3,), -9, dtype=torch.int32, device=dev), z(M, P) - 1
+        lo, cu, pos, slots = z(M) - 9, z(M + 1) - 9, z(rows) - 9, z(rows) - 9
+        tpx.tp_paged_tables(pages, z(M), i32(np.full(M, 1), dev), free, table, lo, cu, pos, slots, counts, head=head)
+        sync()
+        if M == 0:
+            assert all((x == -9).all() for x in (counts, cu, pos, slots))
+            continue
+        given += table[:, 0].tolist()
+        head = counts
+    assert given == free[:6].tolist() and head.tolist() == [6, 1, 0]
+
+
 # -------------------------------------------------------------------------------------------- rope
 def make_qkv(dev, M, n_q, n_kv, hd, seed):
     return inputs.normal_bf16((M, (n_q + 2 * n_kv) * hd), 1.0, seed, 90, dev)
