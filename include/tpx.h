@@ -442,8 +442,12 @@ tp_status tp_rope_append(const tp_shape* shape /* host */, const tp_rope* rope /
  * kv head g = h / (n_q / n_kv), with j over max(0, lens[m] - window) .. lens[m] - 1 (window 0: from 0):
  *   s_j = scale q[m, h] . k_j;   lse[m, h] = ln sum_j exp(s_j);   o[m, h] = bf16( sum_j exp(s_j - lse) v_j )
  * q: [M, n_q hd] bf16, o_in: [M, n_q hd] bf16, lse: [M, n_q] fp32 or NULL; scale 0 stands for
- * 1 / sqrt(hd).  fp32 scores, softmax and accumulation.  A request with lens[m] outside
- * [1, max_pages * page_size] gets a zero row and lse -inf.  Positions of a page whose id is outside
+ * 1 / sqrt(hd).  Scores, softmax statistics and sums are fp32.  On their way into the tensor cores the weights exp(..)
+ * keep fewer bits: over bf16 pages 2^-16 of a weight (two bf16), over e4m3 pages 2^-11 of it and 2^-25 of the
+ * largest (fp16, then three e4m3).  Over e4m3 pages q is two e4m3 after a power of two per head: exact down
+ * to 2^-10 of the head's largest |q|, good to 2^-17 of that largest below.  Each of these is under half a step of a bf16
+ * and shows in o's last bit.  A request with lens[m] outside [1, max_pages * page_size] gets a zero row and lse -inf.
+ * Positions of a page whose id is outside
  * [0, n_pages) are left out as if masked; a row left without positions is zero with lse -inf.  Cache
  * rows outside the positions attended to never enter the result, whatever they hold.  A score of -inf counts
  * as masked; a NaN, and an infinite q or v that is used, gives NaN (an infinite q at the latest where a score

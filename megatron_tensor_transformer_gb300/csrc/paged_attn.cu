@@ -24,7 +24,7 @@
 //     does not show beside the output's own; the tensor cores have the time.
 //   e4m3 pages: e4m3 products (kind::f8f6f4).  q is split into two codes (q / 2^e = hi + lo, all of a
 //     bf16's bits unless it is below 2^-10 of its head's largest value).  P is split into three, each the
-//     rest of the one before times 16: good to 2^-12 of its value or 2^-25 of a weight of 1, so that
+//     rest of the one before times 16: good to 2^-11 of its value and 2^-25 of a weight of 1, so that
 //     the many small weights of a long context are not lost.  The heads' scales go to the scores and to
 //     the output.
 // The codes of a split operand are columns of one MMA side by side (N = 16 per code) and their products
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         }
         uint8_t* pt = sP + (size_t)team * C::TERMS * C::PTILE;
         if (FP8) {
-          __half2 r[HPT / 2];  // fp16 holds 2^-12 of a weight, or 2^-32 of one that is 1
+          __half2 r[HPT / 2];  // good to 2^-11 of a weight, or 2^-32 of one that is 1
 #pragma unroll
           for (int q = 0; q < HPT / 2; ++q) r[q] = __floats2half2_rn(s[2 * q], s[2 * q + 1]);
           const __half2 next = __float2half2_rn(C::kNext);
