@@ -27,7 +27,6 @@
 #include <cuda.h>
 
 #include "attn.h"
-#include "attn_mma.cuh"
 #include "common.cuh"
 #include "tc.h"
 #include "tc_ptx.cuh"
@@ -107,6 +106,17 @@ __device__ __forceinline__ float* part_ptr(const AttnGeo& g, float* ws, int m, i
   const int nch = (g.L + g.P - 1) / g.P;
   const size_t per = (size_t)g.G * (g.hd + 2);
   return ws + (((size_t)m * g.n_kv + gg) * nch + c) * per;
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
 }
 
 // Byte offset of (position r, dim k) in a chunk staged as HD/64 boxes of [P rows][64 dims] in

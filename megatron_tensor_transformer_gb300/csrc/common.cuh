@@ -20,6 +20,16 @@ __device__ __forceinline__ uint16_t f2bf(float f) {
   return *reinterpret_cast<uint16_t*>(&b);
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // one conversion for both
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Shared memory written by ordinary stores is seen by TMA and the tensor cores after it.
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // 16-byte streaming load that bypasses L1 allocation: weights are read exactly once.
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   uint4 r;

@@ -55,7 +55,6 @@
 #include <algorithm>
 #include <atomic>
 
-#include "attn_mma.cuh"
 #include "common.cuh"
 #include "paged.h"
 #include "tc.h"

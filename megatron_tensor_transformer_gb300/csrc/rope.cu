@@ -15,7 +15,6 @@
 // Measured on one GB300: 8192 rows of 64 q and 8 kv heads of 128 into bf16 pages 56.5 us, 5.94 TB/s (a plain
 // copy of as many bytes 50.0 us, the append without turning 52.9); 1003 rows of 32 and 8 heads into e4m3 pages
 // 6.2 us; 32 rows of 64 and 8 heads 2.6 us.  Bound by HBM and, beside it, by the angles and the turning.
-#include "attn_mma.cuh"
 #include "common.cuh"
 #include "paged.h"
 #include "tc_ptx.cuh"
