@@ -118,6 +118,30 @@ def test_logprobs_masked_rows(dev):
     assert got["ti"][2].tolist() == [-1] * 10 and got["rank"][3] == 0
 
 
+@pytest.mark.parametrize("V", [20, 40, 130, 511, 1000, 2047, 8001])
+@pytest.mark.parametrize("kept", [0.02, 0.3, 1.0])
+def test_logprobs_short_masked_rows(dev, V, kept):
+    """Rows with fewer vectors than groups of threads, most of them masked: fewer groups hold a value than there are
+    alternatives, which then go on into the masked ids, the lowest first."""
+    M, rng = 6, np.random.default_rng(V)
+    x = normal(M, V, V)
+    x[rng.random((M, V)) >= kept] = -np.inf
+    x[np.arange(M), rng.integers(0, V, M)] = 1.0            # none is masked altogether
+    for k in (1, min(V, 20), min(V, 24), min(V, 25), min(V, 32)):
+        check(dev, x, rng.integers(0, V, M), k, pad=V % 3, lead=V % 4)
+
+
+@pytest.mark.parametrize("left", [1, 7, 40])
+def test_logprobs_few_ids_left_of_a_large_vocabulary(dev, left):
+    """A vocabulary masked down to a few ids that lie far apart, over one CTA a row and several."""
+    V, rng = 128256, np.random.default_rng(left)
+    for M in (3, 160):
+        x = np.full((M, V), -np.inf, np.float32)
+        for m in range(M):
+            x[m, rng.choice(V, left, replace=False)] = rng.normal(size=left)
+        check(dev, x, [int(np.argmax(r)) for r in x], 20)
+
+
 def test_logprobs_ids_that_ask_for_nothing(dev):
     x = normal(5, 700, 4)
     x[4, 3] = np.nan

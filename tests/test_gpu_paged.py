@@ -506,6 +506,29 @@ def test_paged_attention_many_requests(dev, M):
     Case(dev, 1, 4, 2, 64, 16, lens, seed=M).check()
 
 
+@pytest.mark.parametrize("kv", [tpx.TP_BF16, tpx.TP_FP8_E4M3])
+@pytest.mark.parametrize("t,n_q,n_kv,hd,page,M", [(1, 32, 2, 128, 16, 200), (2, 8, 4, 256, 32, 90), (1, 16, 1, 256, 64, 61),
+                                                  (2, 16, 2, 128, 128, 333), (1, 16, 1, 64, 16, 170)])
+def test_paged_attention_many_requests_by_heads(dev, kv, t, n_q, n_kv, hd, page, M):
+    """Batches whose CTAs take several items each, over both types, 4 and 8 heads a thread and every width."""
+    rng = np.random.default_rng(M)
+    lens = np.where(rng.random(M) < 0.1, 0, rng.integers(1, 400, M))
+    lens[[3, M - 1]] = [1700, 1]
+    Case(dev, t, n_q, n_kv, hd, page, lens, kv, seed=M).check()
+
+
+@pytest.mark.parametrize("kv", [tpx.TP_BF16, tpx.TP_FP8_E4M3])
+@pytest.mark.parametrize("t,n_q,n_kv,hd,page", [(1, 16, 1, 128, 32), (2, 32, 2, 256, 64), (1, 4, 1, 256, 128), (1, 2, 2, 64, 16),
+                                                (1, 15, 1, 64, 256), (1, 5, 1, 128, 16)])
+def test_paged_attention_pieces_joined_twice(dev, kv, t, n_q, n_kv, hd, page):
+    """One or two long requests of few kv heads: more pieces than are joined at once, for every number of heads a
+    thread and every width, and the same bits again."""
+    c = Case(dev, t, n_q, n_kv, hd, page, [9001, 0, 6007], kv, seed=n_q, std=2.0)
+    o, lse = c.check()
+    o2, lse2 = c.launch()
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+
+
 def test_paged_attention_lengths_out_of_range(dev):
     """Lengths below zero or past the table's row: zero rows, and nothing is read for them."""
     c = Case(dev, 1, 8, 2, 128, 16, [40, 100, 7], seed=6)
