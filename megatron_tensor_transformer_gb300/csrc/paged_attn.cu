@@ -267,8 +267,10 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   // A chunk is two units of work, the beginning and end of a (request, kv head) kEnds.  bf16, 128 dims, with 1, 2, 3
   // and 4: 32 requests up to 4096 take 52.9, 53.1, 53.3 and 54.3 us, 100 up to 2000 74.9, 68.3, 68.6 and 69.2, 256
   // up to 700 91.6, 88.1, 84.6 and 84.4; 256 dims: 256 up to 700 63.7, 63.8, 64.8 and 66.3.  e4m3, 8 heads a thread,
-  // with 8, 10 and 12: 48 up to 8192 79.7, 80.7 and 82.0, 100 up to 2000 80.9, 78.5 and 77.9.
-  constexpr int kEnds = FP8 ? (HPT == 8 ? 8 : 6) : C::STAGE >= 64 * 1024 ? 1 : C::STAGE >= 32 * 1024 ? 3 : 4;
+  // with 6, 8, 10 and 12: 48 up to 8192 93.6, 90.4, 90.7 and 91.9, 100 up to 2000 86.5, 80.3, 77.6 and 78.0, 256 up to
+  // 700 140.7, 137.5, 137.4 and 137.5, 32 up to 4096 41.5, 39.7, 40.1 and 40.0, 100 windows of 1024 76.4, 75.3, 73.5
+  // and 73.4, 64 up to 512 37.1, 37.1, 36.7 and 37.2, long ones alike: 10 is the least over all of them.
+  constexpr int kEnds = FP8 ? (HPT == 8 ? 10 : 6) : C::STAGE >= 64 * 1024 ? 1 : C::STAGE >= 32 * 1024 ? 3 : 4;
   constexpr int kProducer = kSoftWarps, kScores = kProducer + 1, kItems = kProducer + 2, kPV = kProducer + 3;
   extern __shared__ __align__(1024) uint8_t ring[];  // the swizzles' atoms; static shared memory is padded to it
   uint8_t* sQ = ring + C::kRing;           // [2][QTILE]
