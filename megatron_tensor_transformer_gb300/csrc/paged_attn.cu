@@ -238,8 +238,10 @@ __device__ __forceinline__ uint32_t group_bits(const Item& it, int c, uint32_t l
   const int a0 = max(0, it.lo - c * kP), a1 = min(kP, it.n - c * kP);
   return loaded & ((1u << ((a1 + 15) >> 4)) - 1) & ~((1u << (a0 >> 4)) - 1);
 }
-// A role's bounded waits: one that runs out sets the error word, and the role goes on without
-// waiting, so that every barrier is still met and the kernel ends.
+// A role's bounded waits.  After one that runs out (it sets the error word) the producer issues no more copies and
+// the two issuing threads no more MMAs, and each waits, bounded again, for what it has in flight; the softmax warps
+// go on without waiting to the item's end, so that their team's barriers are met.  Then the kernel ends: no copy
+// lands in shared memory and no MMA in tensor memory that the CTA has given back.
 // (The loop is a function of its own: inlined at every wait it made the roles' code together larger than the
 // SM's instruction cache, and the kernel's time depend on where the compiler put what, by up to a quarter.)
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
@@ -251,9 +253,10 @@ struct Waits {
   unsigned* err;
   unsigned code;
   bool failed;
-  __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) {
-    if (!tc::mbar_try_wait(bar, parity) && !tc::mbar_try_wait(bar, parity) && !failed)
-      failed = wait_long(bar, parity, err, code);
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
+    if (tc::mbar_try_wait(bar, parity) || tc::mbar_try_wait(bar, parity)) return true;
+    if (!failed) failed = wait_long(bar, parity, err, code);
+    return !failed;
   }
 };
 
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   uint8_t* sP = sQ + 2 * C::QTILE;         // [2][TERMS][PTILE], one per team
   __shared__ Item s_item[4];
   __shared__ __align__(8) uint64_t kv_full[2][C::NS], kv_empty[2][C::NS], q_full[2], q_empty[2], s_full[2], s_empty[2],
-      p_full[2], p_empty[2], o_full[2], o_empty[2], x_full[2], x_empty[2], i_full[4], i_empty[4];
+      p_full[2], p_empty[2], o_full[2], o_empty[2], x_full[2], x_empty[2], i_full[4], i_empty[4], mma_done[2];
   __shared__ long long s_part[kWarps], s_base;  // s_base: units before request s_m, which holds the CTA's first one
   __shared__ float s_max[kSoftWarps][HPT], s_sum[kSoftWarps][HPT], s_x[2][NG][2][HPT], q_pow[FP8 ? 4 : 1][kN];
   __shared__ uint32_t loaded[kMasks];                // 16-position groups of a chunk that were loaded, by bit
@@ -301,6 +304,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       tc::mbar_init(B(o_empty[i]), 4 * NG);
       tc::mbar_init(B(x_full[i]), NG);
       tc::mbar_init(B(x_empty[i]), 4 * NG);
+      tc::mbar_init(B(mma_done[i]), 1);
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(B(i_full[i]), 1);
@@ -392,19 +396,19 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       return p < it.n && p + (1 << a.page_shift) > it.lo ? a.table[(size_t)it.m * a.table_stride + page] : -1;
     };
     int k = 0;
+    bool stop = false;
     Item it = next_item(wait, 0, true), nx = it;
     int at = 0, ids = -1, ids_next = -1, ids_item = -1;  // lanes' ids from page `at` on; the 32 after; the next item's
     if (it.m >= 0) {
       at = first_page(it);
       ids = ids_from(it, at);
     }
-    for (int j = 0; it.m >= 0; ++j) {
+    for (int j = 0; __all_sync(kFull, it.m >= 0) && !stop; ++j) {
       ids_next = ids_from(it, at + 32);
       auto look_ahead = [&]() {
         nx = next_item(wait, j + 1, true);
         if (nx.m >= 0) ids_item = ids_from(nx, first_page(nx));
       };
-      if (j > 0) look_ahead();  // (the first item's copies do not wait for the second item)
       const int base = (it.gg / nkvs) * a.n_pages, g = it.gg % nkvs;
       for (int c = it.c0; c < it.c1; ++c, ++k) {
         const int pos = c * kP + box * box_rows, page = pos >> a.page_shift;
@@ -434,12 +438,23 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
             tc::tma_load_2d_hint(tc::smem_u32(ring + (size_t)st * C::STAGE) + (side * kP + box * box_rows) * C::INB,
                                  kv ? &tmV : &tmK, side * (C::INB / (FP8 ? 1 : 2)), row, B(kv_full[kv][k % C::NS]), pol);
         }
-        if (j == 0 && c == it.c0) look_ahead();
+        if (c == it.c0) look_ahead();
+        // After a wait that ran out the chunk's copies are the last.  Their arrivals meet no open phase all the same:
+        // copy i's barrier served copy i - 2 NS before, which the wait at copy i - NS has seen read.  (A vote before
+        // the copies cost every stage 16 ns: e4m3 1 to 3%.)
+        if (__any_sync(kFull, wait.failed)) {
+          ++k;
+          stop = true;
+          break;
+        }
       }
       it = nx;
       at = first_page(it);
       ids = ids_item;
     }
+    static_assert(2 * C::NS <= 32, "a lane for every barrier");
+    const int last = 2 * k - 1 - lane, lc = last >> 1;  // copies in flight: each barrier's last
+    if (lane < 2 * C::NS && last >= 0) wait_long(B(kv_full[last & 1][lc % C::NS]), (lc / C::NS) & 1, a.err, 44u);
   } else if (warp == kScores) {
     // ---- scores: one thread issues
     if (lane == 0) {
@@ -449,11 +464,11 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       for (int j = 0;; ++j) {
         const Item it = next_item(wait, j, false);
         if (it.m < 0) break;
-        wait(B(q_full[j & 1]), (j >> 1) & 1);
+        if (!wait(B(q_full[j & 1]), (j >> 1) & 1)) break;
         const uint32_t qA = tc::smem_u32(sQ + (size_t)(j & 1) * C::QTILE);
         for (int c = it.c0; c < it.c1; ++c, ++k) {
-          wait(B(kv_full[0][k % C::NS]), (k / C::NS) & 1);
-          if (k >= 2) wait(B(s_empty[k & 1]), ((k >> 1) - 1) & 1);
+          if (!wait(B(kv_full[0][k % C::NS]), (k / C::NS) & 1)) goto scores_end;
+          if (k >= 2 && !wait(B(s_empty[k & 1]), ((k >> 1) - 1) & 1)) goto scores_end;
           tc::tc_fence_after();
           const uint32_t kA = tc::smem_u32(ring + (size_t)(2 * k % C::NS) * C::STAGE);
 #pragma unroll
@@ -468,6 +483,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         }
         tc::mma_commit(B(q_empty[j & 1]));
       }
+    scores_end:;
     }
     __syncwarp();
   } else if (warp == kPV) {
@@ -488,11 +504,11 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
       for (int j = 0;; ++j) {
         const Item it = next_item(wait, j, false);
         if (it.m < 0) break;
-        if (j >= 2) wait(B(o_empty[j & 1]), ((j >> 1) - 1) & 1);
+        if (j >= 2 && !wait(B(o_empty[j & 1]), ((j >> 1) - 1) & 1)) break;
         uint32_t live = 0;  // by team: its O holds something
         for (int c = it.c0; c < it.c1; ++c, ++k) {
-          wait(B(p_full[k & 1]), (k >> 1) & 1);
-          wait(B(kv_full[1][k % C::NS]), (k / C::NS) & 1);
+          if (!wait(B(p_full[k & 1]), (k >> 1) & 1)) goto pv_end;
+          if (!wait(B(kv_full[1][k % C::NS]), (k / C::NS) & 1)) goto pv_end;
           tc::tc_fence_after();
           const uint32_t groups = group_bits(it, c, loaded[k % kMasks]);
           const uint32_t vA = tc::smem_u32(ring + (size_t)((2 * k + 1) % C::NS) * C::STAGE);
@@ -517,6 +533,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         }
         tc::mma_commit(B(o_full[j & 1]));
       }
+    pv_end:;
     }
     __syncwarp();
   } else if (warp == kItems) {
@@ -536,7 +553,8 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     for (;;) {
       Item it{};
       it.m = -1;
-      while (at < u1 && !wait.failed) {
+      if (__any_sync(kFull, wait.failed)) at = u1;  // for all lanes
+      while (at < u1) {
         const int n = units_of(s, kEnds), ch = s.c1 - s.c0;
         if (n > 0) {
           // chunk i begins at unit at + kEnds + 2 i
@@ -943,6 +961,10 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         from = kSlots;
       }
     }
+  }
+  if ((warp == kScores || warp == kPV) && lane == 0) {  // its MMAs in flight
+    tc::mma_commit(B(mma_done[warp == kPV]));
+    wait_long(B(mma_done[warp == kPV]), 0, a.err, 49u);
   }
   tc::tc_fence_before();
   __syncthreads();
