@@ -19,8 +19,10 @@
 // 32 rows 9 us, more than reading them.)
 //
 // Measured on one GB300, 128256 logits a row: 1900 rows 156 us without alternatives (92% of the measured
-// copy's 6792 GB/s), 182 with one, 218 with 20 (66%: instructions issue in 75% of the cycles); 32 rows 7.2
-// us without, 10.9 with 8.
+// copy's 6792 GB/s), 182 with one, 206 with 20 (70%: instructions issue in 75% of the cycles; 219 where the given tokens
+// are random ids and not likely ones, so that more logits are compared with theirs one by one); 32 rows 7.2 us
+// without, 10.8 with 8.  Short rows are a launch and the barriers: 2000 rows of 2000 logits 20 us, with 20
+// alternatives 39.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -337,7 +339,9 @@ cudaError_t launch_token_logprobs(const LogprobsArgs& a, cudaStream_t st) {
   // CTAs per row: two if that is at most one per SM over all rows, four and eight up to 256 in all, while each
   // still has 4 vectors per thread.  With 1, 2, 4, 8 CTAs and 8 alternatives of 128256 logits, 32 rows take 21.0,
   // 16.2, 11.5, 10.8 us, 64 rows 21.9, 16.9, 15.7, 20.8, 76 rows 22.2, 17.1, 22.5, 27.7, 128 rows 22.4, 23.9, 29.3,
-  // 39.4: a second CTA on some SMs takes them nearly as long again.
+  // 39.4: a second CTA on some SMs takes them nearly as long again.  With 8 alternatives the rule is within 12% of the
+  // best of these at 2000, 8000, 16000 and 64000 logits for 1 to 200 rows, and at 32000 for 48 rows and more; one row
+  // of 32000 takes 7.7 us where four CTAs take 6.5, 16 rows 8.2 and 7.0.
   int c = 1;
   while (c < kMaxC && (int64_t)a.M * 2 * c <= (c == 1 ? 152 : 256) && a.vocab / (2 * c) >= 4 * 4 * kNT) c *= 2;
   return c == 1 ? launch<1>(a, st) : c == 2 ? launch<2>(a, st) : c == 4 ? launch<4>(a, st) : launch<8>(a, st);

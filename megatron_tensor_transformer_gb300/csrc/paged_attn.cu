@@ -40,15 +40,16 @@
 // joining 19 pieces took 10 us).  Every sum's order follows from the lengths and the SM count: runs repeat
 // bit for bit.
 // Measured on one GB300 (GPU time of a call among others, fractions of the measured copy's 6792 GB/s):
-//   1 request of 131071 tokens, 64 q and 8 kv heads of 128, bf16, pages of 64        87.7 us, 90%
-//   32 ragged requests up to 4096, the same heads, pages of 16                       53.1 us, 80%
-//   48 ragged requests up to 8192, 128 q and 8 kv heads, e4m3, pages of 32           79.9 us, 67%
-//   61 ragged requests, a window of 1024, 8 q and 4 kv heads of 256, pages of 128    43.1 us, 78%
-//   1 request of 519 tokens, 32 q and 8 kv heads, pages of 16                         9.9 us (latency)
-// What is left: about 3 us before the first products (launch, the lengths' sum, the page look-up, the first
-// copies) and 2.5 us of counting in and joining; the ends of short requests and the SMs' unequal shares of the
-// HBM; and over e4m3 each (request, kv head)'s beginning and end, 2.4 us beside 0.7 us a chunk, with 16 heads
-// per kv head 4.4 beside 0.78 (0.74 at the copy's rate).
+//   1 request of 131071 tokens, 64 q and 8 kv heads of 128, bf16, pages of 64        87.6 us, 90%
+//   32 ragged requests up to 4096, the same heads, pages of 16                       53.4 us, 80%
+//   256 ragged requests up to 700, the same heads, pages of 32                       86.2 us, 63%
+//   48 ragged requests up to 8192, 128 q and 8 kv heads, e4m3, pages of 32           82.0 us, 66%
+//   61 ragged requests, a window of 1024, 8 q and 4 kv heads of 256, pages of 128    43.0 us, 78%
+//   1 request of 519 tokens, 32 q and 8 kv heads, pages of 16                        10.0 us (latency)
+// What is left: the short request's chain, 3.1 us for a call without positions (launch, the lengths' sum), 3.9 more
+// for one chunk (items, page look-up, copies, products, the row), 2.0 more once two chunks are joined; the ends of
+// short requests and the SMs' unequal shares of the HBM; and over e4m3 each (request, kv head)'s beginning and end, 2.4
+// us beside 0.7 us a chunk, with 16 heads per kv head 4.4 beside 0.79 (0.73 at the copy's rate).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -270,9 +271,9 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   // A chunk is two units of work, the beginning and end of a (request, kv head) kEnds.  bf16, 128 dims, with 1, 2, 3
   // and 4: 32 requests up to 4096 take 52.9, 53.1, 53.3 and 54.3 us, 100 up to 2000 74.9, 68.3, 68.6 and 69.2, 256
   // up to 700 91.6, 88.1, 84.6 and 84.4; 256 dims: 256 up to 700 63.7, 63.8, 64.8 and 66.3.  e4m3, 8 heads a thread,
-  // with 6, 8, 10 and 12: 48 up to 8192 93.6, 90.4, 90.7 and 91.9, 100 up to 2000 86.5, 80.3, 77.6 and 78.0, 256 up to
-  // 700 140.7, 137.5, 137.4 and 137.5, 32 up to 4096 41.5, 39.7, 40.1 and 40.0, 100 windows of 1024 76.4, 75.3, 73.5
-  // and 73.4, 64 up to 512 37.1, 37.1, 36.7 and 37.2, long ones alike: 10 is the least over all of them.
+  // with 6, 8, 10 and 12: 48 up to 8192 94.7, 91.4, 91.6 and 92.8, 100 up to 2000 88.8, 82.5, 80.0 and 79.7, 256 up to
+  // 700 143.5, 140.5, 140.1 and 140.1, 32 up to 4096 42.5, 40.4, 40.7 and 40.6, 100 windows of 1024 78.1, 77.0, 75.1
+  // and 74.8, 64 up to 512 37.8, 37.8, 37.6 and 38.0, long ones alike: 10 is the least over all of them.
   constexpr int kEnds = FP8 ? (HPT == 8 ? 10 : 6) : C::STAGE >= 64 * 1024 ? 1 : C::STAGE >= 32 * 1024 ? 3 : 4;
   constexpr int kProducer = kSoftWarps, kScores = kProducer + 1, kItems = kProducer + 2, kPV = kProducer + 3;
   extern __shared__ __align__(1024) uint8_t ring[];  // the swizzles' atoms; static shared memory is padded to it
