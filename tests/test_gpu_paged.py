@@ -911,3 +911,24 @@ def test_paged_attention_block_shares_a_workspace_over_m(dev, wtype, kv):
         for key in a:
             assert torch.equal(a[key].view(torch.int16), b[key].view(torch.int16)), (M, key)
         tpx.tp_rowpar_forward(od, o_w, xs[:, :n_q * hd].contiguous(), None, b16(big, d), ws)  # scratch over the counters
+    # steps captured into a graph per M, as a server keeps them, replayed in turn over the one workspace
+    graphs, side = {}, torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for M in (8, 33, 70):
+        out = dict(y=b16(M, d), qkv=b16(M, (n_q + 2 * n_kv) * hd), q=b16(M, n_q * hd), o=b16(M, n_q * hd))
+        g = torch.cuda.CUDAGraph()
+        step = lambda st: tpx.tp_paged_attn_block_forward(qd, q_w, od, o_w, xs[:M], xs[:M], rope, pages, pos, slots, *cache,
+                                                          table, lens, out["y"], out["qkv"], out["q"], out["o"], ws,
+                                                          k_scale=ks, v_scale=vs, stream=st)
+        step(torch.cuda.current_stream())
+        sync()
+        want = out["y"].clone()
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            step(side)
+        graphs[M] = (g, out, want)                                      # the graph's buffers live as long as it does
+    for M in (70, 8, 33, 8, 70, 33):
+        g, out, want = graphs[M]
+        out["y"].fill_(float("nan"))
+        g.replay()
+        sync()
+        assert torch.equal(out["y"].view(torch.int16), want.view(torch.int16)), M
