@@ -464,6 +464,32 @@ tp_status tp_paged_attn_decode(const tp_shape* shape /* host */, const tp_pages*
                                const int32_t* block_table, const int32_t* lens, int32_t M, float scale, int32_t window,
                                void* o_in, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* The same attention where requests share prefixes: what a group of requests has in common is read, and multiplied
+ * with all their heads, once.  Group g is the rows cu_groups[g] .. cu_groups[g+1]-1, whose block-table rows begin
+ * with the same prefix_lens[g] / page_size pages (whole pages: one that the prefix ends within is each request's own);
+ * these positions are read through the table row of the group's first request, all others through the request's own.
+ * o_in and lse as from tp_paged_attn_decode, whose rules for lengths, windows, pages that are none, infinities and NaN
+ * hold; what is not attended to never enters a result.  A request whose positions do not hold all of the shared ones
+ * (lens[m] is less, or a window begins among them), a group of one request and a row outside every group are
+ * attended to as there, each by itself.
+ * cu_groups [n_groups + 1] and prefix_lens [n_groups]: int32 on the device; 0 <= cu_groups[0] <= cu_groups[1] <= .. <= M
+ * (a group may be empty; a group that breaks this, or whose prefix is negative or longer than a row of the table,
+ * counts as having no prefix).  n_groups is at most M; 0: as tp_paged_attn_decode (the two may then be NULL).
+ * Scores, softmax statistics and sums are fp32.  The shared positions' weights enter the product rounded to bf16 over
+ * bf16 pages (2^-8 of a weight, the tensor cores' operand type) and to fp16 over e4m3 pages (2^-11 of a weight and
+ * 2^-32 of the largest; q is there fp16 after a power of two per head, exact down to 2^-24 of the head's largest |q|),
+ * and the parts' sums are joined in fp32.
+ * ws: tp_prefix_attn_workspace_bytes(shape, M) bytes, zero-filled once before first use (and after a
+ * TP_ERR_DEVICE_TIMEOUT), left reusable by every call whose size it covers, tp_paged_attn_decode's included; calls that
+ * share it must not overlap on the GPU (replays of two captured graphs included).  Up to three kernel launches; runs
+ * repeat bit for bit.  M == 0 is a no-op. */
+size_t tp_prefix_attn_workspace_bytes(const tp_shape* shape /* host */, int32_t M);
+tp_status tp_prefix_attn_decode(const tp_shape* shape /* host */, const tp_pages* pages /* host */, const void* q,
+                                const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                                const int32_t* block_table, const int32_t* lens, int32_t M, const int32_t* cu_groups,
+                                const int32_t* prefix_lens, int32_t n_groups, float scale, int32_t window, void* o_in,
+                                float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Vocabulary-parallel lm_head (the column-parallel GEMM at the model's output edge; each shard's
  * logits are a slice of the output, so the pages' all-gather is a concatenation, scalablesystem.dev
  * "The Tensor-Parallel Shard Group"): logits[m][v] = sum_k x[m][k] W[k][v] for v < vocab, fp32
@@ -510,6 +536,27 @@ tp_status tp_paged_attn_block_forward(const tp_packed_desc* qkv /* host */, cons
 tp_status tp_token_logprobs(const float* logits, int64_t ldl, int32_t M, int32_t vocab, const int32_t* ids, int32_t k,
                             float* logprob, int32_t* rank, float* entropy, float* top_logprob, int32_t* top_id,
                             void* stream);
+
+/* The next token of each row of logits [M, vocab] fp32 (rows ldl apart, ldl >= vocab) from a given random number:
+ *   w_i = exp((x_i - max x) / temperature);  ranks: the greater logit first, of equal ones the lower id
+ *   K = the top_k first ranks                               (top_k <= 0: all)
+ *   N = the ranks of K before which lies less than top_p of K's sum of w    (top_p >= 1: all of K)
+ *   S = the ranks of N with w_i >= min_p, the largest w being 1             (min_p <= 0: all of N)
+ * S always holds the first rank.  ids[m] is the lowest id of S up to which, ids in order, the sum of S's w exceeds u[m]
+ * times all of it (u >= 1: the last id of S with a weight, u < 0: the first); logprob[m] = ln(w / that sum) of it.
+ * temperature <= 0 takes the first rank, with logprob 0; one below 2^-100 counts as 2^-100.  A logit whose difference to
+ * the largest passes fp32's range weighs 0.
+ * u, temperature, top_k, top_p, min_p: [M] on the device (int32 for top_k, else fp32); the last four, and logprob, may be
+ * NULL (1, 0, 1, 0).  A row that holds a NaN or +inf, or only -inf, or has a NaN among its settings, has no
+ * distribution: id -1, logprob NaN.
+ * Weights are good to 2^-29 of themselves and held as whole multiples of 2^-44, rounded down (a token that weighs less
+ * is never chosen), and their sums are exact: a row's result follows from its logits and settings alone, not from how
+ * the work is split.
+ * Pointers 4-byte aligned, logits' rows too; vocab at most 2^19 (TP_ERR_UNSUPPORTED otherwise).  No workspace.  One kernel
+ * launch.  M == 0 is a no-op. */
+tp_status tp_sample_tokens(const float* logits, int64_t ldl, int32_t M, int32_t vocab, const float* u,
+                           const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                           int32_t* ids, float* logprob, void* stream);
 
 /* Vocabulary-parallel embedding lookup (the table split by vocabulary rows; each shard contributes
  * its row if the id is in its range, else zeros, and the contributions are summed, which leaves

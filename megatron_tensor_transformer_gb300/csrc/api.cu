@@ -1204,6 +1204,30 @@ tp_status tp_paged_attn_decode(const tp_shape* sh, const tp_pages* pages, const 
   return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
 }
 
+size_t tp_prefix_attn_workspace_bytes(const tp_shape* sh, int32_t M) {
+  if (M < 0) return 0;
+  return tp_paged_attn_workspace_bytes(sh);
+}
+
+tp_status tp_prefix_attn_decode(const tp_shape* sh, const tp_pages* pages, const void* q, const void* k_pages,
+                                const void* v_pages, const float* k_scale, const float* v_scale,
+                                const int32_t* block_table, const int32_t* lens, int32_t M, const int32_t* cu_groups,
+                                const int32_t* prefix_lens, int32_t n_groups, float scale, int32_t window, void* o_in,
+                                float* lse, void* ws, size_t ws_bytes, void* stream) {
+  tp_status st = check_shape(sh, TP_W_QKV);
+  if (st == TP_OK) st = check_pages(pages);
+  if (st != TP_OK) return st;
+  if (n_groups < 0 || (M >= 0 && n_groups > M) || (n_groups > 0 && (!cu_groups || !prefix_lens)))
+    return TP_ERR_INVALID_ARG;
+  if (!aligned4(cu_groups) || !aligned4(prefix_lens)) return TP_ERR_ALIGN;
+  PagedAttnArgs a;
+  st = attn_args(sh, pages, q, k_pages, v_pages, k_scale, v_scale, block_table, lens, M, scale, window, o_in, lse, ws,
+                 ws_bytes, &a);
+  if (st != TP_OK || M == 0) return st;
+  if (ws_bytes < tp_prefix_attn_workspace_bytes(sh, M)) return TP_ERR_WORKSPACE;
+  return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
+}
+
 // Workspace of the block: [projections][paged attention].  The attention's part begins where M and the flags end the
 // projections', so a call of another M may have left anything there: the append of the same call zeroes its counters.
 size_t tp_paged_attn_block_workspace_bytes(const tp_shape* sh, int32_t M, uint32_t flags) {
@@ -1262,6 +1286,20 @@ tp_status tp_token_logprobs(const float* logits, int64_t ldl, int32_t M, int32_t
     return TP_ERR_ALIGN;
   LogprobsArgs a{logits, ldl, ids, logprob, entropy, top_logprob, rank, top_id, M, vocab, k};
   return cuda_status(launch_token_logprobs(a, S(stream)));
+}
+
+tp_status tp_sample_tokens(const float* logits, int64_t ldl, int32_t M, int32_t vocab, const float* u,
+                           const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                           int32_t* ids, float* logprob, void* stream) {
+  if (M < 0 || vocab <= 0 || ldl < vocab) return TP_ERR_INVALID_ARG;
+  if (vocab > kSampleMaxVocab) return TP_ERR_UNSUPPORTED;
+  if (M == 0) return TP_OK;
+  if (!logits || !u || !ids) return TP_ERR_INVALID_ARG;
+  if (!aligned4(logits) || !aligned4(u) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) ||
+      !aligned4(min_p) || !aligned4(ids) || !aligned4(logprob))
+    return TP_ERR_ALIGN;
+  const SampleArgs a{logits, ldl, u, temperature, top_p, min_p, top_k, ids, logprob, M, vocab};
+  return cuda_status(launch_sample_tokens(a, S(stream)));
 }
 
 tp_status tp_lm_head_forward(const tp_packed_desc* desc, const void* w, const void* x, int32_t M, float* logits,

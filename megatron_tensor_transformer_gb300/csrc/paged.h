@@ -61,6 +61,18 @@ struct LogprobsArgs {
 };
 cudaError_t launch_token_logprobs(const LogprobsArgs& a, cudaStream_t st);
 
+struct SampleArgs {
+  const float* logits;
+  int64_t ldl;
+  const float *u, *temperature, *top_p, *min_p;  // all but u may be nullptr
+  const int32_t* top_k;
+  int32_t* ids;
+  float* logprob;  // or nullptr
+  int32_t M, vocab;
+};
+constexpr int kSampleMaxVocab = 1 << 19;  // 2^19 weights of at most 2^44 sum below 2^64
+cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t st);
+
 // Launch with programmatic dependent launch allowed: the kernel must wait for the work before it
 // (griddepcontrol.wait) before it reads or writes anything that work may touch.
 template <class K, class... A>

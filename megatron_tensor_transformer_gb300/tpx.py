@@ -33,7 +33,8 @@ EXPORTS = ["tp_packed_bytes", "tp_describe", "tp_partition_weights", "tp_workspa
            "tp_attn_block_workspace_bytes", "tp_attn_block_forward", "tp_quantize_fp8_per_token",
            "tp_paged_tables", "tp_rope_describe", "tp_rope_forward", "tp_rope_append",
            "tp_paged_attn_workspace_bytes", "tp_paged_attn_decode", "tp_paged_attn_block_workspace_bytes",
-           "tp_paged_attn_block_forward", "tp_token_logprobs"]
+           "tp_paged_attn_block_forward", "tp_token_logprobs", "tp_prefix_attn_workspace_bytes",
+           "tp_prefix_attn_decode", "tp_sample_tokens"]
 
 
 class TpxError(RuntimeError):
@@ -127,6 +128,10 @@ def lib():
             "tp_paged_attn_block_forward": (I32, [P(PackedDesc), V, P(PackedDesc), V, V, V, I32, P(Rope), P(Pages), V, V,
                                                   V, V, V, V, V, V, I32, V, V, V, V, V, SZ, U32, V]),
             "tp_token_logprobs": (I32, [V, ctypes.c_int64, I32, I32, V, I32, V, V, V, V, V, V]),
+            "tp_prefix_attn_workspace_bytes": (SZ, [P(Shape), I32]),
+            "tp_prefix_attn_decode": (I32, [P(Shape), P(Pages), V, V, V, V, V, V, V, I32, V, V, I32, ctypes.c_float, I32,
+                                            V, V, V, SZ, V]),
+            "tp_sample_tokens": (I32, [V, ctypes.c_int64, I32, I32, V, V, V, V, V, V, V, V]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -409,6 +414,27 @@ def tp_paged_attn_decode(shape, pages, q, k_pages, v_pages, block_table, lens, o
     return o_in
 
 
+def tp_prefix_attn_workspace_bytes(shape, M):
+    return lib().tp_prefix_attn_workspace_bytes(ctypes.byref(shape), M)
+
+
+def new_prefix_attn_workspace(shape, M, device):
+    """Zero-filled workspace of tp_prefix_attn_decode (its counters start at zero), for calls of up to M requests."""
+    return torch.zeros(max(1, tp_prefix_attn_workspace_bytes(shape, M)), dtype=torch.uint8, device=device)
+
+
+def tp_prefix_attn_decode(shape, pages, q, k_pages, v_pages, block_table, lens, cu_groups, prefix_lens, o_in, ws,
+                          lse=None, scale=0.0, window=0, k_scale=None, v_scale=None, stream=None):
+    """As tp_paged_attn_decode, with the requests cu_groups[g] .. cu_groups[g + 1] - 1 sharing their first
+    prefix_lens[g] positions' whole pages; cu_groups [n + 1], prefix_lens [n]: int32 on the device."""
+    _check(lib().tp_prefix_attn_decode(ctypes.byref(shape), ctypes.byref(pages), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+                                       _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(lens), q.shape[0],
+                                       _ptr(cu_groups), _ptr(prefix_lens), prefix_lens.shape[0], scale, window,
+                                       _ptr(o_in), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+           "tp_prefix_attn_decode")
+    return o_in
+
+
 def tp_paged_attn_block_workspace_bytes(shape, M, flags=0):
     return lib().tp_paged_attn_block_workspace_bytes(ctypes.byref(shape), M, flags)
 
@@ -446,3 +472,15 @@ def tp_token_logprobs(logits, ids, logprob, entropy, rank, top_logprob=None, top
                                    _ptr(rank), _ptr(entropy), _ptr(top_logprob), _ptr(top_id), _stream(stream)),
            "tp_token_logprobs")
     return logprob
+
+
+def tp_sample_tokens(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, stream=None):
+    """logits: [M, vocab] fp32, rows logits.stride(0) apart, a row's logits next to one another; u, temperature, top_p,
+    min_p, logprob: [M] fp32, ids, top_k: [M] int32 (all on the device; the settings and logprob may be None)."""
+    if logits.shape[1] > 1 and logits.stride(1) != 1:
+        raise TpxError(TP_ERR_INVALID_ARG, "tp_sample_tokens: logits' stride along the vocabulary")
+    ldl = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+    _check(lib().tp_sample_tokens(_ptr(logits), ldl, logits.shape[0], logits.shape[1], _ptr(u), _ptr(temperature),
+                                  _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(ids), _ptr(logprob), _stream(stream)),
+           "tp_sample_tokens")
+    return ids

@@ -126,3 +126,47 @@ def logprobs(x, ids, k):
             lp[m], rank[m] = y[ids[m]], int(np.nonzero(order == ids[m])[0][0]) + 1
         ti[m], tl[m] = order[:k], y[order[:k]]
     return lp, rank, ent, tl, ti
+
+
+def shared_by(cu, prefix, M, page, max_pages):
+    """Positions that each row reads through its group's first row, and that row: whole pages of the prefixes of
+    groups of two and more that lie in order within the batch."""
+    out = [(0, m) for m in range(M)]
+    for g, p in enumerate(prefix):
+        a, b = int(cu[g]), int(cu[g + 1])
+        if 0 <= a and a + 2 <= b <= M and 0 <= p <= max_pages * page:
+            for m in range(a, b):
+                out[m] = (int(p) // page * page, a)
+    return out
+
+
+def sample(x, u, T=1.0, k=0, p=1.0, q=0.0, slack=0.0):
+    """One row of logits [V] (fp32 values): ids and logprobs of what may be chosen.  One token where no sum lies within
+    `slack`, relative, of its border; what either side of the border gives where one does."""
+    x = np.asarray(x, np.float64)
+    if np.isnan(x).any() or (x == np.inf).any() or (x == -np.inf).all() or np.isnan([u, T, p, q]).any():
+        return [-1], [np.nan]
+    order = np.lexsort((np.arange(len(x)), -x))
+    if T <= 0:
+        return [int(order[0])], [0.0]
+    w = np.exp((x - x.max()) / max(T, 2.0 ** -100))
+    w[x.max() - x > np.finfo(np.float32).max] = 0
+    ranks = order[:k] if k > 0 else order
+    found = set()
+    for s in ((0.0,) if slack == 0 else (-slack, 0.0, slack)):
+        kept = ranks
+        if p < 1:
+            mass = np.cumsum(w[ranks]) - w[ranks]
+            kept = ranks[(mass < p * (1 + s) * w[ranks].sum()) | (np.arange(len(ranks)) == 0)]
+        if q > 0:
+            kept = kept[(w[kept] >= q) | (np.arange(len(kept)) == 0) | (x[kept] == x.max())]
+        live = np.sort(kept[w[kept] >= 2.0 ** -45])
+        edge = np.cumsum(w[live])
+        for s2 in ((0.0,) if slack == 0 else (-slack, 0.0, slack)):
+            if u >= 1:
+                i = len(live) - 1
+            else:
+                i = int((edge <= max(u, 0.0) * edge[-1] + s2 * edge[-1]).sum()) if u >= 0 else 0
+            i = min(i, len(live) - 1)
+            found.add((int(live[i]), math.log(w[live[i]] / edge[-1])))
+    return [f[0] for f in found], [f[1] for f in found]
