@@ -265,7 +265,8 @@ tp_status attn_args(const tp_shape* sh, const tp_pages* pages, const void* q, co
   *out = PagedAttnArgs{static_cast<const __nv_bfloat16*>(q), k_scale, v_scale, block_table, lens,
                        static_cast<__nv_bfloat16*>(o_in), lse, static_cast<unsigned*>(ws), err, M, sh->t, sh->n_q_heads,
                        sh->n_kv_heads, window, page_shift(pages), pages->n_pages, pages->max_pages, pages->table_stride,
-                       scale == 0.f ? 1.0f / sqrtf((float)sh->head_dim) : scale};
+                       scale == 0.f ? 1.0f / sqrtf((float)sh->head_dim) : scale, nullptr, nullptr, 0, nullptr, nullptr,
+                       nullptr};
   return TP_OK;
 }
 
@@ -1205,8 +1206,8 @@ tp_status tp_paged_attn_decode(const tp_shape* sh, const tp_pages* pages, const 
 }
 
 size_t tp_prefix_attn_workspace_bytes(const tp_shape* sh, int32_t M) {
-  if (M < 0) return 0;
-  return tp_paged_attn_workspace_bytes(sh);
+  if (M < 0 || tp_paged_attn_workspace_bytes(sh) == 0) return 0;
+  return prefix_attn_workspace_bytes(sh->n_q_heads, sh->n_kv_heads, sh->head_dim, M);
 }
 
 tp_status tp_prefix_attn_decode(const tp_shape* sh, const tp_pages* pages, const void* q, const void* k_pages,
@@ -1220,12 +1221,17 @@ tp_status tp_prefix_attn_decode(const tp_shape* sh, const tp_pages* pages, const
   if (n_groups < 0 || (M >= 0 && n_groups > M) || (n_groups > 0 && (!cu_groups || !prefix_lens)))
     return TP_ERR_INVALID_ARG;
   if (!aligned4(cu_groups) || !aligned4(prefix_lens)) return TP_ERR_ALIGN;
+  // (0 for a shape that the attention does not take, which is refused as such below)
+  if (M > 0 && ws_bytes < tp_prefix_attn_workspace_bytes(sh, M)) return TP_ERR_WORKSPACE;
   PagedAttnArgs a;
   st = attn_args(sh, pages, q, k_pages, v_pages, k_scale, v_scale, block_table, lens, M, scale, window, o_in, lse, ws,
                  ws_bytes, &a);
   if (st != TP_OK || M == 0) return st;
-  if (ws_bytes < tp_prefix_attn_workspace_bytes(sh, M)) return TP_ERR_WORKSPACE;
-  return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
+  if (n_groups == 0) return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
+  a.cu_groups = cu_groups;
+  a.prefix_lens = prefix_lens;
+  a.n_groups = n_groups;
+  return cuda_status(launch_prefix_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
 }
 
 // Workspace of the block: [projections][paged attention].  The attention's part begins where M and the flags end the

@@ -42,6 +42,12 @@ struct PagedAttnArgs {
   int32_t M, t, n_q, n_kv, window;
   int32_t page_shift, n_pages, max_pages, table_stride;
   float scale;
+  // Requests that share prefixes (n_groups 0: none): a request leaves what its group shares to launch_prefix_attn.
+  const int32_t *cu_groups, *prefix_lens;
+  int32_t n_groups;
+  // Where not nullptr, in place of o and lse: sum p v [M, n_q, hd], its reference and sum p [M, n_q] (0: nothing
+  // attended to, and the other two may hold anything)
+  float *part_o, *part_ref, *part_l;
 };
 // the largest grid
 constexpr int kPagedMaxCtas = 256;
@@ -50,6 +56,12 @@ constexpr int kPagedCounters = 4 * kPagedMaxCtas;
 size_t paged_attn_workspace_bytes(int G, int hd);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,
                               cudaStream_t st);
+
+// The same over what groups share, the requests' own positions, and the two joined: three launches.  a: with groups,
+// its part_* not set; ws: prefix_attn_workspace_bytes.
+size_t prefix_attn_workspace_bytes(int n_q, int n_kv, int hd, int M);
+cudaError_t launch_prefix_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,
+                               cudaStream_t st);
 
 struct LogprobsArgs {
   const float* logits;

@@ -51,25 +51,16 @@
 // short requests and the SMs' unequal shares of the HBM; and over e4m3 each (request, kv head)'s beginning and end, 2.4
 // us beside 0.7 us a chunk, with 16 heads per kv head 4.4 beside 0.79 (0.73 at the copy's rate).
 #include <cuda.h>
-#include <cuda_fp16.h>
 
 #include <algorithm>
-#include <atomic>
 
-#include "common.cuh"
-#include "paged.h"
+#include "paged_attn.cuh"
 #include "tc.h"
-#include "tc_ptx.cuh"
 
 namespace tpx {
 
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNoRef = -3.402823466e38f;  // no reference yet: fp32's lowest, which every finite score reaches (one
-                                            // that only reaches it is rightly a weight of 1 under it)
-constexpr int kP = 128;                    // positions per chunk: the rows of an MMA
 constexpr int kN = 16;                     // heads of an MMA (its columns)
 constexpr int kMasks = 32;                 // ring of the chunks' masks: above the chunks in flight
 constexpr int kFan = 5;                    // pieces joined at once (131071 tokens: 87.4 us with 5, 89.2 with 8, 90.0 with 24)
@@ -104,14 +95,6 @@ struct PCfg {
   static constexpr size_t SMEM = kRing + 2 * TERMS * PTILE + 2 * QTILE;
   static_assert(NS >= 3, "a chunk's k and v and the next one's k");
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// what a sum taken under reference m counts under the reference mx (0 where nothing was summed)
-__device__ __forceinline__ float weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
 
 // the warp's largest value (a NaN is passed over)
 __device__ __forceinline__ float warp_max(float x) {
@@ -174,13 +157,6 @@ __device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[N]) {
   tc::tmem_st_wait();
 }
 
-// Shared-memory operand descriptor: strides in bytes, layout 2 / 4 / 6 / 0 = 128 / 64 / 32-byte swizzle / none.
-// K-major: `stride` between 8-row groups.  Transposed (rows of k): `stride` between groups of 8 k,
-// `lead` between the blocks of a swizzle row's length along the other side.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t layout) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)((lead >> 4) & 0x3FFFu) << 16 |
-         (uint64_t)((stride >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
-}
 constexpr uint32_t kTransposed = (1u << 15) | (1u << 16);  // instruction descriptor: A and B are rows of k
 
 // named barriers of n threads; any(): whether the predicate holds for one of them
@@ -195,40 +171,10 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool p) {
   return r != 0;
 }
 
-// two floats as e4m3 codes (x in the low byte), and back
-__device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ __half2 e4m3x2_half2(uint32_t v) {
-  return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3));
-}
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t v) { return __half22float2(e4m3x2_half2(v)); }
-
-// The positions [lo, n) a request attends to, in chunks [c0, c1); c0 == c1 if there are none.
-struct Span {
-  int lo, n, c0, c1;
-};
-__device__ __forceinline__ Span span_of(const PagedAttnArgs& a, int m) {
-  Span s{0, a.lens[m], 0, 0};
-  if (s.n < 1 || (long long)s.n > ((long long)a.max_pages << a.page_shift)) return s;
-  if (a.window > 0) s.lo = max(0, s.n - a.window);
-  s.c0 = s.lo / kP;
-  s.c1 = (s.n - 1) / kP + 1;
-  return s;
-}
-
 // Units of a request's (request, kv head)s: `ends`, then two per chunk.
 __device__ __forceinline__ int units_of(const Span& s, int ends) { return s.c0 == s.c1 ? 0 : ends + 2 * (s.c1 - s.c0); }
 // CTA i of nct takes units [U i / nct, U (i + 1) / nct), nct at most U / 2; a chunk belongs to the CTA of its
 // first unit, which is owner(u).
-__device__ __forceinline__ long long quot(long long x, long long y) {  // x / y, both >= 0: a 64-bit division only if it must be
-  return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
-}
-__device__ __forceinline__ long long split_at(long long U, int nct, int i) { return quot(U * i, nct); }
-__device__ __forceinline__ int owner(long long U, int nct, long long u) {
-  return (int)quot((u + 1) * nct + U - 1, U) - 1;
-}
-
 // Chunks [c0, c1) of (m, gg), whose request attends to [lo, n): the piece of CTA blockIdx.x of those that CTAs
 // a .. b leave in slots 2 a + second, 2 (a + 1), .., 2 b.  a == b: the whole of it.  m < 0: no more items.
 struct __align__(16) Item {
@@ -239,28 +185,6 @@ __device__ __forceinline__ uint32_t group_bits(const Item& it, int c, uint32_t l
   const int a0 = max(0, it.lo - c * kP), a1 = min(kP, it.n - c * kP);
   return loaded & ((1u << ((a1 + 15) >> 4)) - 1) & ~((1u << (a0 >> 4)) - 1);
 }
-// A role's bounded waits.  After one that runs out (it sets the error word) the producer issues no more copies and
-// the two issuing threads no more MMAs, and each waits, bounded again, for what it has in flight; the softmax warps
-// go on without waiting to the item's end, so that their team's barriers are met.  Then the kernel ends: no copy
-// lands in shared memory and no MMA in tensor memory that the CTA has given back.
-// (The loop is a function of its own: inlined at every wait it made the roles' code together larger than the
-// SM's instruction cache, and the kernel's time depend on where the compiler put what, by up to a quarter.)
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
-  const bool ok = tc::mbar_wait(bar, parity);
-  if (!ok) atomicExch(err, code);
-  return !ok;
-}
-struct Waits {
-  unsigned* err;
-  unsigned code;
-  bool failed;
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
-    if (tc::mbar_try_wait(bar, parity) || tc::mbar_try_wait(bar, parity)) return true;
-    if (!failed) failed = wait_long(bar, parity, err, code);
-    return !failed;
-  }
-};
-
 // grid: one CTA per SM.  Softmax teams of NG groups of 4 warps; a group's threads hold HPT heads, NG HPT >= n_q / n_kv.
 template <int HD, bool FP8, int HPT, int NG>
 __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
@@ -320,10 +244,12 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
   const int G = a.n_q / a.n_kv, nkvs = a.n_kv / a.t;
 
+  // The requests that share prefixes leave those to another kernel: groups that are not in order are none.
+  const bool groups = a.n_groups > 0 && __syncthreads_and(groups_in_order(a, tid, kThreads));
   // The units: a sum over the requests, a contiguous run of them per thread.
   const int per = (a.M + kThreads - 1) / kThreads, r0 = min(a.M, tid * per), r1 = min(a.M, r0 + per);
   long long here = 0;
-  for (int m = r0; m < r1; ++m) here += (long long)units_of(span_of(a, m), kEnds) * a.n_kv;
+  for (int m = r0; m < r1; ++m) here += (long long)units_of(span_of(a, m, groups), kEnds) * a.n_kv;
   long long base = here;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -345,7 +271,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   if (u0 < u1 && u0 >= base && u0 < base + here) {  // this thread's requests hold unit u0
     int m = r0;
     for (;; ++m) {
-      const long long n = (long long)units_of(span_of(a, m), kEnds) * a.n_kv;
+      const long long n = (long long)units_of(span_of(a, m, groups), kEnds) * a.n_kv;
       if (u0 < base + n) break;
       base += n;
     }
@@ -490,8 +416,12 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   } else if (warp == kPV) {
     // ---- P V: one thread issues.  The warp writes the rows without positions first, while the others begin.
     for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
-      const Span s = span_of(a, m);
+      const Span s = span_of(a, m, groups);
       if (s.c0 != s.c1) continue;
+      if (a.part_o) {
+        for (int i = lane; i < a.n_q; i += 32) a.part_l[(size_t)m * a.n_q + i] = 0.f;
+        continue;
+      }
       uint4* o = reinterpret_cast<uint4*>(a.o + (size_t)m * a.n_q * HD);
       for (int i = lane; i < a.n_q * HD / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
       if (a.lse)
@@ -543,7 +473,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     constexpr int RP = HD / 8;       // 16-byte pieces of a row: 8, 16 or 32 neighbouring lanes
     constexpr int QV = 16 * RP / 32;
     int m = u0 < u1 ? s_m : 0, gg = 0;
-    Span s = u0 < u1 ? span_of(a, m) : Span{0, 0, 0, 0};
+    Span s = u0 < u1 ? span_of(a, m, groups) : Span{0, 0, 0, 0};
     long long at = u0 < u1 ? s_base : 0;  // the first unit of (m, gg)
     int j = 0;
     if (u0 < u1) {  // the head that holds u0
@@ -582,7 +512,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         if (++gg >= a.n_kv || n == 0) {
           gg = 0;
           if (++m >= a.M) at = u1;
-          else s = span_of(a, m);
+          else s = span_of(a, m, groups);
         }
         if (it.m >= 0) break;
       }
@@ -851,12 +781,13 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
 #pragma unroll
             for (int t = C::TERMS - 2; t >= 0; --t) v[w] = ot[w][t][h] + v[w] * (1.f / C::kNext);
           }
-          const float r = !whole ? vs : l[h] == 0.f ? 0.f : __fdividef(vs, l[h]);
+          const float r = !whole || a.part_o ? vs : l[h] == 0.f ? 0.f : __fdividef(vs, l[h]);
           const float o = ((f0[h] == 0.f ? 0.f : v[0] * f0[h]) + (f1[h] == 0.f ? 0.f : v[1] * f1[h])) * r;
           if (h0 + h < G && row < HD) {
             const size_t at = (size_t)(h0 + h) * HD + 128 * nb + row;
-            if (whole) a.o[orow * HD + at] = __float2bfloat16_rn(o);
-            else piece[at] = o;
+            if (!whole) piece[at] = o;
+            else if (a.part_o) a.part_o[orow * HD + at] = o;
+            else a.o[orow * HD + at] = __float2bfloat16_rn(o);
           }
         }
       }
@@ -873,6 +804,9 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
           if (!whole) {
             piece[G * HD + h0 + h] = l[h] == 0.f ? -INFINITY : sub[h];
             piece[G * HD + G + h0 + h] = l[h];
+          } else if (a.part_o) {
+            a.part_ref[orow + h0 + h] = sub[h];
+            a.part_l[orow + h0 + h] = l[h];
           } else if (a.lse) {
             a.lse[orow + h0 + h] = l[h] == 0.f ? -INFINITY : (sub[h] + log2f(l[h])) * kLn2;
           }
@@ -950,6 +884,14 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
             }
             continue;
           }
+          if (a.part_o) {
+            *reinterpret_cast<float4*>(a.part_o + orow * HD + e) = v;
+            if (e % HD == 0) {
+              a.part_ref[orow + e / HD] = M;
+              a.part_l[orow + e / HD] = L;
+            }
+            continue;
+          }
           const float r = L == 0.f ? 0.f : 1.0f / L;
           *reinterpret_cast<uint2*>(a.o + orow * HD + e) =
               make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
@@ -977,18 +919,6 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
 }
 
 inline size_t piece_floats(int G, int hd) { return ((size_t)G * (hd + 2) + 3) / 4 * 4; }
-
-int sm_count() {  // of the current device, asked for once
-  static std::atomic<int> known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 1;
-    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
 
 template <int HD, bool FP8, int HPT, int NG>
 cudaError_t launch(const PagedAttnArgs& a, const void* k_pages, const void* v_pages, cudaStream_t st) {

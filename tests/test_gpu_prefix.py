@@ -153,6 +153,28 @@ def test_prefix_attention_many_groups(dev, M, G):
 
 
 @pytest.mark.parametrize("kv", BOTH)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("chunks", [1, 3, 4])
+def test_prefix_attention_tiles_of_both_kinds_in_turn(dev, kv, hd, chunks):
+    """Every CTA takes several tiles, of two blocks of rows and of one in turn, whole ones and parts: as paged attention
+    of each request by itself, to within the weights' rounding and the outputs'."""
+    groups = [g for _ in range(130) for g in ((9, 128 * chunks - 20), (2, 128 * chunks), (17, 64))]
+    lens = tails(groups, chunks, 40)
+    c = Shared(dev, 1, 64, 4, hd, 16, groups, lens, kv, seed=chunks, poison=False)
+    o, lse = c.launch()
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    pages = tpx.make_pages(16, c.n_pages, c.max_pages, kv, c.table.shape[1])
+    tpx.tp_paged_attn_decode(c.sh, pages, c.q, c.k, c.v, c.table_d, c.lens_d, o2, c.ws, lse=lse2, k_scale=c.ks, v_scale=c.vs)
+    sync()
+    seen = torch.isfinite(lse2)
+    assert torch.equal(seen, torch.isfinite(lse)) and float((lse - lse2)[seen].abs().max()) <= 1e-4
+    a, b = o.float().view(-1, hd), o2.float().view(-1, hd)
+    # row by row: half a step of the weights and of both outputs, against the row's size, with room for unlike signs
+    far = (a - b).norm(dim=1) / b.norm(dim=1).clamp(min=1e-6)
+    assert float(far.max()) <= 6 * HALF, int(far.argmax())
+
+
+@pytest.mark.parametrize("kv", BOTH)
 def test_prefix_attention_rows_by_themselves(dev, kv):
     """Shorter than the shared part, empty, negative, past the table, outside every group: as without sharing."""
     groups = [(6, 400), (3, 300), (2, 64)]
