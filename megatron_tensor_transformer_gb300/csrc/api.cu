@@ -265,8 +265,7 @@ tp_status attn_args(const tp_shape* sh, const tp_pages* pages, const void* q, co
   *out = PagedAttnArgs{static_cast<const __nv_bfloat16*>(q), k_scale, v_scale, block_table, lens,
                        static_cast<__nv_bfloat16*>(o_in), lse, static_cast<unsigned*>(ws), err, M, sh->t, sh->n_q_heads,
                        sh->n_kv_heads, window, page_shift(pages), pages->n_pages, pages->max_pages, pages->table_stride,
-                       scale == 0.f ? 1.0f / sqrtf((float)sh->head_dim) : scale, nullptr, nullptr, 0, nullptr, nullptr,
-                       nullptr};
+                       scale == 0.f ? 1.0f / sqrtf((float)sh->head_dim) : scale};
   return TP_OK;
 }
 
@@ -1223,7 +1222,7 @@ tp_status tp_prefix_attn_decode(const tp_shape* sh, const tp_pages* pages, const
   if (!aligned4(cu_groups) || !aligned4(prefix_lens)) return TP_ERR_ALIGN;
   // (0 for a shape that the attention does not take, which is refused as such below)
   if (M > 0 && ws_bytes < tp_prefix_attn_workspace_bytes(sh, M)) return TP_ERR_WORKSPACE;
-  PagedAttnArgs a;
+  GroupedAttnArgs a{};
   st = attn_args(sh, pages, q, k_pages, v_pages, k_scale, v_scale, block_table, lens, M, scale, window, o_in, lse, ws,
                  ws_bytes, &a);
   if (st != TP_OK || M == 0) return st;
@@ -1231,7 +1230,9 @@ tp_status tp_prefix_attn_decode(const tp_shape* sh, const tp_pages* pages, const
   a.cu_groups = cu_groups;
   a.prefix_lens = prefix_lens;
   a.n_groups = n_groups;
-  return cuda_status(launch_prefix_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
+  a.k_pages = static_cast<const uint8_t*>(k_pages);
+  a.v_pages = static_cast<const uint8_t*>(v_pages);
+  return cuda_status(launch_prefix_attn(a, pages->kv_dtype, sh->head_dim, S(stream)));
 }
 
 // Workspace of the block: [projections][paged attention].  The attention's part begins where M and the flags end the

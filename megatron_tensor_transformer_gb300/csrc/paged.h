@@ -42,12 +42,6 @@ struct PagedAttnArgs {
   int32_t M, t, n_q, n_kv, window;
   int32_t page_shift, n_pages, max_pages, table_stride;
   float scale;
-  // Requests that share prefixes (n_groups 0: none): a request leaves what its group shares to launch_prefix_attn.
-  const int32_t *cu_groups, *prefix_lens;
-  int32_t n_groups;
-  // Where not nullptr, in place of o and lse: sum p v [M, n_q, hd], its reference and sum p [M, n_q] (0: nothing
-  // attended to, and the other two may hold anything)
-  float *part_o, *part_ref, *part_l;
 };
 // the largest grid
 constexpr int kPagedMaxCtas = 256;
@@ -57,11 +51,30 @@ size_t paged_attn_workspace_bytes(int G, int hd);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,
                               cudaStream_t st);
 
-// The same over what groups share, the requests' own positions, and the two joined: three launches.  a: with groups,
-// its part_* not set; ws: prefix_attn_workspace_bytes.
+// Requests that share prefixes.  What a request attends to is split between its group and itself; the parts are sum p v,
+// their reference and sum p (0: nothing attended to, and the other two may hold anything).
+struct GroupedAttnArgs : PagedAttnArgs {
+  const int32_t *cu_groups, *prefix_lens;
+  int32_t n_groups;
+  const uint8_t *k_pages, *v_pages;
+  float *part_o, *part_ref, *part_l;  // the requests' own, where not split: [M, n_q, hd], [M, n_q] twice
+  long long* own_plan;                // units of all requests, CTAs, each request's first unit: for the join
+  float* own_pieces;                  // [2 kTailMaxCtas][own_piece]: [G][hd], [G] twice
+  int32_t own_piece;
+};
+constexpr int kTailMaxCtas = 480;
+constexpr int kTailEnds = 2;  // a run's beginning and end, in stages
+// positions of a stage: 16 KB of k, and of v
+constexpr int tail_positions(int hd, bool fp8) {
+  const int n = 16384 / (hd * (fp8 ? 1 : 2));
+  return n < 128 ? n : 128;
+}
+// launched behind launch_prefix_attn's first kernel, for whose end it does not wait before its own
+cudaError_t launch_tail_attn(const GroupedAttnArgs& a, int kv_dtype, int hd, cudaStream_t st);
+// What groups share, the requests' own positions, and the two joined: three launches.  a: with groups and pages set; ws:
+// prefix_attn_workspace_bytes.
 size_t prefix_attn_workspace_bytes(int n_q, int n_kv, int hd, int M);
-cudaError_t launch_prefix_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,
-                               cudaStream_t st);
+cudaError_t launch_prefix_attn(const GroupedAttnArgs& a, int kv_dtype, int hd, cudaStream_t st);
 
 struct LogprobsArgs {
   const float* logits;

@@ -185,6 +185,28 @@ __device__ __forceinline__ uint32_t group_bits(const Item& it, int c, uint32_t l
   const int a0 = max(0, it.lo - c * kP), a1 = min(kP, it.n - c * kP);
   return loaded & ((1u << ((a1 + 15) >> 4)) - 1) & ~((1u << (a0 >> 4)) - 1);
 }
+// A role's bounded waits.  After one that runs out (it sets the error word) the producer issues no more copies and
+// the two issuing threads no more MMAs, and each waits, bounded again, for what it has in flight; the softmax warps
+// go on without waiting to the item's end, so that their team's barriers are met.  Then the kernel ends: no copy
+// lands in shared memory and no MMA in tensor memory that the CTA has given back.
+// (The loop is a function of its own: inlined at every wait it made the roles' code together larger than the
+// SM's instruction cache, and the kernel's time depend on where the compiler put what, by up to a quarter.)
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
+  const bool ok = tc::mbar_wait(bar, parity);
+  if (!ok) atomicExch(err, code);
+  return !ok;
+}
+struct Waits {
+  unsigned* err;
+  unsigned code;
+  bool failed;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
+    if (tc::mbar_try_wait(bar, parity) || tc::mbar_try_wait(bar, parity)) return true;
+    if (!failed) failed = wait_long(bar, parity, err, code);
+    return !failed;
+  }
+};
+
 // grid: one CTA per SM.  Softmax teams of NG groups of 4 warps; a group's threads hold HPT heads, NG HPT >= n_q / n_kv.
 template <int HD, bool FP8, int HPT, int NG>
 __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
@@ -244,12 +266,10 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
   const int G = a.n_q / a.n_kv, nkvs = a.n_kv / a.t;
 
-  // The requests that share prefixes leave those to another kernel: groups that are not in order are none.
-  const bool groups = a.n_groups > 0 && __syncthreads_and(groups_in_order(a, tid, kThreads));
   // The units: a sum over the requests, a contiguous run of them per thread.
   const int per = (a.M + kThreads - 1) / kThreads, r0 = min(a.M, tid * per), r1 = min(a.M, r0 + per);
   long long here = 0;
-  for (int m = r0; m < r1; ++m) here += (long long)units_of(span_of(a, m, groups), kEnds) * a.n_kv;
+  for (int m = r0; m < r1; ++m) here += (long long)units_of(span_of(a, m), kEnds) * a.n_kv;
   long long base = here;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -271,7 +291,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   if (u0 < u1 && u0 >= base && u0 < base + here) {  // this thread's requests hold unit u0
     int m = r0;
     for (;; ++m) {
-      const long long n = (long long)units_of(span_of(a, m, groups), kEnds) * a.n_kv;
+      const long long n = (long long)units_of(span_of(a, m), kEnds) * a.n_kv;
       if (u0 < base + n) break;
       base += n;
     }
@@ -416,12 +436,8 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
   } else if (warp == kPV) {
     // ---- P V: one thread issues.  The warp writes the rows without positions first, while the others begin.
     for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
-      const Span s = span_of(a, m, groups);
+      const Span s = span_of(a, m);
       if (s.c0 != s.c1) continue;
-      if (a.part_o) {
-        for (int i = lane; i < a.n_q; i += 32) a.part_l[(size_t)m * a.n_q + i] = 0.f;
-        continue;
-      }
       uint4* o = reinterpret_cast<uint4*>(a.o + (size_t)m * a.n_q * HD);
       for (int i = lane; i < a.n_q * HD / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
       if (a.lse)
@@ -473,7 +489,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
     constexpr int RP = HD / 8;       // 16-byte pieces of a row: 8, 16 or 32 neighbouring lanes
     constexpr int QV = 16 * RP / 32;
     int m = u0 < u1 ? s_m : 0, gg = 0;
-    Span s = u0 < u1 ? span_of(a, m, groups) : Span{0, 0, 0, 0};
+    Span s = u0 < u1 ? span_of(a, m) : Span{0, 0, 0, 0};
     long long at = u0 < u1 ? s_base : 0;  // the first unit of (m, gg)
     int j = 0;
     if (u0 < u1) {  // the head that holds u0
@@ -512,7 +528,7 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
         if (++gg >= a.n_kv || n == 0) {
           gg = 0;
           if (++m >= a.M) at = u1;
-          else s = span_of(a, m, groups);
+          else s = span_of(a, m);
         }
         if (it.m >= 0) break;
       }
@@ -781,13 +797,12 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
 #pragma unroll
             for (int t = C::TERMS - 2; t >= 0; --t) v[w] = ot[w][t][h] + v[w] * (1.f / C::kNext);
           }
-          const float r = !whole || a.part_o ? vs : l[h] == 0.f ? 0.f : __fdividef(vs, l[h]);
+          const float r = !whole ? vs : l[h] == 0.f ? 0.f : __fdividef(vs, l[h]);
           const float o = ((f0[h] == 0.f ? 0.f : v[0] * f0[h]) + (f1[h] == 0.f ? 0.f : v[1] * f1[h])) * r;
           if (h0 + h < G && row < HD) {
             const size_t at = (size_t)(h0 + h) * HD + 128 * nb + row;
-            if (!whole) piece[at] = o;
-            else if (a.part_o) a.part_o[orow * HD + at] = o;
-            else a.o[orow * HD + at] = __float2bfloat16_rn(o);
+            if (whole) a.o[orow * HD + at] = __float2bfloat16_rn(o);
+            else piece[at] = o;
           }
         }
       }
@@ -804,9 +819,6 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
           if (!whole) {
             piece[G * HD + h0 + h] = l[h] == 0.f ? -INFINITY : sub[h];
             piece[G * HD + G + h0 + h] = l[h];
-          } else if (a.part_o) {
-            a.part_ref[orow + h0 + h] = sub[h];
-            a.part_l[orow + h0 + h] = l[h];
           } else if (a.lse) {
             a.lse[orow + h0 + h] = l[h] == 0.f ? -INFINITY : (sub[h] + log2f(l[h])) * kLn2;
           }
@@ -881,14 +893,6 @@ __global__ void __launch_bounds__(2 * NG * 128 + 128, 1)
             if (e % HD == 0) {
               dst[G * HD + e / HD] = M;
               dst[G * HD + G + e / HD] = L;
-            }
-            continue;
-          }
-          if (a.part_o) {
-            *reinterpret_cast<float4*>(a.part_o + orow * HD + e) = v;
-            if (e % HD == 0) {
-              a.part_ref[orow + e / HD] = M;
-              a.part_l[orow + e / HD] = L;
             }
             continue;
           }

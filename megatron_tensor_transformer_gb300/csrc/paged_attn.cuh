@@ -43,15 +43,28 @@ __device__ __forceinline__ __half2 e4m3x2_half2(uint32_t v) {
 }
 __device__ __forceinline__ float2 e4m3x2_value(uint32_t v) { return __half22float2(e4m3x2_half2(v)); }
 
+// The positions [lo, n) a request attends to, in chunks [c0, c1); c0 == c1 if there are none.
+struct Span {
+  int lo, n, c0, c1;
+};
+__device__ __forceinline__ Span span_of(const PagedAttnArgs& a, int m) {
+  Span s{0, a.lens[m], 0, 0};
+  if (s.n < 1 || (long long)s.n > ((long long)a.max_pages << a.page_shift)) return s;
+  if (a.window > 0) s.lo = max(0, s.n - a.window);
+  s.c0 = s.lo / kP;
+  s.c1 = (s.n - 1) / kP + 1;
+  return s;
+}
+
 // Positions that a group of `size` rows reads once for all of them: the whole pages of its prefix.  0: none, or too few
 // to matter to any row (a window ends before them all).
-__device__ __forceinline__ int shared_len(const PagedAttnArgs& a, int size, int prefix) {
+__device__ __forceinline__ int shared_len(const GroupedAttnArgs& a, int size, int prefix) {
   if (size < 2 || prefix < 0 || (long long)prefix > ((long long)a.max_pages << a.page_shift)) return 0;
   const int p = prefix >> a.page_shift << a.page_shift;
   return a.window > 0 && p > a.window ? 0 : p;
 }
 // The group of row m, -1: none (cu_groups in order).
-__device__ __forceinline__ int group_of(const PagedAttnArgs& a, int m) {
+__device__ __forceinline__ int group_of(const GroupedAttnArgs& a, int m) {
   int g = 0;
   for (int hi = a.n_groups; g < hi;) {  // the first whose end is behind m
     const int mid = (g + hi) >> 1;
@@ -61,13 +74,13 @@ __device__ __forceinline__ int group_of(const PagedAttnArgs& a, int m) {
   return g < a.n_groups && a.cu_groups[g] <= m ? g : -1;
 }
 // What request m of length n leaves to its group: all of the shared positions, or none.
-__device__ __forceinline__ int left_to_group(const PagedAttnArgs& a, int g, int n) {
+__device__ __forceinline__ int left_to_group(const GroupedAttnArgs& a, int g, int n) {
   if (g < 0) return 0;
   const int p = shared_len(a, a.cu_groups[g + 1] - a.cu_groups[g], a.prefix_lens[g]);
   return n >= p && (a.window <= 0 || n <= a.window) ? p : 0;
 }
 // Whether groups i, i + step, .. lie in order within the batch (to be joined over the threads).
-__device__ __forceinline__ bool groups_in_order(const PagedAttnArgs& a, int i, int step) {
+__device__ __forceinline__ bool groups_in_order(const GroupedAttnArgs& a, int i, int step) {
   bool ok = true;
   for (; i <= a.n_groups; i += step) {
     const int c = a.cu_groups[i];
@@ -76,18 +89,14 @@ __device__ __forceinline__ bool groups_in_order(const PagedAttnArgs& a, int i, i
   return ok;
 }
 
-// The positions [lo, n) a request attends to by itself, in chunks [c0, c1); c0 == c1 if there are none.
-struct Span {
-  int lo, n, c0, c1;
-};
-__device__ __forceinline__ Span span_of(const PagedAttnArgs& a, int m, bool groups) {
-  Span s{0, a.lens[m], 0, 0};
-  if (s.n < 1 || (long long)s.n > ((long long)a.max_pages << a.page_shift)) return s;
-  if (a.window > 0) s.lo = max(0, s.n - a.window);
+// The positions that a request attends to by itself, in chunks of SP.
+template <int SP>
+__device__ __forceinline__ Span own_span(const GroupedAttnArgs& a, int m, bool groups) {
+  Span s = span_of(a, m);
+  if (s.c0 == s.c1) return s;
   if (groups) s.lo = max(s.lo, left_to_group(a, group_of(a, m), s.n));
-  if (s.lo == s.n) return s;
-  s.c0 = s.lo / kP;
-  s.c1 = (s.n - 1) / kP + 1;
+  s.c0 = s.lo / SP;
+  s.c1 = s.lo == s.n ? s.c0 : (s.n - 1) / SP + 1;
   return s;
 }
 
@@ -98,28 +107,6 @@ __device__ __forceinline__ long long split_at(long long U, int nct, int i) { ret
 __device__ __forceinline__ int owner(long long U, int nct, long long u) {
   return (int)quot((u + 1) * nct + U - 1, U) - 1;
 }
-
-// A role's bounded waits.  After one that runs out (it sets the error word) the producer issues no more copies and
-// the two issuing threads no more MMAs, and each waits, bounded again, for what it has in flight; the softmax warps
-// go on without waiting to the item's end, so that their team's barriers are met.  Then the kernel ends: no copy
-// lands in shared memory and no MMA in tensor memory that the CTA has given back.
-// (The loop is a function of its own: inlined at every wait it made the roles' code together larger than the
-// SM's instruction cache, and the kernel's time depend on where the compiler put what, by up to a quarter.)
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
-  const bool ok = tc::mbar_wait(bar, parity);
-  if (!ok) atomicExch(err, code);
-  return !ok;
-}
-struct Waits {
-  unsigned* err;
-  unsigned code;
-  bool failed;
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
-    if (tc::mbar_try_wait(bar, parity) || tc::mbar_try_wait(bar, parity)) return true;
-    if (!failed) failed = wait_long(bar, parity, err, code);
-    return !failed;
-  }
-};
 
 int sm_count() {  // of the current device, asked for once
   static std::atomic<int> known[64];

@@ -47,11 +47,12 @@ struct XCfg {
   static constexpr float kStep = 8.f;                   // ref may be behind the maximum by this, in powers of two
   static constexpr float kPLog = FP8 ? 7.f : 0.f;       // weights are held times 2^this: at most 2^15 in fp16
   // units of work: a chunk of a full tile, of one with up to 128 rows, and a tile's beginning and end
+  static constexpr int OWN = tail_positions(HD, FP8);   // positions of a stage of a request by itself
   static constexpr int kWide = 4, kNarrow = T == 2 ? 3 : 4, kEnds = 8;
 };
 
 struct PrefixArgs {
-  PagedAttnArgs a;
+  GroupedAttnArgs a;
   long long* plan;  // units of all groups, CTAs, then each group's first unit
   float4* whole;    // [n_kv][hd / 4][M G] sum p v of tiles that are not split
   float *whole_ref, *whole_l;  // [n_kv][M G]
@@ -66,7 +67,7 @@ struct Tiles {
   long long per_head;  // units
 };
 template <class C>
-__device__ __forceinline__ Tiles tiles_of(const PagedAttnArgs& a, int g) {
+__device__ __forceinline__ Tiles tiles_of(const GroupedAttnArgs& a, int g) {
   Tiles t{};
   const int size = a.cu_groups[g + 1] - a.cu_groups[g];
   t.len = shared_len(a, size, a.prefix_lens[g]);
@@ -122,12 +123,35 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 template <bool FP8>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if (!FP8) return pack_bf16(lo, hi);
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Waits as in paged_attn.cuh, without a call: registers are dealt out anew by setmaxnreg, and a call's convention knows
+// nothing of it.
+struct Waits {
+  unsigned* err;
+  unsigned code;
+  bool failed;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (!failed && !tc::mbar_wait(bar, parity)) {
+      atomicExch(err, code);
+      failed = true;
+    }
+    return !failed;
+  }
+};
+
 // 16-bit operands (bf16, or fp16 with FP8 pages), fp32 sums
 template <bool FP8>
 __host__ __device__ constexpr uint32_t idesc16(int M, int N) {
@@ -141,19 +165,18 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ PrefixArgs pa) {
   using C = XCfg<HD, FP8>;
-  const PagedAttnArgs& a = pa.a;
+  const GroupedAttnArgs& a = pa.a;
   constexpr int kSoftWarps = 4 * C::T, kProducer = kSoftWarps, kMma = kProducer + 1, kItems = kProducer + 2,
-                kWarps = C::kThreads / 32, kQWarps = 2, kWiden = kProducer + 4;
+                kWarps = C::kThreads / 32, kWiden = kProducer + 4;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;                          // [T][HD / 64][128][128 bytes], swizzled
   uint8_t* ring = smem + C::T * C::QBLOCK;     // [NS] stages
   uint8_t* raw = ring + C::NS * C::STAGE;      // [NR] stages of codes
   __shared__ Tile s_tile[4];
-  __shared__ __align__(8) uint64_t full[C::NS], empty[C::NS], rfull[C::NR + 1], rempty[C::NR + 1], q_full, q_empty,
-      s_full[3], p_full[3], pv_done, o_full[2], o_empty[2], i_full[4], i_empty[4], mma_done;
+  __shared__ __align__(8) uint64_t full[C::NS], empty[C::NS], rfull[C::NR + 1], rempty[C::NR + 1], q_full[2],
+      s_full[3], p_full[3], pv_done, o_full[2], i_full[4], i_empty[4], mma_done;
   __shared__ long long s_part[kWarps], s_base;  // s_base: units before group s_g, which holds the CTA's first one
   __shared__ uint32_t loaded[kMasks];           // 16-position groups of a chunk that were loaded, by bit
-  __shared__ uint8_t q_pow[2][FP8 ? C::ROWS : 1];
   __shared__ uint32_t s_tmem;
   __shared__ int s_g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -167,8 +190,6 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
       tc::mbar_init(B(rfull[i]), 1);
       tc::mbar_init(B(rempty[i]), 4);
     }
-    tc::mbar_init(B(q_full), kQWarps);
-    tc::mbar_init(B(q_empty), 1);
     tc::mbar_init(B(pv_done), 1);
     tc::mbar_init(B(mma_done), 1);
     for (int i = 0; i < 3; ++i) {
@@ -176,12 +197,12 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
       tc::mbar_init(B(p_full[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(B(q_full[i]), 4);
       tc::mbar_init(B(o_full[i]), 1);
-      tc::mbar_init(B(o_empty[i]), 4);
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(B(i_full[i]), 1);
-      tc::mbar_init(B(i_empty[i]), kSoftWarps + 2 + kQWarps - 1 + (FP8 ? 4 : 0));
+      tc::mbar_init(B(i_empty[i]), kSoftWarps + 2 + (FP8 ? 4 : 0));
     }
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&tmK);
@@ -260,232 +281,432 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
   // first block, or even chunks of a tile of one; 1 the odd chunks of those; 2 the second block.
   auto wide = [](const Tile& it) { return C::T == 2 && it.rows > 128; };
 
-  if (warp == kProducer) {
-    // ---- k and v in the order in which the MMAs take them: a stage is SUB-th of a chunk's k or v
-    Waits wait{a.err, 54u, false};
-    const int box_rows = min(1 << a.page_shift, C::KS), nbp = C::KS / box_rows;  // boxes along the positions
-    const int box = lane % nbp, side = lane / nbp;
-    int cnt = 0, kc = 0;
-    struct Rows {  // a chunk's boxes, this lane's of each stage
-      int row[C::SUB];
-      unsigned boxes[C::SUB];
-    };
-    uint8_t* dst = FP8 ? raw : ring;
-    constexpr int kBytes = FP8 ? C::RAW : C::STAGE;
-    uint64_t(&tfull)[FP8 ? C::NR + 1 : C::NS] = *(FP8 ? reinterpret_cast<uint64_t(*)[FP8 ? C::NR + 1 : C::NS]>(&rfull)
-                                                      : reinterpret_cast<uint64_t(*)[FP8 ? C::NR + 1 : C::NS]>(&full));
-    uint64_t(&tempty)[FP8 ? C::NR + 1 : C::NS] = *(FP8 ? reinterpret_cast<uint64_t(*)[FP8 ? C::NR + 1 : C::NS]>(&rempty)
-                                                       : reinterpret_cast<uint64_t(*)[FP8 ? C::NR + 1 : C::NS]>(&empty));
-    auto copy = [&](const CUtensorMap& tm, const Rows& r) {
-#pragma unroll
-      for (int s = 0; s < C::SUB; ++s, ++cnt) {
-        const int st = cnt % C::NT;
-        if (cnt >= C::NT) wait(B(tempty[st]), (cnt / C::NT - 1) & 1);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_expect_tx(B(tfull[st]), __popc(r.boxes[s]) * box_rows * C::INB);
-        __syncwarp();
-        if (r.boxes[s] >> lane & 1)
-          tc::tma_load_2d(tc::smem_u32(dst + (size_t)st * kBytes) + (side * C::KS + box * box_rows) * C::INB, &tm,
-                          side * (C::INB / (FP8 ? 1 : 2)), r.row[s], B(tfull[st]));
+  // The softmax threads hold a row of S: registers go from the other warps to them, where the launch's even share is
+  // too few.  (In sum at most what the block was launched with.)
+  constexpr int kSoftRegs = C::T == 2 ? (FP8 ? 168 : 200) : 0, kRestRegs = FP8 ? 88 : 96;
+  static_assert(128 * C::T * kSoftRegs + (C::kThreads - 128 * C::T) * kRestRegs <= 65536 / C::kThreads / 8 * 8 * C::kThreads,
+                "more registers than the launch has");
+  if (warp < kSoftWarps) {
+    if constexpr (kSoftRegs > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ---- softmax: thread = row
+    Waits wait{a.err, 58u, false};
+    const int x = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    int uses[3] = {0, 0, 0}, kc = 0, pv = 0, done = 0;  // S by barrier, chunks, products of narrow items, items
+    int j = 0;
+    auto next_tile = [&]() {  // the next item that has rows for this block
+      for (;; ++j) {
+        const Tile it = next_item(wait, j, true);
+        if (__any_sync(kFull, it.g < 0)) {
+          Tile none = it;
+          none.g = -1;
+          return none;
+        }
+        if (x == 0 || wide(it)) {
+          ++j;
+          return it;
+        }
+        kc += it.c1 - it.c0;
       }
     };
-    bool stop = false;
-    for (int j = 0; !stop; ++j) {
-      const Tile it = next_item(wait, j, true);
-      if (__any_sync(kFull, it.g < 0)) break;
-      const int pages0 = (it.gg / nkvs) * a.n_pages, gl = it.gg % nkvs;
-      // page ids 32 at a time, one per lane, the next 32 on their way; a chunk's pages never straddle two batches
-      int at = it.c0 * kP >> a.page_shift;
-      auto ids_from = [&](int page) {
-        page += lane;
-        return ((long long)page << a.page_shift) < it.len ? a.table[(size_t)it.m0 * a.table_stride + page] : -1;
-      };
-      int ids = ids_from(at), ids_next = ids_from(at + 32);
-      auto look_up = [&](int c, Rows& r) {
-        if (((c * kP + kP - 1) >> a.page_shift) >= at + 32) {
-          at += 32;
-          ids = ids_next;
-          ids_next = ids_from(at + 32);
-        }
-        unsigned groups = 0;
+    // q's row to shared memory: nothing reads the block's q any more once its last S is there.  Returns 2^e by which
+    // the row was divided.
+    auto bring_q = [&](const Tile& it) {
+      const int r = x * 128 + row, R = it.r0 + min(r, it.rows - 1), m = R / G;
+      const __nv_bfloat16* src = a.q + ((size_t)(it.m0 + m) * a.n_q + (size_t)it.gg * G + (R - m * G)) * HD;
+      uint8_t* dst = sQ + x * C::QBLOCK + row * 128;
+      float pow = 1.f;
+      if (!FP8) {
 #pragma unroll
-        for (int s = 0; s < C::SUB; ++s) {
-          const int pos = c * kP + s * C::KS + box * box_rows;
-          int id = __shfl_sync(kFull, ids, ((pos >> a.page_shift) - at) & 31);
-          if (side >= C::NIB || pos >= it.len) id = -1;
-          r.row[s] = (((pages0 + id) * nkvs + gl) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-          r.boxes[s] = __ballot_sync(kFull, id >= 0 && id < a.n_pages);
-          const unsigned in = __ballot_sync(kFull, lane < C::KS / 16 && (r.boxes[s] >> ((lane * 16 / box_rows) & 31) & 1));
-          groups |= in << (s * (C::KS / 16));
+        for (int c8 = 0; c8 < HD / 8; ++c8)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           tc::smem_u32(dst + (c8 >> 3) * 16384 + (((c8 & 7) ^ (row & 7)) << 4))),
+                       "l"(src + 8 * c8), "r"(r < it.rows ? 16 : 0)
+                       : "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      } else {  // q / 2^e below 2^15, as fp16
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int c8 = 0; c8 < HD / 8; ++c8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * c8);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) top = max(top, max((w[q] >> 7) & 0xffu, (w[q] >> 23) & 0xffu));
         }
-        // seen by who waits for the chunk's k
-        if (lane == 0) loaded[kc % kMasks] = groups;
-        ++kc;
-      };
-      Rows now, next;
-      if (wide(it)) {
-        for (int c = it.c0; c < it.c1 && !stop; ++c) {
-          look_up(c, now);
-          copy(tmK, now);
-          copy(tmV, now);
-          stop = __any_sync(kFull, wait.failed);
-        }
-      } else {
-        look_up(it.c0, now);
-        copy(tmK, now);
-        for (int c = it.c0; c < it.c1 && !stop; ++c) {
-          if (c + 1 < it.c1) {
-            look_up(c + 1, next);
-            copy(tmK, next);
-          }
-          copy(tmV, now);
-          now = next;
-          stop = __any_sync(kFull, wait.failed);
+        // exponent field of the largest value, less 14 for 2^14 <= q / 2^e < 2^15; both factors stay normal
+        const int e = min(max((int)top, 15), 254) - 14;
+        // an infinity makes the row NaN, as its scores would
+        const float inv = top == 255u ? NAN : __uint_as_float((uint32_t)(254 - e) << 23);
+        pow = __uint_as_float((uint32_t)e << 23);
+#pragma unroll 4
+        for (int c8 = 0; c8 < HD / 8; ++c8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * c8);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) h[q] = pack16<true>(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
+          *reinterpret_cast<uint4*>(dst + (c8 >> 3) * 16384 + (((c8 & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
-    }
-    const int last = cnt - 1 - lane;  // copies in flight: each stage's last
-    if (lane < C::NT && last >= 0) wait_long(B(tfull[last % C::NT]), (last / C::NT) & 1, a.err, 54u);
-  } else if (warp == kMma) {
-    // ---- one thread issues all MMAs; they run in the order of issue, so a region of S is written anew behind the
-    // product that read P from it
-    if (lane == 0) {
-      Waits wait{a.err, 55u, false};
-      constexpr uint32_t idS = idesc16<FP8>(128, C::KS), idO = idesc16<FP8>(128, HD) | kBTransposed;
-      const uint32_t qA = tc::smem_u32(sQ), rA = tc::smem_u32(ring);
-      int cnt = 0, kc = 0, uses[3] = {0, 0, 0}, done[2] = {0, 0};  // stages, chunks, S by barrier, blocks' items
-      auto take = [&](int& st) {
-        st = cnt % C::NS;
-        const bool there = wait(B(full[st]), (cnt / C::NS) & 1);
-        ++cnt;
-        return there;
-      };
-      auto scores = [&](int x, int region, int st, int sub) {
-        const uint32_t q0 = qA + x * C::QBLOCK, k0 = rA + st * C::STAGE;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(B(q_full[x]));
+      return pow;
+    };
+    Tile it = next_tile();
+    float pow = it.g >= 0 ? bring_q(it) : 1.f;
+    while (it.g >= 0) {
+      const int n = it.c1 - it.c0;
+      const bool w2 = wide(it);
+      float sc = a.scale * kLog2e * (FP8 && a.k_scale ? a.k_scale[it.gg] : 1.0f) * pow, sub = kNoRef, l = 0.f;
+      const bool flip = sc < 0.f;
+      bool live = false;
+      for (int i = 0; i < n; ++i) {
+        const int region = w2 ? x : i & 1, b = w2 ? 2 * x : i & 1;
+        wait(B(s_full[b]), (b == 0 ? uses[0]++ : b == 1 ? uses[1]++ : uses[2]++) & 1);
+        __syncwarp();
+        tc::tc_fence_after();
+        const uint32_t sA = S_at(region) + lanes;
+        const uint32_t groups = loaded[(kc + i) % kMasks];
+        float s[128];
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i)
-          tc::mma_bf16(S_at(region) + sub * C::KS, smem_desc(q0 + i / 4 * 16384 + i % 4 * 32, 16, 1024, 2),
-                       smem_desc(k0 + i / 4 * (C::KS * 128) + i % 4 * 32, 16, 1024, 2), idS, i > 0);
-      };
-      auto scores_end = [&](int b) {
-        tc::mma_commit(B(s_full[b]));
-        tc::mbar_arrive(B(s_full[b]));  // releases what this thread has seen: the chunk's mask, q's powers
-        b == 0 ? ++uses[0] : b == 1 ? ++uses[1] : ++uses[2];
-      };
-      auto values = [&](int x, int region, int st, int sub, uint32_t groups, bool& live) {
-        const uint32_t v0 = rA + st * C::STAGE;
+        for (int c = 0; c < 128; c += 32) tmem_ld32(sA + c, s + c);
+        landed(s);
+        if (groups != 0xffu) {
+          const float out = flip ? INFINITY : -INFINITY;
 #pragma unroll
-        for (int i = 0; i < C::KS / 16; ++i) {
-          const int step = sub * (C::KS / 16) + i;
-          if (!(groups >> step & 1)) continue;  // what was not loaded may hold anything
-          tc::mma_bf16_tmem_a(O_at(x), S_at(region) + 8 * step, smem_desc(v0 + i * 2048, C::KS * 128, 1024, 2), idO, live);
-          live = true;
+          for (int c = 0; c < 128; ++c) s[c] = groups >> (c / 16) & 1 ? s[c] : out;
         }
-      };
-      for (int j = 0;; ++j) {
-        const Tile it = next_item(wait, j, false);
-        if (it.g < 0) break;
-        if (!wait(B(q_full), j & 1)) break;
-        const int n = it.c1 - it.c0;
-        bool live[2] = {false, false};
-        int st, sv;
-        if (wide(it)) {
-          if (!take(st)) goto mma_end;
-          tc::tc_fence_after();
+        float top;
+        if (!flip) {
+          float t4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            scores(x, x, st, 0);
-            scores_end(2 * x);
-          }
-          tc::mma_commit(B(empty[st]));
-          if (n == 1) tc::mma_commit(B(q_empty));
-          for (int i = 0; i < n; ++i) {
-            if (!take(sv)) goto mma_end;
-            const uint32_t groups = loaded[(kc + i) % kMasks];
+          for (int c = 4; c < 124; c += 8)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (!wait(B(p_full[2 * x]), (uses[2 * x] - 1) & 1)) goto mma_end;
-              if (i == 0 && done[x] > 0 && !wait(B(o_empty[x]), (done[x] - 1) & 1)) goto mma_end;
+            for (int q = 0; q < 4; ++q) t4[q] = fmaxf(t4[q], fmaxf(s[c + q], s[c + 4 + q]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) t4[q] = fmaxf(t4[q], s[124 + q]);
+          top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        } else {
+          top = s[0];
+#pragma unroll
+          for (int c = 1; c < 128; ++c) top = fminf(top, s[c]);
+        }
+        top = __fmul_rn(top, sc);
+        const bool raise = top > sub + (C::kStep + C::kPLog);
+        if (__any_sync(kFull, raise)) {  // a new reference: the maximum so far
+          const float to = raise ? fmaxf(sub, top - C::kPLog) : sub, f = ex2(sub - to);  // from kNoRef: of a sum that is 0
+          l *= f;
+          sub = to;
+          if (live) {
+            if (!w2) {
+              wait(B(pv_done), (pv + i - 1) & 1);
+              __syncwarp();
               tc::tc_fence_after();
-              values(x, x, sv, 0, groups, live[x]);
-              if (x == 1) tc::mma_commit(B(empty[sv]));
-              if (i + 1 < n) {
-                if (x == 0 && !take(st)) goto mma_end;
-                tc::tc_fence_after();
-                scores(x, x, st, 0);
-                scores_end(2 * x);
-                if (x == 1) {
-                  tc::mma_commit(B(empty[st]));
-                  if (i + 2 == n) tc::mma_commit(B(q_empty));
-                }
-              } else {
-                tc::mma_commit(B(o_full[x]));
-                ++done[x];
-              }
             }
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              float o[16];
+              tc::tmem_ld16(O_at(x) + lanes + c, o);
+              landed(o);
+              uint32_t y[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) y[q] = __float_as_uint(o[q] * f);
+              tmem_st16(O_at(x) + lanes + c, y);
+            }
+          }
+        }
+        // s sc - sub, rounded once: what sub's own rounding adds is the same for all of the row's weights under it, and
+        // divides out.  Beyond 2^20 it could be large: there the product is rounded by itself.
+        const bool far = !(fabsf(sub) < 1048576.f), any_far = __any_sync(kFull, far);
+        if (any_far) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) s[c] = far ? __fmul_rn(s[c], sc) - sub : fmaf(s[c], sc, -sub);
+        } else {
+          const float2 sc2 = make_float2(sc, sc), sub2 = make_float2(-sub, -sub);
+#pragma unroll
+          for (int c = 0; c < 128; c += 2) {
+            const float2 y = fma2(make_float2(s[c], s[c + 1]), sc2, sub2);
+            s[c] = y.x;
+            s[c + 1] = y.y;
+          }
+        }
+        float2 l2[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          uint32_t p[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float2 y = make_float2(ex2(s[32 * part + 2 * q]), ex2(s[32 * part + 2 * q + 1]));
+            l2[q & 1] = add2(l2[q & 1], y);
+            p[q] = pack16<FP8>(y.x, y.y);
+          }
+          tmem_st16(sA + 16 * part, p);  // over S, which is in registers
+        }
+        l = (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
+        tc::tmem_st_wait();
+        live |= groups != 0;
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(B(p_full[b]));
+      }
+      kc += n;
+      if (!w2) pv += n;
+
+      // The next item's q, then the item's end: O to the joining kernel, a float4 of dims after the other with the rows
+      // side by side.  (P for the next item is written behind this: until then its P V leaves O alone.)
+      const Tile next = next_tile();
+      if (next.g >= 0) pow = bring_q(next);
+      wait(B(o_full[x]), done++ & 1);
+      __syncwarp();
+      tc::tc_fence_after();
+      const float vs = FP8 && a.v_scale ? a.v_scale[it.gg] : 1.0f;
+      const int r = x * 128 + row, RT = a.M * G, R = it.m0 * G + it.r0 + r;
+      const bool whole = it.a == it.b, there = r < it.rows;
+      float* piece = pa.pieces + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == it.a ? it.second : 0)) * pa.piece;
+      float4* dst = whole ? pa.whole + (size_t)it.gg * (HD / 4) * RT + R : reinterpret_cast<float4*>(piece) + r;
+      const size_t step = whole ? RT : pa.rows;
+      if (live) {
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          tmem_ld32(O_at(x) + lanes + c, o);
+          landed(o);
+          if (there) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[(c / 4 + q) * step] = make_float4(o[4 * q] * vs, o[4 * q + 1] * vs, o[4 * q + 2] * vs, o[4 * q + 3] * vs);
+          }
+        }
+      }
+      if (there) {
+        float* refs = whole ? pa.whole_ref + (size_t)it.gg * RT + R : piece + (size_t)pa.rows * HD + r;
+        float* sums = whole ? pa.whole_l + (size_t)it.gg * RT + R : piece + (size_t)pa.rows * (HD + 1) + r;
+        *refs = sub;
+        *sums = l;
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      it = next;
+    }
+  } else {
+    if constexpr (kSoftRegs > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+    if (warp == kProducer) {
+      // ---- k and v in the order in which the MMAs take them: a stage is SUB-th of a chunk's k or v
+      Waits wait{a.err, 54u, false};
+      const int box_rows = min(1 << a.page_shift, C::KS), nbp = C::KS / box_rows;  // boxes along the positions
+      const int box = lane % nbp, side = lane / nbp;
+      int cnt = 0, kc = 0;
+      struct Rows {  // a chunk's boxes, this lane's of each stage
+        int row[C::SUB];
+        unsigned boxes[C::SUB];
+      };
+      uint8_t* dst = FP8 ? raw : ring;
+      constexpr int kBytes = FP8 ? C::RAW : C::STAGE;
+      uint64_t(&tfull)[FP8 ? C::NR + 1 : C::NS] = *(FP8 ? reinterpret_cast<uint64_t(*)[FP8 ? C::NR + 1 : C::NS]>(&rfull)
+                                                        : reinterpret_cast<uint64_t(*)[FP8 ? C::NR + 1 : C::NS]>(&full));
+      uint64_t(&tempty)[FP8 ? C::NR + 1 : C::NS] = *(FP8 ? reinterpret_cast<uint64_t(*)[FP8 ? C::NR + 1 : C::NS]>(&rempty)
+                                                         : reinterpret_cast<uint64_t(*)[FP8 ? C::NR + 1 : C::NS]>(&empty));
+      auto copy = [&](const CUtensorMap& tm, const Rows& r) {
+#pragma unroll
+        for (int s = 0; s < C::SUB; ++s, ++cnt) {
+          const int st = cnt % C::NT;
+          if (cnt >= C::NT) wait(B(tempty[st]), (cnt / C::NT - 1) & 1);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_expect_tx(B(tfull[st]), __popc(r.boxes[s]) * box_rows * C::INB);
+          __syncwarp();
+          if (r.boxes[s] >> lane & 1)
+            tc::tma_load_2d(tc::smem_u32(dst + (size_t)st * kBytes) + (side * C::KS + box * box_rows) * C::INB, &tm,
+                            side * (C::INB / (FP8 ? 1 : 2)), r.row[s], B(tfull[st]));
+        }
+      };
+      bool stop = false;
+      for (int j = 0; !stop; ++j) {
+        const Tile it = next_item(wait, j, true);
+        if (__any_sync(kFull, it.g < 0)) break;
+        const int pages0 = (it.gg / nkvs) * a.n_pages, gl = it.gg % nkvs;
+        // page ids 32 at a time, one per lane, the next 32 on their way; a chunk's pages never straddle two batches
+        int at = it.c0 * kP >> a.page_shift;
+        auto ids_from = [&](int page) {
+          page += lane;
+          return ((long long)page << a.page_shift) < it.len ? a.table[(size_t)it.m0 * a.table_stride + page] : -1;
+        };
+        int ids = ids_from(at), ids_next = ids_from(at + 32);
+        auto look_up = [&](int c, Rows& r) {
+          if (((c * kP + kP - 1) >> a.page_shift) >= at + 32) {
+            at += 32;
+            ids = ids_next;
+            ids_next = ids_from(at + 32);
+          }
+          unsigned groups = 0;
+#pragma unroll
+          for (int s = 0; s < C::SUB; ++s) {
+            const int pos = c * kP + s * C::KS + box * box_rows;
+            int id = __shfl_sync(kFull, ids, ((pos >> a.page_shift) - at) & 31);
+            if (side >= C::NIB || pos >= it.len) id = -1;
+            r.row[s] = (((pages0 + id) * nkvs + gl) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+            r.boxes[s] = __ballot_sync(kFull, id >= 0 && id < a.n_pages);
+            const unsigned in = __ballot_sync(kFull, lane < C::KS / 16 && (r.boxes[s] >> ((lane * 16 / box_rows) & 31) & 1));
+            groups |= in << (s * (C::KS / 16));
+          }
+          // seen by who waits for the chunk's k
+          if (lane == 0) loaded[kc % kMasks] = groups;
+          ++kc;
+        };
+        Rows now, next;
+        if (wide(it)) {
+          for (int c = it.c0; c < it.c1 && !stop; ++c) {
+            look_up(c, now);
+            copy(tmK, now);
+            copy(tmV, now);
+            stop = __any_sync(kFull, wait.failed);
           }
         } else {
-          auto next_scores = [&](int i) {
-            for (int sub = 0; sub < C::SUB; ++sub) {
-              if (!take(st)) return false;
-              tc::tc_fence_after();
-              scores(0, i & 1, st, sub);
-              tc::mma_commit(B(empty[st]));
+          look_up(it.c0, now);
+          copy(tmK, now);
+          for (int c = it.c0; c < it.c1 && !stop; ++c) {
+            if (c + 1 < it.c1) {
+              look_up(c + 1, next);
+              copy(tmK, next);
             }
-            scores_end(i & 1);
-            if (i + 1 == n) tc::mma_commit(B(q_empty));
-            return true;
-          };
-          if (!next_scores(0)) goto mma_end;
-          for (int i = 0; i < n; ++i) {
-            const int p_use = (i & 1 ? uses[1] : uses[0]) - 1;
-            if (i + 1 < n && !next_scores(i + 1)) goto mma_end;
-            if (!wait(B(p_full[i & 1]), p_use & 1)) goto mma_end;
-            if (i == 0 && done[0] > 0 && !wait(B(o_empty[0]), (done[0] - 1) & 1)) goto mma_end;
-            const uint32_t groups = loaded[(kc + i) % kMasks];
-            for (int sub = 0; sub < C::SUB; ++sub) {
-              if (!take(sv)) goto mma_end;
-              tc::tc_fence_after();
-              values(0, i & 1, sv, sub, groups, live[0]);
-              tc::mma_commit(B(empty[sv]));
-            }
-            tc::mma_commit(B(pv_done));
+            copy(tmV, now);
+            now = next;
+            stop = __any_sync(kFull, wait.failed);
           }
-          tc::mma_commit(B(o_full[0]));
-          ++done[0];
         }
-        kc += n;
       }
+      const int last = cnt - 1 - lane;  // copies in flight: each stage's last
+      if (lane < C::NT && last >= 0) if (!tc::mbar_wait(B(tfull[last % C::NT]), (last / C::NT) & 1)) atomicExch(a.err, 54u);
+    } else if (warp == kMma) {
+      // ---- one thread issues all MMAs; they run in the order of issue, so a region of S is written anew behind the
+      // product that read P from it
+      if (lane == 0) {
+        Waits wait{a.err, 55u, false};
+        constexpr uint32_t idS = idesc16<FP8>(128, C::KS), idO = idesc16<FP8>(128, HD) | kBTransposed;
+        const uint32_t qA = tc::smem_u32(sQ), rA = tc::smem_u32(ring);
+        int cnt = 0, kc = 0, uses[3] = {0, 0, 0}, done[2] = {0, 0};  // stages, chunks, S by barrier, blocks' items
+        auto take = [&](int& st) {
+          st = cnt % C::NS;
+          const bool there = wait(B(full[st]), (cnt / C::NS) & 1);
+          ++cnt;
+          return there;
+        };
+        auto scores = [&](int x, int region, int st, int sub) {
+          const uint32_t q0 = qA + x * C::QBLOCK, k0 = rA + st * C::STAGE;
+#pragma unroll 1
+          for (int b = 0; b < HD / 64; ++b)  // 64 dims: a row of 128 bytes
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tc::mma_bf16(S_at(region) + sub * C::KS, smem_desc(q0 + b * 16384 + i * 32, 16, 1024, 2),
+                           smem_desc(k0 + b * (C::KS * 128) + i * 32, 16, 1024, 2), idS, b + i > 0);
+        };
+        auto scores_end = [&](int b) {
+          tc::mma_commit(B(s_full[b]));
+          tc::mbar_arrive(B(s_full[b]));  // releases what this thread has seen: the chunk's mask, q's powers
+          b == 0 ? ++uses[0] : b == 1 ? ++uses[1] : ++uses[2];
+        };
+        auto values = [&](int x, int region, int st, int sub, uint32_t groups, bool& live) {
+          const uint32_t v0 = rA + st * C::STAGE;
+#pragma unroll 1
+          for (int i = 0; i < C::KS / 16; ++i) {
+            const int step = sub * (C::KS / 16) + i;
+            if (!(groups >> step & 1)) continue;  // what was not loaded may hold anything
+            tc::mma_bf16_tmem_a(O_at(x), S_at(region) + 8 * step, smem_desc(v0 + i * 2048, C::KS * 128, 1024, 2), idO, live);
+            live = true;
+          }
+        };
+        for (int j = 0;; ++j) {
+          const Tile it = next_item(wait, j, false);
+          if (it.g < 0) break;
+          if (!wait(B(q_full[0]), done[0] & 1)) break;
+          if (wide(it) && !wait(B(q_full[1]), done[1] & 1)) break;
+          const int n = it.c1 - it.c0;
+          bool live[2] = {false, false};
+          int st, sv;
+          if (wide(it)) {
+            if (!take(st)) goto mma_end;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              scores(x, x, st, 0);
+              scores_end(2 * x);
+            }
+            tc::mma_commit(B(empty[st]));
+            for (int i = 0; i < n; ++i) {
+              if (!take(sv)) goto mma_end;
+              const uint32_t groups = loaded[(kc + i) % kMasks];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                if (!wait(B(p_full[2 * x]), (uses[2 * x] - 1) & 1)) goto mma_end;
+                tc::tc_fence_after();
+                values(x, x, sv, 0, groups, live[x]);
+                if (x == 1) tc::mma_commit(B(empty[sv]));
+                if (i + 1 < n) {
+                  if (x == 0 && !take(st)) goto mma_end;
+                  tc::tc_fence_after();
+                  scores(x, x, st, 0);
+                  scores_end(2 * x);
+                  if (x == 1) tc::mma_commit(B(empty[st]));
+                } else {
+                  tc::mma_commit(B(o_full[x]));
+                  ++done[x];
+                }
+              }
+            }
+          } else {
+            auto next_scores = [&](int i) {
+              for (int sub = 0; sub < C::SUB; ++sub) {
+                if (!take(st)) return false;
+                tc::tc_fence_after();
+                scores(0, i & 1, st, sub);
+                tc::mma_commit(B(empty[st]));
+              }
+              scores_end(i & 1);
+              return true;
+            };
+            if (!next_scores(0)) goto mma_end;
+            for (int i = 0; i < n; ++i) {
+              const int p_use = (i & 1 ? uses[1] : uses[0]) - 1;
+              if (i + 1 < n && !next_scores(i + 1)) goto mma_end;
+              if (!wait(B(p_full[i & 1]), p_use & 1)) goto mma_end;
+              const uint32_t groups = loaded[(kc + i) % kMasks];
+              for (int sub = 0; sub < C::SUB; ++sub) {
+                if (!take(sv)) goto mma_end;
+                tc::tc_fence_after();
+                values(0, i & 1, sv, sub, groups, live[0]);
+                tc::mma_commit(B(empty[sv]));
+              }
+              tc::mma_commit(B(pv_done));
+            }
+            tc::mma_commit(B(o_full[0]));
+            ++done[0];
+          }
+          kc += n;
+        }
     mma_end:
-      tc::mma_commit(B(mma_done));  // the MMAs in flight
-      wait_long(B(mma_done), 0, a.err, 55u);
-    }
-    __syncwarp();
-  } else if (warp == kItems || warp == kItems + 1) {
-    // ---- items (the first of the two warps), and the q of each
-    Waits wait{a.err, 56u, false};
-    constexpr int RP = HD / 8;  // 16-byte pieces of a row of q
-    const bool first = warp == kItems;
-    const int qt = tid - kItems * 32;
-    int g = first && u0 < u1 ? s_g : 0, gg = 0, tile = 0;
-    long long at = first && u0 < u1 ? s_base : 0;  // the first unit of the tile
-    Tiles ts{};
-    int j = 0;
-    if (first && u0 < u1) {  // the tile that holds u0
-      ts = tiles_of<C>(a, g);
-      gg = (int)quot(u0 - at, ts.per_head);
-      at += (long long)gg * ts.per_head;
-      if (ts.full) {
-        const long long one = C::kEnds + (C::T == 2 ? C::kWide : C::kNarrow) * (long long)ts.chunks;
-        tile = (int)min((long long)ts.full, quot(u0 - at, one));
-        if (tile == ts.full && !ts.rest) --tile;  // (cannot be: u0 is before the head's end)
-        at += tile * one;
+        tc::mma_commit(B(mma_done));  // the MMAs in flight
+        if (!tc::mbar_wait(B(mma_done), 0)) atomicExch(a.err, 55u);
       }
-    }
-    for (;; ++j) {
-      Tile it{};
-      it.g = -1;
-      if (first) {
+      __syncwarp();
+    } else if (warp == kItems) {
+      // ---- items
+      Waits wait{a.err, 56u, false};
+      int g = u0 < u1 ? s_g : 0, gg = 0, tile = 0;
+      long long at = u0 < u1 ? s_base : u1;  // the first unit of the tile
+      Tiles ts{};
+      if (u0 < u1) {  // the tile that holds u0
+        ts = tiles_of<C>(a, g);
+        gg = (int)quot(u0 - at, ts.per_head);
+        at += (long long)gg * ts.per_head;
+        if (ts.full) {
+          const long long one = C::kEnds + (C::T == 2 ? C::kWide : C::kNarrow) * (long long)ts.chunks;
+          tile = (int)min((long long)ts.full, quot(u0 - at, one));
+          at += tile * one;
+        }
+      }
+      for (int j = 0;; ++j) {
+        Tile it{};
+        it.g = -1;
         if (__any_sync(kFull, wait.failed)) at = u1;  // for all lanes
         while (at < u1) {
           const int ntiles = ts.full + (ts.rest > 0), ch = ts.chunks;
@@ -529,247 +750,50 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
           s_tile[j & 3] = it;
           tc::mbar_arrive(B(i_full[j & 3]));
         }
-      } else {
-        it = next_item(wait, j, true);
+        if (it.g < 0) break;
       }
-      if (__any_sync(kFull, it.g < 0)) break;
-      if (j >= 1) wait(B(q_empty), (j - 1) & 1);
-      __syncwarp();
-      const int blocks = wide(it) ? 2 : 1;
-      auto q_row = [&](int r) {  // row r of the tile
-        const int R = it.r0 + r, m = R / G;
-        return a.q + ((size_t)(it.m0 + m) * a.n_q + (size_t)it.gg * G + (R - m * G)) * HD;
-      };
-      auto q_at = [&](int r, int c8) {
-        return sQ + (r >> 7) * C::QBLOCK + (c8 >> 3) * 16384 + (r & 127) * 128 + (((c8 & 7) ^ (r & 7)) << 4);
-      };
-      if (!FP8) {
-        for (int i = qt; i < blocks * 128 * RP; i += 32 * kQWarps) {
-          const int r = i / RP, c8 = i % RP;
-          const void* src = q_row(min(r, it.rows - 1)) + 8 * c8;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(q_at(r, c8))), "l"(src),
-                       "r"(r < it.rows ? 16 : 0)
-                       : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-      } else {
-        for (int i = qt; i < blocks * 128 * RP; i += 32 * kQWarps) {  // q / 2^e below 2^15, as fp16
-          const int r = i / RP, c8 = i % RP;
-          const uint4 v = r < it.rows ? *reinterpret_cast<const uint4*>(q_row(r) + 8 * c8) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t top = 0, h[4];
+    } else if (FP8 && warp >= kWiden) {
+      // ---- codes to fp16, a stage after the other: thread = position (and half of the dims for stages of 64)
+      Waits wait{a.err, 57u, false};
+      const int wt = tid - kWiden * 32, r = wt % C::KS;
+      int cnt = 0;
+      for (int j = 0;; ++j) {
+        const Tile it = next_item(wait, j, true);
+        if (__any_sync(kFull, it.g < 0)) break;
+        for (int f = 0; f < 2 * C::SUB * (it.c1 - it.c0); ++f, ++cnt) {
+          const int rs = cnt % max(1, C::NR), ws = cnt % C::NS;
+          wait(B(rfull[rs]), (cnt / max(1, C::NR)) & 1);
+          if (cnt >= C::NS) wait(B(empty[ws]), (cnt / C::NS - 1) & 1);
+          if (__any_sync(kFull, wait.failed)) goto widen_end;
+          const uint8_t* src = raw + (size_t)rs * C::RAW + r * C::INB;
+          uint8_t* dst = ring + (size_t)ws * C::STAGE + r * 128;
+          constexpr int kUnits = HD / 16 / (128 / C::KS);  // 16 codes each
 #pragma unroll
-          for (int q = 0; q < 4; ++q) top = max(top, max((w[q] >> 7) & 0xffu, (w[q] >> 23) & 0xffu));
+          for (int i = 0; i < kUnits; ++i) {
+            const int u = i + (wt / C::KS) * kUnits, side = u / (C::INB / 16), p = u % (C::INB / 16);
+            const int at = C::INB == 128 ? p ^ (r & 7) : p ^ ((r >> 1) & 3);
+            const uint4 v = *reinterpret_cast<const uint4*>(src + side * (C::KS * C::INB) + (at << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[8];
 #pragma unroll
-          for (int o = 1; o < RP; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-          // exponent field of the largest value, less 14 for 2^14 <= q / 2^e < 2^15; both factors stay normal
-          const int e = min(max((int)top, 15), 254) - 14;
-          // an infinity makes the row NaN, as its scores would
-          const float inv = top == 255u ? NAN : __uint_as_float((uint32_t)(254 - e) << 23);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) h[q] = pack16<true>(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
-          *reinterpret_cast<uint4*>(q_at(r, c8)) = make_uint4(h[0], h[1], h[2], h[3]);
-          if (c8 == 0) q_pow[j & 1][r] = (uint8_t)e;
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(B(q_full));
-    }
-  } else if (FP8 && warp >= kWiden) {
-    // ---- codes to fp16, a stage after the other: thread = position (and half of the dims for stages of 64)
-    Waits wait{a.err, 57u, false};
-    const int wt = tid - kWiden * 32, r = wt % C::KS;
-    int cnt = 0;
-    for (int j = 0;; ++j) {
-      const Tile it = next_item(wait, j, true);
-      if (__any_sync(kFull, it.g < 0)) break;
-      for (int f = 0; f < 2 * C::SUB * (it.c1 - it.c0); ++f, ++cnt) {
-        const int rs = cnt % max(1, C::NR), ws = cnt % C::NS;
-        wait(B(rfull[rs]), (cnt / max(1, C::NR)) & 1);
-        if (cnt >= C::NS) wait(B(empty[ws]), (cnt / C::NS - 1) & 1);
-        if (__any_sync(kFull, wait.failed)) goto widen_end;
-        const uint8_t* src = raw + (size_t)rs * C::RAW + r * C::INB;
-        uint8_t* dst = ring + (size_t)ws * C::STAGE + r * 128;
-        constexpr int kUnits = HD / 16 / (128 / C::KS);  // 16 codes each
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-          const int u = i + (wt / C::KS) * kUnits, side = u / (C::INB / 16), p = u % (C::INB / 16);
-          const int at = C::INB == 128 ? p ^ (r & 7) : p ^ ((r >> 1) & 3);
-          const uint4 v = *reinterpret_cast<const uint4*>(src + side * (C::KS * C::INB) + (at << 4));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const __half2 x = e4m3x2_half2((w[q >> 1] >> (16 * (q & 1))) & 0xffffu);
-            h[q] = *reinterpret_cast<const uint32_t*>(&x);
+            for (int q = 0; q < 8; ++q) {
+              const __half2 x = e4m3x2_half2((w[q >> 1] >> (16 * (q & 1))) & 0xffffu);
+              h[q] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            uint8_t* to = dst + (u >> 2) * (C::KS * 128);
+            const int p16 = 2 * (u & 3);
+            *reinterpret_cast<uint4*>(to + ((p16 ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(to + (((p16 + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
           }
-          uint8_t* to = dst + (u >> 2) * (C::KS * 128);
-          const int p16 = 2 * (u & 3);
-          *reinterpret_cast<uint4*>(to + ((p16 ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(to + (((p16 + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(B(full[ws]));
-          tc::mbar_arrive(B(rempty[rs]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(B(full[ws]));
+            tc::mbar_arrive(B(rempty[rs]));
+          }
         }
       }
-    }
   widen_end:;
-  } else if (warp < kSoftWarps) {
-    // ---- softmax: thread = row
-    Waits wait{a.err, 58u, false};
-    const int x = warp >> 2, row = tid & 127;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    int uses[3] = {0, 0, 0}, kc = 0, pv = 0, done = 0;  // S by barrier, chunks, products of narrow items, items
-    for (int j = 0;; ++j) {
-      const Tile it = next_item(wait, j, true);
-      if (__any_sync(kFull, it.g < 0)) break;
-      const int n = it.c1 - it.c0;
-      const bool w2 = wide(it);
-      if (x == 1 && !w2) {
-        kc += n;
-        continue;
-      }
-      float sc = a.scale * kLog2e * (FP8 && a.k_scale ? a.k_scale[it.gg] : 1.0f), sub = kNoRef, l = 0.f;
-      const bool flip = sc < 0.f;
-      bool live = false;
-      for (int i = 0; i < n; ++i) {
-        const int region = w2 ? x : i & 1, b = w2 ? 2 * x : i & 1;
-        wait(B(s_full[b]), (b == 0 ? uses[0]++ : b == 1 ? uses[1]++ : uses[2]++) & 1);
-        __syncwarp();
-        tc::tc_fence_after();
-        if (FP8 && i == 0) sc *= __uint_as_float((uint32_t)q_pow[j & 1][x * 128 + row] << 23);
-        const uint32_t sA = S_at(region) + lanes;
-        const uint32_t groups = loaded[(kc + i) % kMasks];
-        // the maximum, 64 positions at a time
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 128; c += 64) {
-          float s[64];
-          tmem_ld32(sA + c, s);
-          tmem_ld32(sA + c + 32, s + 32);
-          landed(s);
-          if (flip) {
-#pragma unroll
-            for (int q = 0; q < 64; ++q) s[q] = -s[q];
-          }
-          if (groups != 0xffu) {
-#pragma unroll
-            for (int q = 0; q < 64; ++q) s[q] = groups >> ((c + q) / 16) & 1 ? s[q] : -INFINITY;
-          }
-          float t4[4] = {top, s[61], s[62], s[63]};
-#pragma unroll
-          for (int q = 0; q < 60; q += 8) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], q + 4 + k < 61 ? fmaxf(s[q + k], s[q + 4 + k]) : s[q + k]);
-          }
-          top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        }
-        top = __fmul_rn(top, fabsf(sc));
-        const bool raise = top > sub + (C::kStep + C::kPLog);
-        if (__any_sync(kFull, raise)) {  // a new reference: the maximum so far
-          const float to = raise ? fmaxf(sub, top - C::kPLog) : sub, f = ex2(sub - to);  // from kNoRef: of a sum that is 0
-          l *= f;
-          sub = to;
-          if (live) {
-            if (!w2) {
-              wait(B(pv_done), (pv + i - 1) & 1);
-              __syncwarp();
-              tc::tc_fence_after();
-            }
-#pragma unroll 1
-            for (int c = 0; c < HD; c += 16) {
-              float o[16];
-              tc::tmem_ld16(O_at(x) + lanes + c, o);
-              landed(o);
-              uint32_t y[16];
-#pragma unroll
-              for (int q = 0; q < 16; ++q) y[q] = __float_as_uint(o[q] * f);
-              tmem_st16(O_at(x) + lanes + c, y);
-            }
-          }
-        }
-        // s sc - sub, rounded once: what sub's own rounding adds is the same for all of the row's weights under it, and
-        // divides out.  Beyond 2^20 it could be large: there the product is rounded by itself.
-        const bool far = !(fabsf(sub) < 1048576.f), any_far = __any_sync(kFull, far);
-        const float2 sc2 = make_float2(sc, sc), sub2 = make_float2(-sub, -sub);
-        float buf[2][32], l4[4] = {0.f, 0.f, 0.f, 0.f};
-        tmem_ld32(sA, buf[0]);
-#pragma unroll
-        for (int part = 0; part < 4; ++part) {  // 32 positions, the next 32 on their way
-          float(&s)[32] = buf[part & 1];
-          landed(s);
-          if (part < 3) tmem_ld32(sA + 32 * (part + 1), buf[(part + 1) & 1]);
-          if (any_far) {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) s[q] = far ? __fmul_rn(s[q], sc) - sub : fmaf(s[q], sc, -sub);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 32; q += 2) {
-              const float2 y = fma2(make_float2(s[q], s[q + 1]), sc2, sub2);
-              s[q] = y.x;
-              s[q + 1] = y.y;
-            }
-          }
-          if (groups != 0xffu) {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) s[q] = groups >> (2 * part + q / 16) & 1 ? s[q] : -INFINITY;
-          }
-          uint32_t p[16];
-#pragma unroll
-          for (int q = 0; q < 32; q += 2) {
-            const float y0 = ex2(s[q]), y1 = ex2(s[q + 1]);
-            l4[q & 2] += y0;
-            l4[(q & 2) + 1] += y1;
-            p[q / 2] = pack16<FP8>(y0, y1);
-          }
-          tmem_st16(sA + 16 * part, p);  // over columns that have been read
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        tc::tmem_st_wait();
-        live |= groups != 0;
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(B(p_full[b]));
-      }
-      kc += n;
-      if (!w2) pv += n;
-
-      // The item's end: O to the joining kernel, a float4 of dims after the other with the rows side by side.
-      wait(B(o_full[x]), done++ & 1);
-      __syncwarp();
-      tc::tc_fence_after();
-      const float vs = FP8 && a.v_scale ? a.v_scale[it.gg] : 1.0f;
-      const int r = x * 128 + row, RT = a.M * G, R = it.m0 * G + it.r0 + r;
-      const bool whole = it.a == it.b, there = r < it.rows;
-      float* piece = pa.pieces + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == it.a ? it.second : 0)) * pa.piece;
-      float4* dst = whole ? pa.whole + (size_t)it.gg * (HD / 4) * RT + R : reinterpret_cast<float4*>(piece) + r;
-      const size_t step = whole ? RT : pa.rows;
-      if (live) {
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          tmem_ld32(O_at(x) + lanes + c, o);
-          landed(o);
-          if (there) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[(c / 4 + q) * step] = make_float4(o[4 * q] * vs, o[4 * q + 1] * vs, o[4 * q + 2] * vs, o[4 * q + 3] * vs);
-          }
-        }
-      }
-      if (there) {
-        float* refs = whole ? pa.whole_ref + (size_t)it.gg * RT + R : piece + (size_t)pa.rows * HD + r;
-        float* sums = whole ? pa.whole_l + (size_t)it.gg * RT + R : piece + (size_t)pa.rows * (HD + 1) + r;
-        *refs = sub;
-        *sums = l;
-      }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(B(o_empty[x]));
     }
   }
   tc::tc_fence_before();
@@ -781,62 +805,114 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
   }
 }
 
-// The parts of a row in order: the pieces of what its group shares, then its own positions.  One block per (request,
-// kv head), a float4 of a head's dims per thread.
+// The parts of a row in order: the pieces of what its group shares, then of its own positions.  One block per (request,
+// kv head), a float4 of a head's dims per thread; kBatch pieces are read at once.
 template <int HD, bool FP8>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixArgs pa) {
   using C = XCfg<HD, FP8>;
+  constexpr int SP = C::OWN, kBatch = 4;
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const PagedAttnArgs& a = pa.a;
+  const GroupedAttnArgs& a = pa.a;
   const int m = blockIdx.x / a.n_kv, gg = blockIdx.x % a.n_kv, G = a.n_q / a.n_kv, RT = a.M * G;
-  const long long U = pa.plan[0];
-  const int nct = (int)pa.plan[1];
-  const int n = a.lens[m];
-  int g = -1, m0 = 0;
+  const long long U = pa.plan[0], V = a.own_plan[0], own0 = a.own_plan[2 + m];
+  const int nct = (int)pa.plan[1], own_nct = (int)a.own_plan[1];
+  const Span s = own_span<SP>(a, m, U > 0);
+  int g = U > 0 ? group_of(a, m) : -1, m0 = 0;
+  if (g >= 0 && (s.n < 1 || (long long)s.n > ((long long)a.max_pages << a.page_shift) || left_to_group(a, g, s.n) == 0)) g = -1;
   Tiles ts{};
-  if (U > 0 && n > 0 && (long long)n <= ((long long)a.max_pages << a.page_shift)) {
-    g = group_of(a, m);
-    if (left_to_group(a, g, n) == 0) g = -1;
-    if (g >= 0) {
-      ts = tiles_of<C>(a, g);
-      m0 = a.cu_groups[g];
-    }
+  long long base = 0;
+  if (g >= 0) {
+    ts = tiles_of<C>(a, g);
+    m0 = a.cu_groups[g];
+    base = pa.plan[2 + g];
   }
-  for (int e = threadIdx.x; e < G * (HD / 4); e += 256) {
+  // its own run: CTAs oa .. ob
+  const int ch = s.c1 - s.c0;
+  int oa = 0, ob = -1, own_second = 0;
+  if (ch > 0) {
+    const long long at = own0 + (long long)gg * (kTailEnds + ch);
+    oa = owner(V, own_nct, at + kTailEnds);
+    ob = owner(V, own_nct, at + kTailEnds + ch - 1);
+    own_second = split_at(V, own_nct, oa) < at;
+  }
+  for (int e = threadIdx.x; e < G * (HD / 4); e += blockDim.x) {
     const int h = e % G, c4 = e / G;
     const size_t row = (size_t)m * a.n_q + (size_t)gg * G + h;
     float ref = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float pref, float psum, const float4* at) {
-      if (psum == 0.f) return;  // nothing attended to: the rest may hold anything
-      const float4 v = __ldcg(at);
-      const float mx = fmaxf(ref, pref), f0 = weight(ref, mx), f1 = weight(pref, mx);
-      sum = sum * f0 + psum * f1;
-      o.x = o.x * f0 + v.x * f1;
-      o.y = o.y * f0 + v.y * f1;
-      o.z = o.z * f0 + v.z * f1;
-      o.w = o.w * f0 + v.w * f1;
-      ref = mx;
+    // n parts: at(i, ref, sum, v) says where the i-th is
+    auto add = [&](int n, auto at) {
+      for (int b = 0; b < n; b += kBatch) {
+        float r[kBatch], l[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const float *pr, *pl;
+          const float4* pv;
+          at(min(b + q, n - 1), pr, pl, pv);
+          r[q] = __ldcg(pr);
+          l[q] = __ldcg(pl);
+          v[q] = __ldcg(pv);
+        }
+        float mx = ref;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          if (b + q >= n || l[q] == 0.f) r[q] = -INFINITY;  // nothing attended to: the rest may hold anything
+          mx = fmaxf(mx, r[q]);
+        }
+        const float f = weight(ref, mx);
+        sum *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          if (r[q] == -INFINITY) continue;
+          const float w = ex2(r[q] - mx);
+          sum += l[q] * w;
+          o.x += v[q].x * w;
+          o.y += v[q].y * w;
+          o.z += v[q].z * w;
+          o.w += v[q].w * w;
+        }
+        ref = mx;
+      }
     };
     if (g >= 0) {
       const int R = (m - m0) * G + h, tile = R / C::ROWS, r = R % C::ROWS;
       const int cost_full = C::T == 2 ? C::kWide : C::kNarrow, cost = tile < ts.full ? cost_full : ts.cost_rest;
-      const long long at = pa.plan[2 + g] + gg * ts.per_head + tile * (C::kEnds + cost_full * (long long)ts.chunks);
+      const long long at = base + gg * ts.per_head + tile * (C::kEnds + cost_full * (long long)ts.chunks);
       const int ca = owner(U, nct, at + C::kEnds), cb = owner(U, nct, at + C::kEnds + cost * (long long)(ts.chunks - 1));
       if (ca == cb) {
-        const size_t w = (size_t)gg * RT + (size_t)m * G + h;
-        add(__ldcg(pa.whole_ref + w), __ldcg(pa.whole_l + w), pa.whole + ((size_t)gg * (HD / 4) + c4) * RT + (size_t)m * G + h);
+        const size_t w = (size_t)m * G + h;
+        add(1, [&](int, const float*& pr, const float*& pl, const float4*& pv) {
+          pr = pa.whole_ref + (size_t)gg * RT + w;
+          pl = pa.whole_l + (size_t)gg * RT + w;
+          pv = pa.whole + ((size_t)gg * (HD / 4) + c4) * RT + w;
+        });
       } else {
         const int second = split_at(U, nct, ca) < at;
-        for (int c = ca; c <= cb; ++c) {
-          const float* p = pa.pieces + (size_t)(2 * c + (c == ca ? second : 0)) * pa.piece;
-          add(__ldcg(p + (size_t)pa.rows * HD + r), __ldcg(p + (size_t)pa.rows * (HD + 1) + r),
-              reinterpret_cast<const float4*>(p) + (size_t)c4 * pa.rows + r);
-        }
+        add(cb - ca + 1, [&](int i, const float*& pr, const float*& pl, const float4*& pv) {
+          const float* p = pa.pieces + (size_t)(2 * (ca + i) + (i == 0 ? second : 0)) * pa.piece;
+          pr = p + (size_t)pa.rows * HD + r;
+          pl = p + (size_t)pa.rows * (HD + 1) + r;
+          pv = reinterpret_cast<const float4*>(p) + (size_t)c4 * pa.rows + r;
+        });
       }
     }
-    add(__ldcg(a.part_ref + row), __ldcg(a.part_l + row), reinterpret_cast<const float4*>(a.part_o + row * HD) + c4);
+    if (oa == ob) {
+      add(1, [&](int, const float*& pr, const float*& pl, const float4*& pv) {
+        pr = a.part_ref + row;
+        pl = a.part_l + row;
+        pv = reinterpret_cast<const float4*>(a.part_o + row * HD) + c4;
+      });
+    } else {
+      add(ob - oa + 1, [&](int i, const float*& pr, const float*& pl, const float4*& pv) {
+        const float* p = a.own_pieces + (size_t)(2 * (oa + i) + (i == 0 ? own_second : 0)) * a.own_piece;
+        pr = p + G * HD + h;
+        pl = p + G * HD + G + h;
+        pv = reinterpret_cast<const float4*>(p + h * HD) + c4;
+      });
+    }
     const float f = sum == 0.f ? 0.f : 1.0f / sum;
     *reinterpret_cast<uint2*>(a.o + row * HD + 4 * c4) = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
     if (a.lse && c4 == 0) a.lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
@@ -845,8 +921,8 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
 
 // The workspace behind paged attention's: the plan, the requests' own parts, the tiles that are not split, the pieces.
 struct Layout {
-  size_t plan, own_o, own_ref, own_l, whole, whole_ref, whole_l, pieces, total;
-  int piece, rows;
+  size_t plan, own_plan, own_o, own_ref, own_l, own_pieces, whole, whole_ref, whole_l, pieces, total;
+  int piece, rows, own_piece;
 };
 Layout layout_of(int n_q, int n_kv, int hd, int M) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -862,6 +938,9 @@ Layout layout_of(int n_q, int n_kv, int hd, int M) {
   w.rows = (int)std::min<size_t>(hd == 256 ? 128 : 256, ((size_t)M * G + 31) / 32 * 32);
   w.piece = w.rows * (hd + 2);
   w.plan = take(8 * ((size_t)M + 2));
+  w.own_piece = (G * (hd + 2) + 3) / 4 * 4;
+  w.own_plan = take(8 * ((size_t)M + 2));
+  w.own_pieces = take((size_t)2 * kTailMaxCtas * w.own_piece * 4);
   w.own_o = take(heads * hd * 4);
   w.own_ref = take(heads * 4);
   w.own_l = take(heads * 4);
@@ -874,7 +953,7 @@ Layout layout_of(int n_q, int n_kv, int hd, int M) {
 }
 
 template <int HD, bool FP8>
-cudaError_t launch(const PagedAttnArgs& args, const void* k_pages, const void* v_pages, cudaStream_t st) {
+cudaError_t launch(const GroupedAttnArgs& args, cudaStream_t st) {
   using C = XCfg<HD, FP8>;
   EncodeTiled enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
@@ -885,7 +964,7 @@ cudaError_t launch(const PagedAttnArgs& args, const void* k_pages, const void* v
     const cuuint64_t strides[1] = {(cuuint64_t)C::ROWB};
     const cuuint32_t box[2] = {(cuuint32_t)(C::INB / (FP8 ? 1 : 2)), (cuuint32_t)std::min(page, C::KS)}, es[2] = {1, 1};
     if (enc(&tm[i], FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(i ? v_pages : k_pages), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            const_cast<uint8_t*>(i ? args.v_pages : args.k_pages), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             C::INB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
@@ -899,6 +978,9 @@ cudaError_t launch(const PagedAttnArgs& args, const void* k_pages, const void* v
   p.a.part_o = f(w.own_o);
   p.a.part_ref = f(w.own_ref);
   p.a.part_l = f(w.own_l);
+  p.a.own_plan = reinterpret_cast<long long*>(ws + w.own_plan);
+  p.a.own_pieces = f(w.own_pieces);
+  p.a.own_piece = w.own_piece;
   p.whole = reinterpret_cast<float4*>(ws + w.whole);
   p.whole_ref = f(w.whole_ref);
   p.whole_l = f(w.whole_l);
@@ -911,9 +993,10 @@ cudaError_t launch(const PagedAttnArgs& args, const void* k_pages, const void* v
   e = launch_dependent(kernel, dim3(std::min(sm_count(), kPrefixMaxCtas)), dim3(C::kThreads), C::SMEM, st, tm[0], tm[1], p);
   note_launch();
   if (e != cudaSuccess) return e;
-  e = launch_paged_attn(p.a, FP8 ? TP_FP8_E4M3 : TP_BF16, HD, k_pages, v_pages, st);
+  e = launch_tail_attn(p.a, FP8 ? TP_FP8_E4M3 : TP_BF16, HD, st);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(prefix_join_kernel<HD, FP8>, dim3((unsigned)args.M * args.n_kv), dim3(256), 0, st, p);
+  const int threads = std::min(256, (args.n_q / args.n_kv * HD / 4 + 31) / 32 * 32);
+  e = launch_dependent(prefix_join_kernel<HD, FP8>, dim3((unsigned)args.M * args.n_kv), dim3(threads), 0, st, p);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -922,13 +1005,10 @@ cudaError_t launch(const PagedAttnArgs& args, const void* k_pages, const void* v
 
 size_t prefix_attn_workspace_bytes(int n_q, int n_kv, int hd, int M) { return layout_of(n_q, n_kv, hd, M).total; }
 
-cudaError_t launch_prefix_attn(const PagedAttnArgs& a, int kv_dtype, int hd, const void* k_pages, const void* v_pages,
-                               cudaStream_t st) {
+cudaError_t launch_prefix_attn(const GroupedAttnArgs& a, int kv_dtype, int hd, cudaStream_t st) {
   auto go = [&](auto fp8) {
     constexpr bool F = decltype(fp8)::value;
-    return hd == 64    ? launch<64, F>(a, k_pages, v_pages, st)
-           : hd == 128 ? launch<128, F>(a, k_pages, v_pages, st)
-                       : launch<256, F>(a, k_pages, v_pages, st);
+    return hd == 64 ? launch<64, F>(a, st) : hd == 128 ? launch<128, F>(a, st) : launch<256, F>(a, st);
   };
   return kv_dtype == TP_BF16 ? go(std::false_type{}) : go(std::true_type{});
 }
