@@ -591,14 +591,15 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
           ++cnt;
           return there;
         };
+        // The thread has 64 cycles for an MMA: descriptors are a base and constants (addresses do not carry out of
+        // their field).  Loops that computed them took 140.
         auto scores = [&](int x, int region, int st, int sub) {
-          const uint32_t q0 = qA + x * C::QBLOCK, k0 = rA + st * C::STAGE;
-#pragma unroll 1
-          for (int b = 0; b < HD / 64; ++b)  // 64 dims: a row of 128 bytes
+          const uint64_t q0 = smem_desc(qA + x * C::QBLOCK, 16, 1024, 2), k0 = smem_desc(rA + st * C::STAGE, 16, 1024, 2);
+          const uint32_t d = S_at(region) + sub * C::KS;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              tc::mma_bf16(S_at(region) + sub * C::KS, smem_desc(q0 + b * 16384 + i * 32, 16, 1024, 2),
-                           smem_desc(k0 + b * (C::KS * 128) + i * 32, 16, 1024, 2), idS, b + i > 0);
+          for (int i = 0; i < HD / 16; ++i)  // 64 dims: rows of 128 bytes
+            tc::mma_bf16(d, q0 + tc::desc_off(i / 4 * 16384 + i % 4 * 32), k0 + tc::desc_off(i / 4 * (C::KS * 128) + i % 4 * 32),
+                         idS, i > 0);
         };
         auto scores_end = [&](int b) {
           tc::mma_commit(B(s_full[b]));
@@ -606,12 +607,19 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
           b == 0 ? ++uses[0] : b == 1 ? ++uses[1] : ++uses[2];
         };
         auto values = [&](int x, int region, int st, int sub, uint32_t groups, bool& live) {
-          const uint32_t v0 = rA + st * C::STAGE;
+          const uint64_t v0 = smem_desc(rA + st * C::STAGE, C::KS * 128, 1024, 2);
+          const uint32_t p = S_at(region) + 8 * sub * (C::KS / 16), d = O_at(x);
+          if (groups == 0xffu) {
+#pragma unroll
+            for (int i = 0; i < C::KS / 16; ++i)
+              tc::mma_bf16_tmem_a(d, p + 8 * i, v0 + tc::desc_off(i * 2048), idO, i > 0 || live);
+            live = true;
+            return;
+          }
 #pragma unroll 1
           for (int i = 0; i < C::KS / 16; ++i) {
-            const int step = sub * (C::KS / 16) + i;
-            if (!(groups >> step & 1)) continue;  // what was not loaded may hold anything
-            tc::mma_bf16_tmem_a(O_at(x), S_at(region) + 8 * step, smem_desc(v0 + i * 2048, C::KS * 128, 1024, 2), idO, live);
+            if (!(groups >> (sub * (C::KS / 16) + i) & 1)) continue;  // what was not loaded may hold anything
+            tc::mma_bf16_tmem_a(d, p + 8 * i, v0 + tc::desc_off(i * 2048), idO, live);
             live = true;
           }
         };
