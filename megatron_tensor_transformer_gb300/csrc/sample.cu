@@ -11,6 +11,17 @@
 // A weight is 2^-E, E = (max - x) log2(e) / T held with 32 bits behind the point: the difference to the maximum and
 // its product with log2(e) / T are each two fp32 (the rounded value and the rounding's rest), 2^-F of the fraction F
 // a table of 64 and a cubic in what is left (|r| <= 2^-7): good to 2^-29 of the weight, 2^-31 on average.
+//
+// A row is shared by the CTAs of a cluster, which keep it in shared memory (from global again where it is too long) and join
+// through distributed shared memory.  With a temperature or min-p alone one pass sums the weights.  Top-k and top-p look
+// for the key (logit, then the lower id) of the last kept token by bins: a histogram of approximate weights (or of
+// counts) says in which bin the border lies, a second pass sums the exact weights above it, checks that it does, and lists
+// that bin's tokens, among which the first CTA finds the border.  Where they are too many to list (flat rows, ties) the
+// bin is divided again by key.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
 #include "common.cuh"
 #include "paged.h"
 #include "tc_ptx.cuh"
@@ -19,8 +30,17 @@ namespace tpx {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kNT = 1024, kNW = kNT / 32;
+constexpr int kNT = 512, kNW = kNT / 32, kMaxC = 8;
+constexpr int kPerOctave = 64, kOctaves = 24;            // bins of the first division, by the weight
+constexpr int kBins = kPerOctave * kOctaves;             // the last one holds all that is lighter
+static_assert(kBins % kNT == 0, "bins per thread");
+constexpr float kUnit = 4096.f;                          // of the approximate weights
+constexpr int kList = 512;                               // tokens that are listed
+constexpr int kMostShared = 40 * 1024;                   // logits of a CTA that are kept in shared memory
+constexpr float kLightest = 46.f;                        // exponent from which a weight is 0
 
 // Orders as the logit does, -0 as +0.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -30,6 +50,18 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 // (logit, then the lower id): the greater the further ahead
 __device__ __forceinline__ uint64_t key_of(float x, int id) { return (uint64_t)order_of(x) << 32 | (uint32_t)~id; }
+
+// 2^(31 - (j + 1/2) / 64)
+__device__ const uint32_t kPowers[64] = {
+    2135885998u, 2112878262u, 2090118366u, 2067603638u, 2045331439u, 2023299156u, 2001504204u, 1979944027u,
+    1958616096u, 1937517909u, 1916646992u, 1896000896u, 1875577199u, 1855373507u, 1835387448u, 1815616678u,
+    1796058879u, 1776711757u, 1757573041u, 1738640488u, 1719911875u, 1701385007u, 1683057710u, 1664927835u,
+    1646993254u, 1629251865u, 1611701585u, 1594340357u, 1577166143u, 1560176931u, 1543370725u, 1526745556u,
+    1510299473u, 1494030547u, 1477936870u, 1462016553u, 1446267730u, 1430688553u, 1415277195u, 1400031848u,
+    1384950723u, 1370032052u, 1355274085u, 1340675091u, 1326233356u, 1311947188u, 1297814910u, 1283834865u,
+    1270005413u, 1256324931u, 1242791816u, 1229404479u, 1216161350u, 1203060876u, 1190101520u, 1177281762u,
+    1164600099u, 1152055042u, 1139645120u, 1127368878u, 1115224875u, 1103211687u, 1091327906u, 1079572136u,
+};
 
 struct Scale {  // of a row's exponents
   float top, hi, lo;
@@ -51,108 +83,451 @@ __device__ __forceinline__ uint64_t weight_of(float x, const Scale& s, const uin
   return ((uint64_t)v << 13) >> (int)(e >> 32);
 }
 
-// One CTA per row, the row read again for each step of the searches: exact and slow.
-__global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
-  __shared__ uint32_t table[64];
-  __shared__ uint64_t s_sum[kNW];
-  __shared__ float s_top[kNW];
-  const int tid = threadIdx.x, m = blockIdx.x, V = a.vocab;
-  const float* x = a.logits + (int64_t)m * a.ldl;
-  tc::griddep_wait();
-  tc::griddep_launch_dependents();
-  if (tid < 64) table[tid] = (uint32_t)__double2ll_rn(exp2(31.0 - (tid + 0.5) / 64));
-  auto block_sum = [&](uint64_t v) {  // to all threads
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    __syncthreads();
-    if ((tid & 31) == 0) s_sum[tid >> 5] = v;
-    __syncthreads();
-    v = 0;
-    for (int w = 0; w < kNW; ++w) v += s_sum[w];
-    return v;
-  };
-  float top = -INFINITY;
-  int bad = 0;
-  for (int i = tid; i < V; i += kNT) {
-    top = fmaxf(top, x[i]);
-    bad |= !(x[i] < INFINITY);
-  }
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  if ((tid & 31) == 0) s_top[tid >> 5] = top;
-  bad = __syncthreads_or(bad);
-  for (int w = 0; w < kNW; ++w) top = fmaxf(top, s_top[w]);
+// the larger of the two, NaN if x is one (fmaxf drops it)
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float logit_of(uint32_t order) {  // of order_of
+  return __uint_as_float(order >> 31 ? order & 0x7fffffffu : ~order);
+}
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+// 2^64 p for p in [0, 1), rounded down (exact from 2^-40 on)
+__device__ __forceinline__ uint64_t frac64(float p) {
+  const uint32_t b = __float_as_uint(p);
+  const int e = (int)(b >> 23) - 86;  // p = mantissa 2^(e - 64)
+  const uint64_t mant = (b & 0x7fffffu) | 0x800000u;
+  return !(p > 0.f) || b < 0x800000u || e <= -24 ? 0 : e >= 0 ? mant << e : mant >> -e;
+}
+// p of all: rounded down and up
+__device__ __forceinline__ uint64_t share_down(float p, uint64_t all) { return __umul64hi(frac64(p), all); }
+__device__ __forceinline__ uint64_t share_up(float p, uint64_t all) {
+  const uint64_t q = frac64(p);
+  return __umul64hi(q, all) + (q * all != 0);
+}
 
+// A division of the keys into bins, the highest keys first: by the weight, or evenly by key from `high` down.
+struct Bins {
+  uint64_t low, high;  // keys [low, high] are divided, the others have no bin
+  int shift;           // < 0: by the weight
+};
+// What the first CTA tells the others, and what it is told.
+struct Shared {
+  float top[kMaxC];
+  uint32_t hist[kBins];
+  uint64_t key[kList], weight[kList];
+  int listed;                    // tokens of the bin, of which the first kList are listed
+  uint64_t above[kMaxC], in[kMaxC], all[kMaxC], least[kMaxC], most[kMaxC];  // of each CTA
+  int bin, state;                // the border's bin; what to do next
+  uint64_t border;               // the lowest key that is kept
+  Bins bins;
+};
+enum { kFound, kAgain, kDivide };  // the border is known; it lies in another bin; divide the bin
+
+// Grid: M clusters of C CTAs.
+__global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int per_cta, int in_shared) {
+  extern __shared__ __align__(16) float s_row[];
+  __shared__ Shared sh;
+  __shared__ uint32_t table[64];
+  __shared__ uint64_t s_sum[kNW], s_sum2[kNW], s_sum3[kNW], s_least[kNW], s_most[kNW];
+  __shared__ float s_top[kNW], s_scale[2], s_floor;
+  __shared__ double s_t, s_min;
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), c = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, m = blockIdx.x / C, V = a.vocab;
+  cl.barrier_arrive();  // all have begun where it is waited for: then their memory may be written
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
+  if (tid < 64) table[tid] = kPowers[tid];
+
+  // The row from the 16-byte boundary at or before it on: place i holds id i - lead.  This CTA's places are
+  // [i0, i1), in vectors of four; a place outside the row holds -inf.
+  const float* row = a.logits + (int64_t)m * a.ldl;
+  const int lead = (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
+  row -= lead;
+  const int places = (lead + V + 3) / 4 * 4, i0 = min(places, c * per_cta), i1 = min(places, i0 + per_cta);
+  auto vector_at = [&](int i) {  // global memory
+    if (i >= lead && i + 4 <= lead + V) return __ldcs(reinterpret_cast<const float4*>(row + i));
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = i + k >= lead && i + k < lead + V ? row[i + k] : -INFINITY;
+    return make_float4(v[0], v[1], v[2], v[3]);
+  };
   const float T = a.temperature ? a.temperature[m] : 1.f, tp = a.top_p ? a.top_p[m] : 1.f,
               mp = a.min_p ? a.min_p[m] : 0.f, u = a.u[m];
   const int tk = T <= 0.f ? 1 : a.top_k ? a.top_k[m] : 0;
-  if (bad || top == -INFINITY || T != T || tp != tp || mp != mp || u != u) {
-    if (tid == 0) {
+  if (tid == kNT - 1) {  // 64-bit arithmetic is slow here: one thread's, beside the loads
+    const double t64 = T <= 0.f ? 1.0 : fmax((double)T, 0x1p-100), scale = 1.4426950408889634 / t64;
+    s_scale[0] = (float)scale;
+    s_scale[1] = (float)(scale - (double)s_scale[0]);
+    s_t = t64;
+    s_min = mp > 0.f ? t64 * log((double)fminf(mp, 1.f)) : 0.0;
+  }
+  float top = -INFINITY;
+  {
+    constexpr int kAhead = 4;
+    for (int i = i0 + 4 * tid; i < i1; i += 4 * kNT * kAhead) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        v[k] = i + 4 * kNT * k < i1 ? vector_at(i + 4 * kNT * k) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        top = max_nan(max_nan(top, max_nan(v[k].x, v[k].y)), max_nan(v[k].z, v[k].w));
+        if (in_shared && i + 4 * kNT * k < i1) *reinterpret_cast<float4*>(s_row + (i + 4 * kNT * k - i0)) = v[k];
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, o));
+  if (lane == 0) s_top[warp] = top;
+  if (tid == 0) sh.listed = 0;
+  for (int b = tid; b < kBins; b += kNT) sh.hist[b] = 0;
+  cl.barrier_wait();
+  __syncthreads();
+  if (warp == 0) {
+    top = s_top[lane % kNW];
+#pragma unroll
+    for (int o = kNW / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, o));
+    if (lane < C) cl.map_shared_rank(&sh, lane)->top[c] = top;
+  }
+  cl.sync();
+  top = sh.top[0];
+  for (int r = 1; r < C; ++r) top = max_nan(top, sh.top[r]);
+
+  if (!(top > -INFINITY && top < INFINITY) || T != T || tp != tp || mp != mp || u != u) {  // no distribution
+    if (c == 0 && tid == 0) {
       a.ids[m] = -1;
       if (a.logprob) a.logprob[m] = NAN;
     }
     return;
   }
-  const double t64 = T <= 0.f ? 1.0 : fmax((double)T, 0x1p-100), c = 1.4426950408889634 / t64;
-  Scale s{top, (float)c, 0.f};
-  s.lo = (float)(c - (double)s.hi);
+  const Scale s{top, s_scale[0], s_scale[1]};
 
-  // The lowest key that is kept: the least t for which what lies above it (all of `from` and over) is less than lim.
-  auto lowest = [&](uint64_t from, uint64_t lim, bool weights) {
-    uint64_t lo = 0, hi = key_of(top, 0);  // above hi there is nothing
-    while (lo < hi) {
-      const uint64_t t = lo + (hi - lo) / 2;
-      uint64_t v = 0;
-      for (int i = tid; i < V; i += kNT) {
-        const uint64_t k = key_of(x[i], i);
-        if (k > t && k >= from) v += weights ? weight_of(x[i], s, table) : 1;
+  // f(place, four logits) over the CTA's vectors
+  auto each = [&](int from, int to, int step, auto f) {
+    for (int i = from; i < to; i += step) f(i, in_shared ? *reinterpret_cast<const float4*>(s_row + (i - i0)) : vector_at(i));
+  };
+  auto key_at = [&](float x, int place) { return key_of(x, place - lead); };
+  Shared* first = cl.map_shared_rank(&sh, 0);
+
+  // Of the keys from `from` on: the lowest before which fewer than k of them lie (share < 0), or before which less than
+  // `share` of their sum does.
+  auto lowest = [&](uint64_t from, int k, float share) {
+    const bool by_weight = share >= 0.f;
+    Bins bins{from, ~0ull, -1};
+    uint64_t base = 0, limit = k;  // what lies above the bins; by_weight: limit is known after the first sums
+    auto exponent = [&](float x) { return __fmul_rn(s.top - x, s.hi); };  // monotone in x, as the keys are
+    auto bin_of = [&](float x, uint64_t key) {
+      if (bins.shift >= 0) return key >= bins.low && key <= bins.high ? (int)((bins.high - key) >> bins.shift) : -1;
+      const float p = exponent(x);
+      return key >= bins.low && p < kLightest ? min((int)(p * kPerOctave), kBins - 1) : -1;
+    };
+    auto bin_exponent = [&](int b) {  // of a bin's highest key
+      if (bins.shift < 0) return (float)b * (1.f / kPerOctave);
+      return exponent(logit_of((uint32_t)((bins.high - ((uint64_t)b << bins.shift)) >> 32)));
+    };
+    for (bool first_sums = true;;) {
+      // What the bins hold: tokens, or roughly their weights in terms of the bin's heaviest (whole numbers, in any order).
+      each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int b = bin_of(v[q], key_at(v[q], i + q));
+          if (b < 0) continue;
+          const uint32_t n = by_weight ? __float2uint_rn(ex2(bin_exponent(b) - exponent(v[q])) * kUnit) : 1u;
+          if (n) atomicAdd(&sh.hist[b], n);
+        }
+      });
+      __syncthreads();
+      if (c != 0) {
+        for (int b = tid; b < kBins; b += kNT) {
+          const uint32_t n = sh.hist[b];
+          if (n) {
+            atomicAdd(&first->hist[b], n);
+            sh.hist[b] = 0;
+          }
+        }
       }
-      if (block_sum(v) < lim) hi = t;
-      else lo = t + 1;
+      cl.sync();
+      if (c == 0) {  // the bin with the border, as far as these tell
+        constexpr int kEach = kBins / kNT;
+        uint64_t n[kEach], sum = 0;  // in units of 2^-24 of the bins' first weight
+        const float p0 = bin_exponent(0);
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+          const int b = tid * kEach + q;
+          const uint32_t h = sh.hist[b];
+          sh.hist[b] = 0;
+          n[q] = !by_weight || h == 0 ? h : (uint64_t)((float)h * ex2(p0 - bin_exponent(b)) * (0x1p24f / kUnit));
+          sum += n[q];
+        }
+        uint64_t before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t x = __shfl_up_sync(kFull, before, o);
+          if (lane >= o) before += x;
+        }
+        if (lane == 31) s_sum[warp] = before;
+        before -= sum;
+        if (tid == 0) sh.bin = kBins - 1;  // where none is found below: too few tokens, or rounding
+        __syncthreads();
+        uint64_t all = 0;
+        for (int w = 0; w < kNW; ++w) {
+          if (w < warp) before += s_sum[w];
+          all += s_sum[w];
+        }
+        uint64_t goal = limit - base;
+        if (by_weight) goal = first_sums ? share_down(share, all) : (uint64_t)((float)goal * (0x1p-20f * ex2(p0)));
+        if (goal == 0) goal = 1;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+          if (before < goal && before + n[q] >= goal) atomicMin(&sh.bin, tid * kEach + q);
+          before += n[q];
+        }
+        __syncthreads();
+        if (tid < C) {
+          Shared* to = cl.map_shared_rank(&sh, tid);
+          const int bin = sh.bin;
+          to->bin = bin;
+          to->state = !by_weight && all < goal ? kFound : kAgain;  // fewer than k tokens have a weight: all are kept
+        }
+      }
+      cl.sync();
+      if (sh.state == kFound) return from;
+      for (;;) {
+        // The exact sums above the bin and in it, its keys' ends, and its tokens, listed as far as they fit.
+        const int bin = sh.bin;
+        uint64_t above = 0, in = 0, all = 0, least = ~0ull, most = 0;
+        each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint64_t key = key_at(v[q], i + q);
+            const int b = bin_of(v[q], key);
+            if (b < 0 || (b > bin && !(by_weight && first_sums))) continue;
+            const uint64_t w = by_weight ? weight_of(v[q], s, table) : 1;
+            all += w;
+            if (b < bin) above += w;
+            if (b != bin) continue;
+            in += w;
+            least = min(least, key);
+            most = max(most, key);
+            const int at = first->listed < kList ? atomicAdd(&first->listed, 1) : kList;
+            if (at < kList) {
+              first->key[at] = key;
+              first->weight[at] = w;
+            }
+          }
+        });
+        above = warp_sum(above);
+        in = warp_sum(in);
+        all = warp_sum(all);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          least = min(least, __shfl_xor_sync(kFull, least, o));
+          most = max(most, __shfl_xor_sync(kFull, most, o));
+        }
+        if (lane == 0) {
+          s_sum[warp] = above;
+          s_sum2[warp] = in;
+          s_sum3[warp] = all;
+          s_least[warp] = least;
+          s_most[warp] = most;
+        }
+        __syncthreads();
+        if (tid == 0) {
+          for (int w = 1; w < kNW; ++w) {
+            above += s_sum[w];
+            in += s_sum2[w];
+            all += s_sum3[w];
+            least = min(least, s_least[w]);
+            most = max(most, s_most[w]);
+          }
+          first->above[c] = above;
+          first->in[c] = in;
+          first->all[c] = all;
+          first->least[c] = least;
+          first->most[c] = most;
+        }
+        cl.sync();
+        if (c == 0) {
+          above = base;
+          in = all = most = 0;
+          least = ~0ull;
+          for (int r = 0; r < C; ++r) {
+            above += sh.above[r];
+            in += sh.in[r];
+            all += sh.all[r];
+            least = min(least, sh.least[r]);
+            most = max(most, sh.most[r]);
+          }
+          if (by_weight && first_sums) limit = max(uint64_t(1), share_up(share, all));
+          const int listed = sh.listed;
+          int state = kFound, to = bin;
+          if (above >= limit) {
+            state = kAgain;
+            to = bin - 1;
+          } else if (above + in < limit) {
+            state = kAgain;
+            to = bin + 1;
+          } else if (listed >= kList) {  // some may not be there
+            state = kDivide;
+          }
+          uint64_t lowest_kept = ~0ull;
+          if (state == kFound) {  // a token is kept if what is ahead of it is below the limit
+            for (int i = tid; i < listed; i += kNT) {
+              const uint64_t key = sh.key[i];
+              uint64_t ahead = above;
+              for (int j = 0; j < listed; ++j) ahead += sh.key[j] > key ? sh.weight[j] : 0;
+              if (ahead < limit) lowest_kept = min(lowest_kept, key);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) lowest_kept = min(lowest_kept, __shfl_xor_sync(kFull, lowest_kept, o));
+          }
+          __syncthreads();
+          if (lane == 0) s_least[warp] = lowest_kept;
+          __syncthreads();
+          if (tid < C) {
+            for (int w = 0; w < kNW; ++w) lowest_kept = min(lowest_kept, s_least[w]);
+            Shared* to_sh = cl.map_shared_rank(&sh, tid);
+            to_sh->state = state;
+            to_sh->bin = to;
+            to_sh->border = lowest_kept;
+            const int bits = 64 - __clzll((long long)(most - least));
+            to_sh->bins = Bins{least, most, max(0, bits - 10)};
+            to_sh->above[0] = above;
+            to_sh->all[0] = limit;
+          }
+          if (tid == 0) sh.listed = 0;
+        }
+        cl.sync();
+        limit = sh.all[0];
+        first_sums = false;
+        if (sh.state == kFound) return sh.border;
+        if (sh.state == kDivide) {
+          bins = sh.bins;
+          base = sh.above[0];
+          break;
+        }
+      }
     }
-    return lo;
   };
-  auto sum_from = [&](uint64_t from) {
-    uint64_t v = 0;
-    for (int i = tid; i < V; i += kNT)
-      if (key_of(x[i], i) >= from) v += weight_of(x[i], s, table);
-    return block_sum(v);
-  };
-  // the lowest key of the first rank
+
   uint64_t from = 0;
-  if (tk > 0 && tk < V) from = lowest(0, tk, false);
-  if (tp < 1.f) {
-    const uint64_t all = sum_from(from);
-    const uint64_t p = tp <= 0.f ? 0 : (uint64_t)((double)tp * 0x1p64);  // exact from 2^-40 on
-    const uint64_t lim = __umul64hi(p, all) + (p * all != 0);
-    from = lowest(from, lim == 0 ? 1 : lim, true);
-  }
+  if (tk > 0 && tk < V) from = lowest(from, tk, -1.f);
+  if (tp < 1.f) from = lowest(from, 0, fmaxf(tp, 0.f));
   if (mp > 0.f) {
-    // w >= mp is x >= top + T ln mp: the lowest fp32 that is not less
-    const double lowest_x = (double)top + t64 * log((double)fminf(mp, 1.f));
-    float b = __double2float_ru(lowest_x);
-    from = max(from, (uint64_t)order_of(b) << 32);
+    // w >= mp is x >= top + T ln mp: from the lowest fp32 that is not less
+    if (tid == 0) s_floor = __double2float_ru((double)top + s_min);
+    __syncthreads();
+    from = max(from, uint64_t(order_of(s_floor)) << 32);
   }
-  const uint64_t all = sum_from(from);
-  const uint64_t target = u < 0.f ? 0 : u >= 1.f ? all - 1 : __umul64hi((uint64_t)((double)u * 0x1p64), all);
-  // the lowest id up to which the weights pass the target
-  int lo = 0, hi = V - 1;
-  while (lo < hi) {
-    const int id = (lo + hi) / 2;
-    uint64_t v = 0;
-    for (int i = tid; i <= id; i += kNT)
-      if (key_of(x[i], i) >= from) v += weight_of(x[i], s, table);
-    if (block_sum(v) > target) hi = id;
-    else lo = id + 1;
+
+  // The sums of the kept weights: each warp those of a run of vectors, so that they add up in the order of ids.
+  const int vectors = (i1 - i0) / 4, per_warp = (vectors + kNW - 1) / kNW;
+  const int v0 = min(vectors, warp * per_warp), v1 = min(vectors, v0 + per_warp);
+  auto kept_sum = [&](int i, float4 v4) {
+    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+    uint64_t w = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (key_at(v[q], i + q) >= from) w += weight_of(v[q], s, table);
+    return w;
+  };
+  uint64_t mine = 0;
+  each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v) { mine += kept_sum(i, v); });
+  mine = warp_sum(mine);
+  __syncthreads();  // (s_sum may still be read)
+  if (lane == 0) s_sum[warp] = mine;
+  __syncthreads();
+  if (warp == 0 && lane < C) {
+    uint64_t sum = 0;
+    for (int w = 0; w < kNW; ++w) sum += s_sum[w];
+    cl.map_shared_rank(&sh, lane)->in[c] = sum;
   }
-  if (tid == 0) {
-    a.ids[m] = lo;
-    if (a.logprob) a.logprob[m] = (float)(((double)x[lo] - (double)top) / t64 - log((double)all * 0x1p-44));
+  cl.sync();  // the last use of another CTA's memory
+  uint64_t all = 0, before = 0;
+  for (int r = 0; r < C; ++r) {
+    if (r < c) before += sh.in[r];
+    all += sh.in[r];
+  }
+  // the lowest id up to which the sum passes this
+  const uint64_t target = u >= 1.f ? all - 1 : share_down(u, all);
+  for (int w = 0; w < warp; ++w) before += s_sum[w];
+  if (target < before || target >= before + s_sum[warp]) return;
+  // this warp's run holds it: 32 vectors at a time
+  for (int i = i0 + 4 * v0; i < i0 + 4 * v1; i += 128) {
+    const int at = i + 4 * lane;
+    float4 v4 = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (at < i0 + 4 * v1) v4 = in_shared ? *reinterpret_cast<const float4*>(s_row + (at - i0)) : vector_at(at);
+    const uint64_t own = kept_sum(at, v4);
+    uint64_t upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t x = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint64_t round = __shfl_sync(kFull, upto, 31);
+    if (target >= before + round) {
+      before += round;
+      continue;
+    }
+    before += upto - own;
+    if (target >= before && target < before + own) {
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (key_at(v[q], at + q) < from) continue;
+        const uint64_t w = weight_of(v[q], s, table);
+        if (target < before + w) {
+          a.ids[m] = at + q - lead;
+          if (a.logprob)
+            a.logprob[m] = (float)(((double)v[q] - (double)top) / s_t - log((double)all * 0x1p-44));
+          break;
+        }
+        before += w;
+      }
+    }
+    break;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t st) {
-  const cudaError_t e = launch_dependent(sample_kernel, dim3((unsigned)a.M), dim3(kNT), 0, st, a);
+  // CTAs per row: as few as keep it in shared memory, and more while all rows' CTAs are resident at once
+  int c = 1;
+  auto per_cta = [&](int n) { return ((a.vocab + 3 + 3) / 4 + n - 1) / n * 4; };  // places, the row's lead among them
+  while (c < kMaxC && (per_cta(c) > 16 * 1024 || ((int64_t)a.M * 2 * c <= 304 && per_cta(2 * c) >= 4 * kNT))) c *= 2;
+  const int per = per_cta(c), in_shared = per <= kMostShared;
+  const size_t smem = in_shared ? (size_t)per * 4 : 0;
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.M * c);
+  cfg.blockDim = dim3(kNT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = c;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, sample_kernel, a, per, in_shared);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
