@@ -8,9 +8,9 @@
 //
 // Which token that is may hang on the last bits of a sum over the vocabulary, so the sums must not depend on how
 // they are split: a weight is a whole number of 2^-44 and sums are 64-bit integers, exact in any order.
-// A weight is 2^-E, E = (max - x) log2(e) / T held with 32 bits behind the point: the difference to the maximum and
-// its product with log2(e) / T are each two fp32 (the rounded value and the rounding's rest), 2^-F of the fraction F
-// a table of 64 and a cubic in what is left (|r| <= 2^-7): good to 2^-29 of the weight, 2^-31 on average.
+// A weight is 2^-E, E = (max - x) log2(e) / T good to 32 bits behind the point: the difference to the maximum and
+// its product with log2(e) / T are each two fp32 (the rounded value and the rounding's rest), 2^-E a table of 256 for the
+// nearest 256th and a cubic in what is left: good to 2^-29 of the weight, 2^-31 on average.
 //
 // A row is shared by the CTAs of a cluster, which keep it in shared memory (from global again where it is too long) and join
 // through distributed shared memory.  With a temperature or min-p alone one pass sums the weights.  Top-k and top-p look
@@ -51,36 +51,67 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 // (logit, then the lower id): the greater the further ahead
 __device__ __forceinline__ uint64_t key_of(float x, int id) { return (uint64_t)order_of(x) << 32 | (uint32_t)~id; }
 
-// 2^(31 - (j + 1/2) / 64)
-__device__ const uint32_t kPowers[64] = {
-    2135885998u, 2112878262u, 2090118366u, 2067603638u, 2045331439u, 2023299156u, 2001504204u, 1979944027u,
-    1958616096u, 1937517909u, 1916646992u, 1896000896u, 1875577199u, 1855373507u, 1835387448u, 1815616678u,
-    1796058879u, 1776711757u, 1757573041u, 1738640488u, 1719911875u, 1701385007u, 1683057710u, 1664927835u,
-    1646993254u, 1629251865u, 1611701585u, 1594340357u, 1577166143u, 1560176931u, 1543370725u, 1526745556u,
-    1510299473u, 1494030547u, 1477936870u, 1462016553u, 1446267730u, 1430688553u, 1415277195u, 1400031848u,
-    1384950723u, 1370032052u, 1355274085u, 1340675091u, 1326233356u, 1311947188u, 1297814910u, 1283834865u,
-    1270005413u, 1256324931u, 1242791816u, 1229404479u, 1216161350u, 1203060876u, 1190101520u, 1177281762u,
-    1164600099u, 1152055042u, 1139645120u, 1127368878u, 1115224875u, 1103211687u, 1091327906u, 1079572136u,
+// 2^(31 - j / 256)
+__device__ const uint32_t kPowers[256] = {
+    2147483648u, 2141676973u, 2135885998u, 2130110682u, 2124350982u, 2118606857u, 2112878262u, 2107165158u,
+    2101467502u, 2095785251u, 2090118366u, 2084466803u, 2078830522u, 2073209480u, 2067603638u, 2062012954u,
+    2056437387u, 2050876895u, 2045331439u, 2039800978u, 2034285470u, 2028784876u, 2023299156u, 2017828268u,
+    2012372174u, 2006930832u, 2001504204u, 1996092249u, 1990694927u, 1985312200u, 1979944027u, 1974590370u,
+    1969251188u, 1963926443u, 1958616096u, 1953320108u, 1948038440u, 1942771053u, 1937517909u, 1932278970u,
+    1927054196u, 1921843549u, 1916646992u, 1911464486u, 1906295993u, 1901141476u, 1896000896u, 1890874216u,
+    1885761398u, 1880662405u, 1875577199u, 1870505744u, 1865448001u, 1860403934u, 1855373507u, 1850356681u,
+    1845353420u, 1840363688u, 1835387448u, 1830424663u, 1825475297u, 1820539314u, 1815616678u, 1810707353u,
+    1805811301u, 1800928489u, 1796058879u, 1791202437u, 1786359126u, 1781528911u, 1776711757u, 1771907628u,
+    1767116489u, 1762338305u, 1757573041u, 1752820662u, 1748081133u, 1743354420u, 1738640488u, 1733939301u,
+    1729250827u, 1724575029u, 1719911875u, 1715261330u, 1710623359u, 1705997930u, 1701385007u, 1696784557u,
+    1692196547u, 1687620943u, 1683057710u, 1678506817u, 1673968228u, 1669441912u, 1664927835u, 1660425963u,
+    1655936265u, 1651458706u, 1646993254u, 1642539877u, 1638098541u, 1633669214u, 1629251865u, 1624846459u,
+    1620452965u, 1616071351u, 1611701585u, 1607343634u, 1602997467u, 1598663052u, 1594340357u, 1590029350u,
+    1585730000u, 1581442275u, 1577166143u, 1572901575u, 1568648537u, 1564406999u, 1560176931u, 1555958300u,
+    1551751076u, 1547555228u, 1543370725u, 1539197537u, 1535035634u, 1530884983u, 1526745556u, 1522617322u,
+    1518500250u, 1514394310u, 1510299473u, 1506215708u, 1502142985u, 1498081275u, 1494030547u, 1489990772u,
+    1485961921u, 1481943963u, 1477936870u, 1473940611u, 1469955159u, 1465980482u, 1462016553u, 1458063343u,
+    1454120821u, 1450188960u, 1446267730u, 1442357104u, 1438457051u, 1434567544u, 1430688553u, 1426820052u,
+    1422962010u, 1419114401u, 1415277195u, 1411450365u, 1407633882u, 1403827719u, 1400031848u, 1396246240u,
+    1392470869u, 1388705706u, 1384950723u, 1381205894u, 1377471191u, 1373746586u, 1370032052u, 1366327563u,
+    1362633090u, 1358948606u, 1355274085u, 1351609500u, 1347954824u, 1344310030u, 1340675091u, 1337049980u,
+    1333434672u, 1329829140u, 1326233356u, 1322647296u, 1319070932u, 1315504238u, 1311947188u, 1308399756u,
+    1304861917u, 1301333643u, 1297814910u, 1294305692u, 1290805962u, 1287315695u, 1283834865u, 1280363448u,
+    1276901417u, 1273448747u, 1270005413u, 1266571390u, 1263146652u, 1259731174u, 1256324931u, 1252927899u,
+    1249540052u, 1246161366u, 1242791816u, 1239431376u, 1236080024u, 1232737732u, 1229404479u, 1226080238u,
+    1222764986u, 1219458698u, 1216161350u, 1212872918u, 1209593378u, 1206322705u, 1203060876u, 1199807867u,
+    1196563654u, 1193328213u, 1190101520u, 1186883552u, 1183674286u, 1180473697u, 1177281762u, 1174098458u,
+    1170923762u, 1167757650u, 1164600099u, 1161451085u, 1158310587u, 1155178580u, 1152055042u, 1148939949u,
+    1145833280u, 1142735011u, 1139645120u, 1136563583u, 1133490379u, 1130425485u, 1127368878u, 1124320536u,
+    1121280436u, 1118248556u, 1115224875u, 1112209370u, 1109202018u, 1106202798u, 1103211687u, 1100228665u,
+    1097253708u, 1094286796u, 1091327906u, 1088377016u, 1085434106u, 1082499153u, 1079572136u, 1076653033u,
+};
+struct Power {
+  uint32_t value;
+  float rounded;
 };
 
 struct Scale {  // of a row's exponents
   float top, hi, lo;
 };
-__device__ __forceinline__ uint64_t weight_of(float x, const Scale& s, const uint32_t* table) {
-  if (x == -INFINITY) return 0;
+// E rounded to fp32: monotone in x, as the keys are
+__device__ __forceinline__ float exponent_of(float x, const Scale& s) { return __fmul_rn(s.top - x, s.hi); }
+// Whole numbers come out of the mantissa of a sum with 1.5 2^23 units, and no conversion is needed (they share the
+// exponentials' unit).
+constexpr float kWhole = 12582912.f;
+constexpr int kWholeBits = 0x4b400000;
+__device__ __forceinline__ uint64_t weight_of(float x, const Scale& s, const Power* table) {
   const float d = s.top - x, t = d - s.top, rest = (s.top - (d - t)) + (-x - t);  // d + rest is exact
   const float p = __fmul_rn(d, s.hi);  // rounded here: its rest goes to lo
-  if (!(p < 46.f)) return 0;
+  if (!(p < kLightest)) return 0;      // (an infinite difference too)
   const float lo = fmaf(d, s.lo, __fmul_rn(rest, s.hi)) + fmaf(d, s.hi, -p);
-  const float whole = floorf(p);
-  long long e = ((long long)(int)whole << 32) + __float2uint_rn((p - whole) * 4294967296.f) + __float2int_rn(lo * 4294967296.f);
-  if (e <= 0) return 1ull << 44;
-  const uint32_t f = (uint32_t)e;
-  const uint32_t w = table[f >> 26];
-  const float z = (float)((int)(f & 0x3ffffffu) - (1 << 25)) * -1.6138637e-10f;  // - ln 2 / 2^32
+  const float k = p + kWhole / 256.f;  // p to the nearest 256th
+  const int bits = __float_as_int(k) - (kWholeBits - (8 << 23));
+  const Power w = table[bits & 255];
+  const float z = ((p - (k - kWhole / 256.f)) + lo) * -0.69314718f;  // 2^-(rest of E) = 1 + z + z^2 / 2 + z^3 / 6
   const float q = fmaf(fmaf(z, 1.f / 6.f, 0.5f), z * z, z);
-  const uint32_t v = min(w + __float2int_rn((float)w * q), 1u << 31);
-  return ((uint64_t)v << 13) >> (int)(e >> 32);
+  const uint32_t v = w.value + (uint32_t)(__float_as_int(fmaf(w.rounded, q, kWhole)) - kWholeBits);
+  return ((uint64_t)v << 13) >> (bits >> 8);
 }
 
 // the larger of the two, NaN if x is one (fmaxf drops it)
@@ -116,6 +147,15 @@ __device__ __forceinline__ uint64_t share_up(float p, uint64_t all) {
   return __umul64hi(q, all) + (q * all != 0);
 }
 
+// A key as an edge: whether a token's reaches it.
+struct Edge {
+  float x;
+  uint32_t id;
+  __device__ __forceinline__ explicit Edge(uint64_t key)
+      : x(key >> 32 ? logit_of((uint32_t)(key >> 32)) : -INFINITY), id((uint32_t)key) {}
+  __device__ __forceinline__ bool reached(float y, int of) const { return y > x || (y == x && ~(uint32_t)of >= id); }
+};
+
 // A division of the keys into bins, the highest keys first: by the weight, or evenly by key from `high` down.
 struct Bins {
   uint64_t low, high;  // keys [low, high] are divided, the others have no bin
@@ -138,8 +178,8 @@ enum { kFound, kAgain, kDivide };  // the border is known; it lies in another bi
 __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int per_cta, int in_shared) {
   extern __shared__ __align__(16) float s_row[];
   __shared__ Shared sh;
-  __shared__ uint32_t table[64];
-  __shared__ uint64_t s_sum[kNW], s_sum2[kNW], s_sum3[kNW], s_least[kNW], s_most[kNW];
+  __shared__ Power table[256];
+  __shared__ uint64_t s_sum[kNW], s_above[kNW], s_sum2[kNW], s_sum3[kNW], s_least[kNW], s_most[kNW];
   __shared__ float s_top[kNW], s_scale[2], s_floor;
   __shared__ double s_t, s_min;
   cg::cluster_group cl = cg::this_cluster();
@@ -148,7 +188,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
   cl.barrier_arrive();  // all have begun where it is waited for: then their memory may be written
   tc::griddep_wait();
   tc::griddep_launch_dependents();  // after the wait: what follows may then rely on all work before this kernel
-  if (tid < 64) table[tid] = kPowers[tid];
+  if (tid < 256) table[tid] = Power{kPowers[tid], (float)kPowers[tid]};
 
   // The row from the 16-byte boundary at or before it on: place i holds id i - lead.  This CTA's places are
   // [i0, i1), in vectors of four; a place outside the row holds -inf.
@@ -220,6 +260,10 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
   };
   auto key_at = [&](float x, int place) { return key_of(x, place - lead); };
   Shared* first = cl.map_shared_rank(&sh, 0);
+  // Exact sums: each warp those of a run of vectors, so that they add up in the order of ids.
+  const int vectors = (i1 - i0) / 4, per_warp = (vectors + kNW - 1) / kNW;
+  const int v0 = min(vectors, warp * per_warp), v1 = min(vectors, v0 + per_warp);
+  int summed = -1;  // >= 0: s_above holds the warps' exact sums of all tokens kept so far above that bin, by the weight
 
   // Of the keys from `from` on: the lowest before which fewer than k of them lie (share < 0), or before which less than
   // `share` of their sum does.
@@ -227,15 +271,28 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
     const bool by_weight = share >= 0.f;
     Bins bins{from, ~0ull, -1};
     uint64_t base = 0, limit = k;  // what lies above the bins; by_weight: limit is known after the first sums
-    auto exponent = [&](float x) { return __fmul_rn(s.top - x, s.hi); };  // monotone in x, as the keys are
-    auto bin_of = [&](float x, uint64_t key) {
-      if (bins.shift >= 0) return key >= bins.low && key <= bins.high ? (int)((bins.high - key) >> bins.shift) : -1;
-      const float p = exponent(x);
-      return key >= bins.low && p < kLightest ? min((int)(p * kPerOctave), kBins - 1) : -1;
+    // by the weight: the nearest 64th of the exponent, and what the weight is of the bin's, 2^(-rest / 64) (the rest
+    // within a half)
+    struct Place {
+      int bin;
+      float rest;
     };
-    auto bin_exponent = [&](int b) {  // of a bin's highest key
+    auto place_of = [&](float p) {
+      const float k = __fmul_rn(p, (float)kPerOctave) + kWhole, near = k - kWhole;
+      return Place{__float_as_int(k) - kWholeBits, fmaf(p, (float)kPerOctave, -near)};
+    };
+    const Edge low{from};
+    auto bin_of = [&](float x, int place) {
+      if (bins.shift >= 0) {
+        const uint64_t key = key_at(x, place);
+        return key >= bins.low && key <= bins.high ? (int)((bins.high - key) >> bins.shift) : -1;
+      }
+      const float p = exponent_of(x, s);
+      return p < kLightest && low.reached(x, place - lead) ? min(place_of(p).bin, kBins - 1) : -1;
+    };
+    auto bin_exponent = [&](int b) {  // by key: of a bin's highest key
       if (bins.shift < 0) return (float)b * (1.f / kPerOctave);
-      return exponent(logit_of((uint32_t)((bins.high - ((uint64_t)b << bins.shift)) >> 32)));
+      return exponent_of(logit_of((uint32_t)((bins.high - ((uint64_t)b << bins.shift)) >> 32)), s);
     };
     for (bool first_sums = true;;) {
       // What the bins hold: tokens, or roughly their weights in terms of the bin's heaviest (whole numbers, in any order).
@@ -243,9 +300,16 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
         const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int b = bin_of(v[q], key_at(v[q], i + q));
+          const int b = bin_of(v[q], i + q);
           if (b < 0) continue;
-          const uint32_t n = by_weight ? __float2uint_rn(ex2(bin_exponent(b) - exponent(v[q])) * kUnit) : 1u;
+          uint32_t n = 1;
+          if (by_weight) {
+            const float p = exponent_of(v[q], s);
+            if (bins.shift < 0 && b < kBins - 1)  // 2^x = 1 + x ln 2 is near enough
+              n = (uint32_t)(__float_as_int(fmaf(place_of(p).rest, -0.69314718f / kPerOctave * kUnit, kWhole + kUnit)) - kWholeBits);
+            else
+              n = __float2uint_rn(ex2(bin_exponent(b) - p) * kUnit);
+          }
           if (n) atomicAdd(&sh.hist[b], n);
         }
       });
@@ -309,27 +373,31 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
         // The exact sums above the bin and in it, its keys' ends, and its tokens, listed as far as they fit.
         const int bin = sh.bin;
         uint64_t above = 0, in = 0, all = 0, least = ~0ull, most = 0;
-        each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+        each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
           const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint64_t key = key_at(v[q], i + q);
-            const int b = bin_of(v[q], key);
+            const int b = bin_of(v[q], i + q);
             if (b < 0 || (b > bin && !(by_weight && first_sums))) continue;
             const uint64_t w = by_weight ? weight_of(v[q], s, table) : 1;
-            all += w;
-            if (b < bin) above += w;
-            if (b != bin) continue;
-            in += w;
-            least = min(least, key);
-            most = max(most, key);
-            const int at = first->listed < kList ? atomicAdd(&first->listed, 1) : kList;
-            if (at < kList) {
-              first->key[at] = key;
-              first->weight[at] = w;
+            if (b < bin) {
+              above += w;
+            } else if (b > bin) {
+              all += w;
+            } else {
+              const uint64_t key = key_at(v[q], i + q);
+              in += w;
+              least = min(least, key);
+              most = max(most, key);
+              const int at = first->listed < kList ? atomicAdd(&first->listed, 1) : kList;
+              if (at < kList) {
+                first->key[at] = key;
+                first->weight[at] = w;
+              }
             }
           }
         });
+        all += above + in;
         above = warp_sum(above);
         in = warp_sum(in);
         all = warp_sum(all);
@@ -339,7 +407,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
           most = max(most, __shfl_xor_sync(kFull, most, o));
         }
         if (lane == 0) {
-          s_sum[warp] = above;
+          s_above[warp] = above;
           s_sum2[warp] = in;
           s_sum3[warp] = all;
           s_least[warp] = least;
@@ -348,7 +416,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
         __syncthreads();
         if (tid == 0) {
           for (int w = 1; w < kNW; ++w) {
-            above += s_sum[w];
+            above += s_above[w];
             in += s_sum2[w];
             all += s_sum3[w];
             least = min(least, s_least[w]);
@@ -414,7 +482,10 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
         cl.sync();
         limit = sh.all[0];
         first_sums = false;
-        if (sh.state == kFound) return sh.border;
+        if (sh.state == kFound) {
+          summed = by_weight && bins.shift < 0 ? bin : -1;
+          return sh.border;
+        }
         if (sh.state == kDivide) {
           bins = sh.bins;
           base = sh.above[0];
@@ -427,6 +498,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
   uint64_t from = 0;
   if (tk > 0 && tk < V) from = lowest(from, tk, -1.f);
   if (tp < 1.f) from = lowest(from, 0, fmaxf(tp, 0.f));
+  const uint64_t border = from;
   if (mp > 0.f) {
     // w >= mp is x >= top + T ln mp: from the lowest fp32 that is not less
     if (tid == 0) s_floor = __double2float_ru((double)top + s_min);
@@ -434,20 +506,32 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
     from = max(from, uint64_t(order_of(s_floor)) << 32);
   }
 
-  // The sums of the kept weights: each warp those of a run of vectors, so that they add up in the order of ids.
-  const int vectors = (i1 - i0) / 4, per_warp = (vectors + kNW - 1) / kNW;
-  const int v0 = min(vectors, warp * per_warp), v1 = min(vectors, v0 + per_warp);
+  // The sums of the kept weights.
+  const Edge edge{from};
   auto kept_sum = [&](int i, float4 v4) {
     const float v[4] = {v4.x, v4.y, v4.z, v4.w};
     uint64_t w = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (key_at(v[q], i + q) >= from) w += weight_of(v[q], s, table);
+      if (edge.reached(v[q], i + q - lead)) w += weight_of(v[q], s, table);
     return w;
   };
   uint64_t mine = 0;
-  each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v) { mine += kept_sum(i, v); });
+  if (summed >= 0 && from == border) {  // known but for the border's bin
+    each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float k = __fmul_rn(exponent_of(v[q], s), (float)kPerOctave) + kWhole;
+        if (min(__float_as_int(k) - kWholeBits, kBins - 1) == summed && edge.reached(v[q], i + q - lead))
+          mine += weight_of(v[q], s, table);
+      }
+    });
+  } else {
+    each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v) { mine += kept_sum(i, v); });
+  }
   mine = warp_sum(mine);
+  if (summed >= 0 && from == border) mine += s_above[warp];
   __syncthreads();  // (s_sum may still be read)
   if (lane == 0) s_sum[warp] = mine;
   __syncthreads();
@@ -488,7 +572,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
       const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (key_at(v[q], at + q) < from) continue;
+        if (!edge.reached(v[q], at + q - lead)) continue;
         const uint64_t w = weight_of(v[q], s, table);
         if (target < before + w) {
           a.ids[m] = at + q - lead;
