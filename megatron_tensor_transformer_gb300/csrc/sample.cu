@@ -7,10 +7,11 @@
 // and the lowest id up to which the kept weights exceed u times their sum is chosen.
 //
 // Which token that is may hang on the last bits of a sum over the vocabulary, so the sums must not depend on how
-// they are split: a weight is a whole number of 2^-44 and sums are 64-bit integers, exact in any order.
-// A weight is 2^-E, E = (max - x) log2(e) / T good to 32 bits behind the point: the difference to the maximum and
-// its product with log2(e) / T are each two fp32 (the rounded value and the rounding's rest), 2^-E a table of 256 for the
-// nearest 256th and a cubic in what is left: good to 2^-29 of the weight, 2^-31 on average.
+// they are split: a weight is a whole number of 2^-44 (of a power of two at or
+// just above the largest) and sums are 64-bit integers, exact in any order.
+// A weight is 2^-E, E good to 32 bits behind the point: the product of x with log2(e) / T is two fp32 (the rounded value
+// and the rounding's rest), taken from a whole number so that nothing is lost; 2^-E is a table of 256 for the nearest
+// 256th and a parabola in what is left: good to 2^-29 of the weight, 2^-31 on average.
 //
 // A row is shared by the CTAs of a cluster, which keep it in shared memory (from global again where it is too long) and join
 // through distributed shared memory.  With a temperature or min-p alone one pass sums the weights.  Top-k and top-p look
@@ -33,10 +34,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kNT = 512, kNW = kNT / 32, kMaxC = 8;
-constexpr int kPerOctave = 64, kOctaves = 24;            // bins of the first division, by the weight
+constexpr int kMaxC = 8;
+constexpr int kPerOctave = 64, kOctaves = 16;            // bins of the first division, by the weight
 constexpr int kBins = kPerOctave * kOctaves;             // the last one holds all that is lighter
-static_assert(kBins % kNT == 0, "bins per thread");
 constexpr float kUnit = 4096.f;                          // of the approximate weights
 constexpr int kList = 512;                               // tokens that are listed
 constexpr int kMostShared = 40 * 1024;                   // logits of a CTA that are kept in shared memory
@@ -91,27 +91,44 @@ struct Power {
   float rounded;
 };
 
-struct Scale {  // of a row's exponents
+// Of a row: its largest logit, log2(e) / T in two parts, and the whole number R that weights are held against: 2^(y - R),
+// y = x log2(e) / T, so that R is at or just above the largest y.  R of kFar: y is too large for it, and weights are held
+// against the largest itself.
+struct Scale {
   float top, hi, lo;
+  int whole;
+  float above_top;  // 2^R over the largest weight: in [1, 2), about
 };
-// E rounded to fp32: monotone in x, as the keys are
+constexpr int kFar = 1 << 30;
+// (max - x) log2(e) / T rounded to fp32: monotone in x, as the keys are
 __device__ __forceinline__ float exponent_of(float x, const Scale& s) { return __fmul_rn(s.top - x, s.hi); }
 // Whole numbers come out of the mantissa of a sum with 1.5 2^23 units, and no conversion is needed (they share the
 // exponentials' unit).
 constexpr float kWhole = 12582912.f;
 constexpr int kWholeBits = 0x4b400000;
-__device__ __forceinline__ uint64_t weight_of(float x, const Scale& s, const Power* table) {
-  const float d = s.top - x, t = d - s.top, rest = (s.top - (d - t)) + (-x - t);  // d + rest is exact
-  const float p = __fmul_rn(d, s.hi);  // rounded here: its rest goes to lo
-  if (!(p < kLightest)) return 0;      // (an infinite difference too)
-  const float lo = fmaf(d, s.lo, __fmul_rn(rest, s.hi)) + fmaf(d, s.hi, -p);
-  const float k = p + kWhole / 256.f;  // p to the nearest 256th
-  const int bits = __float_as_int(k) - (kWholeBits - (8 << 23));
-  const Power w = table[bits & 255];
-  const float z = ((p - (k - kWhole / 256.f)) + lo) * -0.69314718f;  // 2^-(rest of E) = 1 + z + z^2 / 2 + z^3 / 6
-  const float q = fmaf(fmaf(z, 1.f / 6.f, 0.5f), z * z, z);
+// y of kFar aside, for an exponent below kLightest.
+__device__ __forceinline__ uint64_t near_weight(float x, const Scale& s, const Power* table) {
+  const float y = __fmul_rn(x, s.hi), k = y + kWhole / 256.f, near = k - kWhole / 256.f;
+  const float rest = (y - near) + fmaf(x, s.lo, fmaf(x, s.hi, -y));
+  const int d = s.whole * 256 + (kWholeBits - (8 << 23)) - __float_as_int(k);  // 256 (R - near)
+  const float z = rest * 0.69314718f, q = fmaf(z * 0.5f, z, z);  // 2^rest = 1 + z + z^2 / 2, |z| below 2^-9.5
+  const Power w = table[d & 255];
   const uint32_t v = w.value + (uint32_t)(__float_as_int(fmaf(w.rounded, q, kWhole)) - kWholeBits);
-  return ((uint64_t)v << 13) >> (bits >> 8);
+  return ((uint64_t)v << 13) >> (d >> 8 & 63);
+}
+__device__ __noinline__ uint64_t far_weight(float x, const Scale& s, const Power* table) {
+  const float df = s.top - x, t = df - s.top, left = (s.top - (df - t)) + (-x - t);  // df + left is exact
+  const float y = __fmul_rn(df, s.hi), k = y + kWhole / 256.f, near = k - kWhole / 256.f;
+  const float rest = -((y - near) + (fmaf(df, s.lo, __fmul_rn(left, s.hi)) + fmaf(df, s.hi, -y)));
+  const int d = __float_as_int(k) - (kWholeBits - (8 << 23));
+  const float z = rest * 0.69314718f, q = fmaf(z * 0.5f, z, z);
+  const Power w = table[d & 255];
+  const uint32_t v = w.value + (uint32_t)(__float_as_int(fmaf(w.rounded, q, kWhole)) - kWholeBits);
+  return ((uint64_t)v << 13) >> (d >> 8 & 63);
+}
+__device__ __forceinline__ uint64_t weight_of(float x, const Scale& s, const Power* table) {
+  if (!(exponent_of(x, s) < kLightest)) return 0;  // (an infinite difference too)
+  return s.whole != kFar ? near_weight(x, s, table) : far_weight(x, s, table);
 }
 
 // the larger of the two, NaN if x is one (fmaxf drops it)
@@ -175,13 +192,16 @@ struct Shared {
 enum { kFound, kAgain, kDivide };  // the border is known; it lies in another bin; divide the bin
 
 // Grid: M clusters of C CTAs.
-__global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int per_cta, int in_shared) {
+template <int kNT, int kPerSm>
+__global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a, int per_cta, int in_shared) {
+  constexpr int kNW = kNT / 32;
+  static_assert(kBins % kNT == 0, "bins per thread");
   extern __shared__ __align__(16) float s_row[];
   __shared__ Shared sh;
   __shared__ Power table[256];
   __shared__ uint64_t s_sum[kNW], s_above[kNW], s_sum2[kNW], s_sum3[kNW], s_least[kNW], s_most[kNW];
   __shared__ float s_top[kNW], s_scale[2], s_floor;
-  __shared__ double s_t, s_min;
+  __shared__ double s_inv, s_min;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), c = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, m = blockIdx.x / C, V = a.vocab;
@@ -210,7 +230,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
     const double t64 = T <= 0.f ? 1.0 : fmax((double)T, 0x1p-100), scale = 1.4426950408889634 / t64;
     s_scale[0] = (float)scale;
     s_scale[1] = (float)(scale - (double)s_scale[0]);
-    s_t = t64;
+    s_inv = 1.0 / t64;
     s_min = mp > 0.f ? t64 * log((double)fminf(mp, 1.f)) : 0.0;
   }
   float top = -INFINITY;
@@ -238,7 +258,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
   if (warp == 0) {
     top = s_top[lane % kNW];
 #pragma unroll
-    for (int o = kNW / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, o));
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, o));
     if (lane < C) cl.map_shared_rank(&sh, lane)->top[c] = top;
   }
   cl.sync();
@@ -252,7 +272,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
     }
     return;
   }
-  const Scale s{top, s_scale[0], s_scale[1]};
+  const float y_top = __fmul_rn(top, s_scale[0]);
+  const bool near = fabsf(y_top) < 8000.f;
+  const Scale s{top, s_scale[0], s_scale[1], near ? (int)ceilf(y_top) : kFar, near ? ex2(ceilf(y_top) - y_top) : 1.f};
 
   // f(place, four logits) over the CTA's vectors
   auto each = [&](int from, int to, int step, auto f) {
@@ -278,7 +300,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
       float rest;
     };
     auto place_of = [&](float p) {
-      const float k = __fmul_rn(p, (float)kPerOctave) + kWhole, near = k - kWhole;
+      const float k = fmaf(p, (float)kPerOctave, kWhole), near = k - kWhole;
       return Place{__float_as_int(k) - kWholeBits, fmaf(p, (float)kPerOctave, -near)};
     };
     const Edge low{from};
@@ -296,7 +318,21 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
     };
     for (bool first_sums = true;;) {
       // What the bins hold: tokens, or roughly their weights in terms of the bin's heaviest (whole numbers, in any order).
-      each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+      const bool plain = by_weight && bins.shift < 0 && from == 0 && s.whole != kFar;  // the usual case, in fewer steps
+      if (plain) {
+        each(i0 + 4 * tid, i1, 4 * kNT, [&](int, float4 v4) {
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float p = exponent_of(v[q], s);
+            const Place at = place_of(p);
+            // 2^x = 1 + x ln 2 is near enough
+            uint32_t n = (uint32_t)(__float_as_int(fmaf(at.rest, -0.69314718f / kPerOctave * kUnit, kWhole + kUnit)) - kWholeBits);
+            if (at.bin >= kBins - 1) n = p < kLightest ? __float2uint_rn(ex2(bin_exponent(kBins - 1) - p) * kUnit) : 0;
+            if (n) atomicAdd(&sh.hist[min(at.bin, kBins - 1)], n);
+          }
+        });
+      } else each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
         const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -352,7 +388,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
           all += s_sum[w];
         }
         uint64_t goal = limit - base;
-        if (by_weight) goal = first_sums ? share_down(share, all) : (uint64_t)((float)goal * (0x1p-20f * ex2(p0)));
+        if (by_weight) goal = first_sums ? share_down(share, all) : (uint64_t)((float)goal * (0x1p-20f * s.above_top * ex2(p0)));
         if (goal == 0) goal = 1;
 #pragma unroll
         for (int q = 0; q < kEach; ++q) {
@@ -373,28 +409,46 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
         // The exact sums above the bin and in it, its keys' ends, and its tokens, listed as far as they fit.
         const int bin = sh.bin;
         uint64_t above = 0, in = 0, all = 0, least = ~0ull, most = 0;
-        each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
+        auto list = [&](float x, int place, uint64_t w) {
+          const uint64_t key = key_at(x, place);
+          in += w;
+          least = min(least, key);
+          most = max(most, key);
+          const int at = first->listed < kList ? atomicAdd(&first->listed, 1) : kList;
+          if (at < kList) {
+            first->key[at] = key;
+            first->weight[at] = w;
+          }
+        };
+        if (plain) {
+          each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
+            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+            bool any = false;
+            uint64_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float p = exponent_of(v[q], s);
+              const int b = min(place_of(p).bin, kBins - 1);
+              w[q] = near_weight(v[q], s, table);
+              if (!(p < kLightest)) w[q] = 0;
+              if (b < bin) above += w[q];
+              if (b > bin) all += w[q];
+              any |= b == bin;
+            }
+            if (!any) return;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (w[q] && min(place_of(exponent_of(v[q], s)).bin, kBins - 1) == bin) list(v[q], i + q, w[q]);
+          });
+        } else each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
           const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int b = bin_of(v[q], i + q);
-            if (b < 0 || (b > bin && !(by_weight && first_sums))) continue;
             const uint64_t w = by_weight ? weight_of(v[q], s, table) : 1;
-            if (b < bin) {
-              above += w;
-            } else if (b > bin) {
-              all += w;
-            } else {
-              const uint64_t key = key_at(v[q], i + q);
-              in += w;
-              least = min(least, key);
-              most = max(most, key);
-              const int at = first->listed < kList ? atomicAdd(&first->listed, 1) : kList;
-              if (at < kList) {
-                first->key[at] = key;
-                first->weight[at] = w;
-              }
-            }
+            above += b >= 0 && b < bin ? w : 0;
+            all += b > bin ? w : 0;
+            if (b == bin) list(v[q], i + q, w);
           }
         });
         all += above + in;
@@ -522,9 +576,18 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
       const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float k = __fmul_rn(exponent_of(v[q], s), (float)kPerOctave) + kWhole;
+        const float k = fmaf(exponent_of(v[q], s), (float)kPerOctave, kWhole);
         if (min(__float_as_int(k) - kWholeBits, kBins - 1) == summed && edge.reached(v[q], i + q - lead))
           mine += weight_of(v[q], s, table);
+      }
+    });
+  } else if (from == 0 && s.whole != kFar) {
+    each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int, float4 v4) {
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint64_t w = near_weight(v[q], s, table);
+        if (exponent_of(v[q], s) < kLightest) mine += w;
       }
     });
   } else {
@@ -576,8 +639,11 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
         const uint64_t w = weight_of(v[q], s, table);
         if (target < before + w) {
           a.ids[m] = at + q - lead;
-          if (a.logprob)
-            a.logprob[m] = (float)(((double)v[q] - (double)top) / s_t - log((double)all * 0x1p-44));
+          if (a.logprob) {
+            const double lw = s.whole != kFar ? (double)v[q] * s_inv - s.whole * 0.6931471805599453
+                                              : ((double)v[q] - (double)top) * s_inv;
+            a.logprob[m] = w == all ? 0.f : (float)(lw - log((double)all * 0x1p-44));
+          }
           break;
         }
         before += w;
@@ -587,21 +653,16 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a, int 
   }
 }
 
-}  // namespace
-
-cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t st) {
-  // CTAs per row: as few as keep it in shared memory, and more while all rows' CTAs are resident at once
-  int c = 1;
-  auto per_cta = [&](int n) { return ((a.vocab + 3 + 3) / 4 + n - 1) / n * 4; };  // places, the row's lead among them
-  while (c < kMaxC && (per_cta(c) > 16 * 1024 || ((int64_t)a.M * 2 * c <= 304 && per_cta(2 * c) >= 4 * kNT))) c *= 2;
-  const int per = per_cta(c), in_shared = per <= kMostShared;
-  const size_t smem = in_shared ? (size_t)per * 4 : 0;
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared * 4);
+template <int NT, int PER_SM>
+cudaError_t launch(const SampleArgs& a, int c, int per, cudaStream_t st) {
+  auto kernel = sample_kernel<NT, PER_SM>;
+  const int in_shared = per <= kMostShared;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.M * c);
-  cfg.blockDim = dim3(kNT);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = in_shared ? (size_t)per * 4 : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -611,9 +672,21 @@ cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, sample_kernel, a, per, in_shared);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, per, in_shared);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t st) {
+  // CTAs per row: as few as keep it in shared memory, and more while all rows' CTAs are resident at once
+  int c = 1;
+  auto per_cta = [&](int n) { return ((a.vocab + 3 + 3) / 4 + n - 1) / n * 4; };  // places, the row's lead among them
+  while (c < kMaxC && (per_cta(c) > 16 * 1024 || ((int64_t)a.M * 2 * c <= 2 * 152 && per_cta(2 * c) >= 2048))) c *= 2;
+  const int per = per_cta(c);
+  // one CTA of many threads per SM where there are no more CTAs than SMs
+  return (int64_t)a.M * c <= 152 && per > 4096 ? launch<1024, 1>(a, c, per, st) : launch<512, 2>(a, c, per, st);
 }
 
 }  // namespace tpx
