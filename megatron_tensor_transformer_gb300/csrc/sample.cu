@@ -35,11 +35,10 @@ namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxC = 8;
-constexpr int kPerOctave = 64, kOctaves = 16;            // bins of the first division, by the weight
-constexpr int kBins = kPerOctave * kOctaves;             // the last one holds all that is lighter
+constexpr int kBins = 1024;                              // of a division by key, and by the weight
 constexpr float kUnit = 4096.f;                          // of the approximate weights
-constexpr int kList = 512;                               // tokens that are listed
-constexpr int kMostShared = 40 * 1024;                   // logits of a CTA that are kept in shared memory
+constexpr int kList = 256;                               // tokens that are listed
+constexpr int kMostShared = 32 * 1024;                   // logits of a CTA that are kept in shared memory
 constexpr float kLightest = 46.f;                        // exponent from which a weight is 0
 
 // Orders as the logit does, -0 as +0.
@@ -178,10 +177,21 @@ struct Bins {
   uint64_t low, high;  // keys [low, high] are divided, the others have no bin
   int shift;           // < 0: by the weight
 };
+// The bin, by the weight, of an exponent below kLightest: the nearest 64th up to 15 octaves, then half octaves.  Monotone.
+constexpr int kPerOctave = 64, kOctaves = 16, kFine = (kOctaves - 1) * kPerOctave;
+__device__ __forceinline__ int nearest_64th(float p) {  // large for a large exponent and an infinite one
+  return __float_as_int(fmaf(p, (float)kPerOctave, kWhole)) - kWholeBits;
+}
+__device__ __forceinline__ int weight_bin(float p) {
+  const int b = nearest_64th(p);
+  return b < kFine ? b : kFine + ((b - kFine) >> 5);
+}
+static_assert(kFine + ((46 - 15) * kPerOctave >> 5) < kOctaves * kPerOctave, "kLightest has a bin");
 // What the first CTA tells the others, and what it is told.
 struct Shared {
   float top[kMaxC];
-  uint32_t hist[kBins];
+  uint32_t hist[kBins], fine[2][kMaxC][kPerOctave];  // of the search for top-k's border, and for top-p's: no CTA may still
+  float octave[2][kMaxC][kOctaves];                  // be reading what another one writes
   uint64_t key[kList], weight[kList];
   int listed;                    // tokens of the bin, of which the first kList are listed
   uint64_t above[kMaxC], in[kMaxC], all[kMaxC], least[kMaxC], most[kMaxC];  // of each CTA
@@ -199,9 +209,11 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   extern __shared__ __align__(16) float s_row[];
   __shared__ Shared sh;
   __shared__ Power table[256];
+  __shared__ uint32_t fine[kPerOctave];
   __shared__ uint64_t s_sum[kNW], s_above[kNW], s_sum2[kNW], s_sum3[kNW], s_least[kNW], s_most[kNW];
   __shared__ float s_top[kNW], s_scale[2], s_floor;
   __shared__ double s_inv, s_min;
+  __shared__ int s_at;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), c = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, m = blockIdx.x / C, V = a.vocab;
@@ -215,6 +227,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   const float* row = a.logits + (int64_t)m * a.ldl;
   const int lead = (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
   row -= lead;
+  const int own = in_shared ? per_cta : 0;  // behind the row: the threads' own sums
   const int places = (lead + V + 3) / 4 * 4, i0 = min(places, c * per_cta), i1 = min(places, i0 + per_cta);
   auto vector_at = [&](int i) {  // global memory
     if (i >= lead && i + 4 <= lead + V) return __ldcs(reinterpret_cast<const float4*>(row + i));
@@ -293,16 +306,6 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
     const bool by_weight = share >= 0.f;
     Bins bins{from, ~0ull, -1};
     uint64_t base = 0, limit = k;  // what lies above the bins; by_weight: limit is known after the first sums
-    // by the weight: the nearest 64th of the exponent, and what the weight is of the bin's, 2^(-rest / 64) (the rest
-    // within a half)
-    struct Place {
-      int bin;
-      float rest;
-    };
-    auto place_of = [&](float p) {
-      const float k = fmaf(p, (float)kPerOctave, kWhole), near = k - kWhole;
-      return Place{__float_as_int(k) - kWholeBits, fmaf(p, (float)kPerOctave, -near)};
-    };
     const Edge low{from};
     auto bin_of = [&](float x, int place) {
       if (bins.shift >= 0) {
@@ -310,42 +313,131 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         return key >= bins.low && key <= bins.high ? (int)((bins.high - key) >> bins.shift) : -1;
       }
       const float p = exponent_of(x, s);
-      return p < kLightest && low.reached(x, place - lead) ? min(place_of(p).bin, kBins - 1) : -1;
+      return p < kLightest && low.reached(x, place - lead) ? weight_bin(p) : -1;
     };
     auto bin_exponent = [&](int b) {  // by key: of a bin's highest key
-      if (bins.shift < 0) return (float)b * (1.f / kPerOctave);
+      if (bins.shift < 0)
+        return b < kFine ? (float)b * (1.f / kPerOctave) : (float)(kFine / kPerOctave) + 0.5f * (float)(b - kFine);
       return exponent_of(logit_of((uint32_t)((bins.high - ((uint64_t)b << bins.shift)) >> 32)), s);
     };
-    for (bool first_sums = true;;) {
-      // What the bins hold: tokens, or roughly their weights in terms of the bin's heaviest (whole numbers, in any order).
-      const bool plain = by_weight && bins.shift < 0 && from == 0 && s.whole != kFar;  // the usual case, in fewer steps
+    const bool plain = from == 0;  // the usual case, in fewer steps
+    // The first division, by the weight: the octave that holds the border from sums of a thread's own (one atomic a logit
+    // took 26 cycles a warp), then its bins.  Every CTA comes to the same conclusion from the same numbers.
+    {
+      float* mine = s_row + own + tid;
+#pragma unroll
+      for (int o = 0; o < kOctaves; ++o) mine[o * kNT] = 0.f;
       if (plain) {
         each(i0 + 4 * tid, i1, 4 * kNT, [&](int, float4 v4) {
           const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float p = exponent_of(v[q], s);
-            const Place at = place_of(p);
-            // 2^x = 1 + x ln 2 is near enough
-            uint32_t n = (uint32_t)(__float_as_int(fmaf(at.rest, -0.69314718f / kPerOctave * kUnit, kWhole + kUnit)) - kWholeBits);
-            if (at.bin >= kBins - 1) n = p < kLightest ? __float2uint_rn(ex2(bin_exponent(kBins - 1) - p) * kUnit) : 0;
-            if (n) atomicAdd(&sh.hist[min(at.bin, kBins - 1)], n);
+            const int o = min(nearest_64th(p) >> 6, kOctaves - 1);
+            mine[o * kNT] += by_weight ? ex2(-p) : p < kLightest ? 1.f : 0.f;
           }
         });
-      } else each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+      } else {
+      each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float p = exponent_of(v[q], s);
+          if (!(p < kLightest) || (from != 0 && !low.reached(v[q], i + q - lead))) continue;
+          mine[(weight_bin(p) / kPerOctave) * kNT] += by_weight ? ex2(-p) : 1.f;
+        }
+      });
+      }
+      __syncthreads();
+      for (int o = warp; o < kOctaves; o += kNW) {
+        float sum = 0.f;
+        for (int t = lane; t < kNT; t += 32) sum += s_row[own + o * kNT + t];
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
+        if (lane < C) cl.map_shared_rank(&sh, lane)->octave[by_weight][c][o] = sum;
+      }
+      if (tid < kPerOctave) fine[tid] = 0;
+      cl.sync();
+      auto find = [&](float v, float goal, float& before) {  // the lane whose part of the sum holds goal, and what is before
+        float upto = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float x = __shfl_up_sync(kFull, upto, o);
+          if (lane >= o) upto += x;
+        }
+        const unsigned over = __ballot_sync(kFull, upto >= goal && v > 0.f), some = __ballot_sync(kFull, v > 0.f);
+        const int l = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
+        before = __shfl_sync(kFull, upto - v, l);
+        return l;
+      };
+      float part = 0.f, before, before2;
+      if (lane < kOctaves)
+        for (int r = 0; r < C; ++r) part += sh.octave[by_weight][r][lane];
+      float all = part;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) all += __shfl_xor_sync(kFull, all, x);
+      if (!by_weight && all < (float)k) return from;  // fewer than k tokens have a weight: all are kept
+      const float goal = by_weight ? all * share : (float)k;
+      const int octave = find(part, goal, before);
+      if (plain && octave < kOctaves - 1) {
+        each(i0 + 4 * tid, i1, 4 * kNT, [&](int, float4 v4) {
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float p = exponent_of(v[q], s), near = fmaf(p, (float)kPerOctave, kWhole);
+            const unsigned b = (unsigned)(__float_as_int(near) - (kWholeBits + octave * kPerOctave));
+            // 2^x = 1 + x ln 2 is near enough
+            const float rest = fmaf(p, (float)kPerOctave, kWhole - near);
+            const uint32_t n = (uint32_t)(__float_as_int(fmaf(rest, -0.69314718f / kPerOctave * kUnit, kWhole + kUnit)) - kWholeBits);
+            if (b < kPerOctave) atomicAdd(&fine[b], by_weight ? n : 1u);
+          }
+        });
+      } else {
+      each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float p = exponent_of(v[q], s);
+          if (!(p < kLightest)) continue;
+          const int b = weight_bin(p);
+          if (b / kPerOctave != octave || (from != 0 && !low.reached(v[q], i + q - lead))) continue;
+          const uint32_t n = by_weight ? __float2uint_rn(ex2(bin_exponent(b) - p) * kUnit) : 1u;
+          if (n) atomicAdd(&fine[b % kPerOctave], n);
+        }
+      });
+      }
+      __syncthreads();
+      for (int t = tid; t < C * kPerOctave; t += kNT)
+        cl.map_shared_rank(&sh, t / kPerOctave)->fine[by_weight][c][t % kPerOctave] = fine[t % kPerOctave];
+      cl.sync();
+      // two bins per lane
+      float two[2] = {0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int b = 2 * lane + q;
+        uint32_t n = 0;
+        for (int r = 0; r < C; ++r) n += sh.fine[by_weight][r][b];
+        two[q] = !by_weight || n == 0 ? (float)n : (float)n * ex2(-bin_exponent(octave * kPerOctave + b)) * (1.f / kUnit);
+      }
+      const int l = find(two[0] + two[1], goal - before, before2);
+      const float first_of = __shfl_sync(kFull, two[0], l);
+      const int b = octave * kPerOctave + 2 * l + (first_of > 0.f && before + before2 + first_of >= goal ? 0 : 1);
+      __syncthreads();
+      if (tid == 0) sh.bin = b;
+      __syncthreads();
+    }
+    for (bool first_sums = true;;) {
+      // Divided by key: what the bins hold, tokens, or roughly their weights in terms of the bin's heaviest (whole numbers, in
+      // any order).
+      if (bins.shift >= 0) {
+      each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
         const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int b = bin_of(v[q], i + q);
           if (b < 0) continue;
           uint32_t n = 1;
-          if (by_weight) {
-            const float p = exponent_of(v[q], s);
-            if (bins.shift < 0 && b < kBins - 1)  // 2^x = 1 + x ln 2 is near enough
-              n = (uint32_t)(__float_as_int(fmaf(place_of(p).rest, -0.69314718f / kPerOctave * kUnit, kWhole + kUnit)) - kWholeBits);
-            else
-              n = __float2uint_rn(ex2(bin_exponent(b) - p) * kUnit);
-          }
+          if (by_weight) n = __float2uint_rn(ex2(bin_exponent(b) - exponent_of(v[q], s)) * kUnit);
           if (n) atomicAdd(&sh.hist[b], n);
         }
       });
@@ -382,13 +474,9 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         before -= sum;
         if (tid == 0) sh.bin = kBins - 1;  // where none is found below: too few tokens, or rounding
         __syncthreads();
-        uint64_t all = 0;
-        for (int w = 0; w < kNW; ++w) {
-          if (w < warp) before += s_sum[w];
-          all += s_sum[w];
-        }
+        for (int w = 0; w < warp; ++w) before += s_sum[w];
         uint64_t goal = limit - base;
-        if (by_weight) goal = first_sums ? share_down(share, all) : (uint64_t)((float)goal * (0x1p-20f * s.above_top * ex2(p0)));
+        if (by_weight) goal = (uint64_t)((float)goal * (0x1p-20f * s.above_top * ex2(p0)));
         if (goal == 0) goal = 1;
 #pragma unroll
         for (int q = 0; q < kEach; ++q) {
@@ -397,14 +485,12 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         }
         __syncthreads();
         if (tid < C) {
-          Shared* to = cl.map_shared_rank(&sh, tid);
           const int bin = sh.bin;
-          to->bin = bin;
-          to->state = !by_weight && all < goal ? kFound : kAgain;  // fewer than k tokens have a weight: all are kept
+          cl.map_shared_rank(&sh, tid)->bin = bin;
         }
       }
       cl.sync();
-      if (sh.state == kFound) return from;
+      }
       for (;;) {
         // The exact sums above the bin and in it, its keys' ends, and its tokens, listed as far as they fit.
         const int bin = sh.bin;
@@ -414,31 +500,31 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
           in += w;
           least = min(least, key);
           most = max(most, key);
-          const int at = first->listed < kList ? atomicAdd(&first->listed, 1) : kList;
+          const int at = atomicAdd(&sh.listed, 1);
           if (at < kList) {
-            first->key[at] = key;
-            first->weight[at] = w;
+            sh.key[at] = key;
+            sh.weight[at] = w;
           }
         };
-        if (plain) {
+        if (plain && by_weight && bins.shift < 0 && bin < kFine && s.whole != kFar) {
           each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
             const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-            bool any = false;
             uint64_t w[4];
+            int b[4];
+            bool any = false;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float p = exponent_of(v[q], s);
-              const int b = min(place_of(p).bin, kBins - 1);
+              b[q] = nearest_64th(p);
               w[q] = near_weight(v[q], s, table);
-              if (!(p < kLightest)) w[q] = 0;
-              if (b < bin) above += w[q];
-              if (b > bin) all += w[q];
-              any |= b == bin;
+              if (b[q] < bin) above += w[q];
+              if (b[q] > bin && p < kLightest) all += w[q];
+              any |= b[q] == bin;
             }
             if (!any) return;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              if (w[q] && min(place_of(exponent_of(v[q], s)).bin, kBins - 1) == bin) list(v[q], i + q, w[q]);
+              if (b[q] == bin) list(v[q], i + q, w[q]);
           });
         } else each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
           const float v[4] = {v4.x, v4.y, v4.z, v4.w};
@@ -468,19 +554,27 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
           s_most[warp] = most;
         }
         __syncthreads();
-        if (tid == 0) {
-          for (int w = 1; w < kNW; ++w) {
-            above += s_above[w];
-            in += s_sum2[w];
-            all += s_sum3[w];
-            least = min(least, s_least[w]);
-            most = max(most, s_most[w]);
+        if (warp < 5) {  // one of the five per warp
+          const uint64_t* part = warp == 0 ? s_above : warp == 1 ? s_sum2 : warp == 2 ? s_sum3 : warp == 3 ? s_least : s_most;
+          uint64_t v = lane < kNW ? part[lane] : warp == 3 ? ~0ull : 0;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t x = __shfl_xor_sync(kFull, v, o);
+            v = warp < 3 ? v + x : warp == 3 ? min(v, x) : max(v, x);
           }
-          first->above[c] = above;
-          first->in[c] = in;
-          first->all[c] = all;
-          first->least[c] = least;
-          first->most[c] = most;
+          uint64_t* to = warp == 0 ? first->above : warp == 1 ? first->in : warp == 2 ? first->all : warp == 3 ? first->least
+                                                                                                             : first->most;
+          if (lane == 0) to[c] = v;
+        }
+        if (c != 0) {  // what is listed goes behind what the first CTA has
+          const int n = sh.listed;
+          if (tid == 0) s_at = n ? atomicAdd(&first->listed, n) : 0;
+          __syncthreads();
+          for (int i = tid; i < min(n, kList - s_at); i += kNT) {
+            first->key[s_at + i] = sh.key[i];
+            first->weight[s_at + i] = sh.weight[i];
+          }
+          if (tid == 0) sh.listed = 0;
         }
         cl.sync();
         if (c == 0) {
@@ -508,19 +602,18 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
           }
           uint64_t lowest_kept = ~0ull;
           if (state == kFound) {  // a token is kept if what is ahead of it is below the limit
-            for (int i = tid; i < listed; i += kNT) {
+            for (int i = warp; i < listed; i += kNW) {
               const uint64_t key = sh.key[i];
-              uint64_t ahead = above;
-              for (int j = 0; j < listed; ++j) ahead += sh.key[j] > key ? sh.weight[j] : 0;
-              if (ahead < limit) lowest_kept = min(lowest_kept, key);
+              uint64_t ahead = 0;
+              for (int j = lane; j < listed; j += 32) ahead += sh.key[j] > key ? sh.weight[j] : 0;
+              if (above + warp_sum(ahead) < limit) lowest_kept = min(lowest_kept, key);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) lowest_kept = min(lowest_kept, __shfl_xor_sync(kFull, lowest_kept, o));
           }
           __syncthreads();
           if (lane == 0) s_least[warp] = lowest_kept;
           __syncthreads();
           if (tid < C) {
+#pragma unroll
             for (int w = 0; w < kNW; ++w) lowest_kept = min(lowest_kept, s_least[w]);
             Shared* to_sh = cl.map_shared_rank(&sh, tid);
             to_sh->state = state;
@@ -537,7 +630,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         limit = sh.all[0];
         first_sums = false;
         if (sh.state == kFound) {
-          summed = by_weight && bins.shift < 0 ? bin : -1;
+          summed = by_weight && bins.shift < 0 && bin < kFine ? bin : -1;
           return sh.border;
         }
         if (sh.state == kDivide) {
@@ -575,11 +668,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
     each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
       const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float k = fmaf(exponent_of(v[q], s), (float)kPerOctave, kWhole);
-        if (min(__float_as_int(k) - kWholeBits, kBins - 1) == summed && edge.reached(v[q], i + q - lead))
-          mine += weight_of(v[q], s, table);
-      }
+      for (int q = 0; q < 4; ++q)
+        if (nearest_64th(exponent_of(v[q], s)) == summed && edge.reached(v[q], i + q - lead)) mine += weight_of(v[q], s, table);
     });
   } else if (from == 0 && s.whole != kFar) {
     each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int, float4 v4) {
@@ -598,10 +688,9 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   __syncthreads();  // (s_sum may still be read)
   if (lane == 0) s_sum[warp] = mine;
   __syncthreads();
-  if (warp == 0 && lane < C) {
-    uint64_t sum = 0;
-    for (int w = 0; w < kNW; ++w) sum += s_sum[w];
-    cl.map_shared_rank(&sh, lane)->in[c] = sum;
+  if (warp == 0) {
+    const uint64_t sum = warp_sum(lane < kNW ? s_sum[lane] : 0);
+    if (lane < C) cl.map_shared_rank(&sh, lane)->in[c] = sum;
   }
   cl.sync();  // the last use of another CTA's memory
   uint64_t all = 0, before = 0;
@@ -611,45 +700,48 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   }
   // the lowest id up to which the sum passes this
   const uint64_t target = u >= 1.f ? all - 1 : share_down(u, all);
-  for (int w = 0; w < warp; ++w) before += s_sum[w];
-  if (target < before || target >= before + s_sum[warp]) return;
-  // this warp's run holds it: 32 vectors at a time
-  for (int i = i0 + 4 * v0; i < i0 + 4 * v1; i += 128) {
-    const int at = i + 4 * lane;
+  if (target < before || target >= before + sh.in[c]) return;
+  // The run of the warp that holds it, a vector per thread.
+  int holder = 0;
+  for (; holder < kNW - 1 && target >= before + s_sum[holder]; ++holder) before += s_sum[holder];
+  const int h0 = min(vectors, holder * per_warp), h1 = min(vectors, h0 + per_warp);
+  __syncthreads();  // s_sum is written anew
+  for (int base = h0; base < h1; base += kNT) {  // (once: a run is shorter than the CTA has threads, but for long rows)
+    const int at = i0 + 4 * (base + tid);
     float4 v4 = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (at < i0 + 4 * v1) v4 = in_shared ? *reinterpret_cast<const float4*>(s_row + (at - i0)) : vector_at(at);
-    const uint64_t own = kept_sum(at, v4);
-    uint64_t upto = own;
+    if (base + tid < h1) v4 = in_shared ? *reinterpret_cast<const float4*>(s_row + (at - i0)) : vector_at(at);
+    const uint64_t here = kept_sum(at, v4);
+    uint64_t upto = here;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t x = __shfl_up_sync(kFull, upto, o);
       if (lane >= o) upto += x;
     }
-    const uint64_t round = __shfl_sync(kFull, upto, 31);
-    if (target >= before + round) {
-      before += round;
-      continue;
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    uint64_t start = before + upto - here;
+    for (int w = 0; w < kNW; ++w) {
+      if (w < warp) start += s_sum[w];
+      before += s_sum[w];
     }
-    before += upto - own;
-    if (target >= before && target < before + own) {
-      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+    __syncthreads();
+    if (target < start || target >= start + here) continue;
+    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (!edge.reached(v[q], at + q - lead)) continue;
-        const uint64_t w = weight_of(v[q], s, table);
-        if (target < before + w) {
-          a.ids[m] = at + q - lead;
-          if (a.logprob) {
-            const double lw = s.whole != kFar ? (double)v[q] * s_inv - s.whole * 0.6931471805599453
-                                              : ((double)v[q] - (double)top) * s_inv;
-            a.logprob[m] = w == all ? 0.f : (float)(lw - log((double)all * 0x1p-44));
-          }
-          break;
+    for (int q = 0; q < 4; ++q) {
+      if (!edge.reached(v[q], at + q - lead)) continue;
+      const uint64_t w = weight_of(v[q], s, table);
+      if (target < start + w) {
+        a.ids[m] = at + q - lead;
+        if (a.logprob) {
+          const double lw = s.whole != kFar ? (double)v[q] * s_inv - s.whole * 0.6931471805599453
+                                            : ((double)v[q] - (double)top) * s_inv;
+          a.logprob[m] = w == all ? 0.f : (float)(lw - log((double)all * 0x1p-44));
         }
-        before += w;
+        break;
       }
+      start += w;
     }
-    break;
   }
 }
 
@@ -657,12 +749,12 @@ template <int NT, int PER_SM>
 cudaError_t launch(const SampleArgs& a, int c, int per, cudaStream_t st) {
   auto kernel = sample_kernel<NT, PER_SM>;
   const int in_shared = per <= kMostShared;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared * 4);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kMostShared + kOctaves * NT) * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.M * c);
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = in_shared ? (size_t)per * 4 : 0;
+  cfg.dynamicSmemBytes = ((in_shared ? (size_t)per : 0) + kOctaves * NT) * 4;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

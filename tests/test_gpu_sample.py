@@ -41,7 +41,7 @@ def run(dev, x, u, T=None, k=None, p=None, q=None, pad=0, lead=0, logprob=True, 
     return ids[:M].cpu().numpy(), lp[:M].cpu().numpy()
 
 
-def check(dev, x, u, T=1.0, k=0, p=1.0, q=0.0, **kw):
+def check(dev, x, u, T=1.0, k=0, p=1.0, q=0.0, sharp=True, **kw):
     x = np.asarray(x, np.float32)
     M = len(x)
     ids, lp = run(dev, x, u, T, k, p, q, **kw)
@@ -56,7 +56,7 @@ def check(dev, x, u, T=1.0, k=0, p=1.0, q=0.0, **kw):
         # the sum's error (2^-28), one rounding to fp32
         near = lambda y: abs(float(lp[m]) - y) <= 2.0 ** -24 * abs(y) + 2.0 ** -24
         assert not kw.get("logprob", True) or any(np.isnan(lp[m]) if np.isnan(y) else near(y) for y in refs), (m, lp[m], refs)
-    assert sure >= 0.95 * M - 1                                        # the borders are the exception
+    assert sure >= 0.95 * M - 1 or not sharp                           # the borders are the exception
     return ids, lp
 
 
@@ -169,6 +169,20 @@ def test_sample_u_outside(dev):
 @pytest.mark.parametrize("T", [2.0 ** -140, 2.0 ** -100, 1e-6, 1e-3, 50.0, 1e9, 3e38])
 def test_sample_temperatures(dev, T):
     check(dev, normal(6, 7001, 11, 20.0), us(6, 11), T=T, p=[1.0, 1.0, 0.7, 0.7, 0.1, 0.999])
+
+
+@pytest.mark.parametrize("V", [3001, 120011])
+def test_sample_borders_among_light_tokens(dev, V):
+    """One token ahead of all others, far enough that the borders of top-p and top-k lie among weights of 2^-20 to 2^-40,
+    spread, nearly alike, and alike."""
+    rng = np.random.default_rng(V)
+    x = np.stack([-rng.uniform(11, 28, V), -rng.uniform(14.0, 14.02, V), np.full(V, -15.5), -rng.uniform(10, 30, V)]).astype(np.float32)
+    x[:, V // 3] = 0.0
+    rest = np.exp(x.astype(np.float64)).sum(1) - 1
+    for share in (0.1, 0.5, 0.93):
+        check(dev, x, us(4, V), p=(1 + share * rest) / (1 + rest), sharp=False)  # a weight is as small as the slack
+    check(dev, x, [1 - 2.0 ** -24] * 4, p=(1 + 0.7 * rest) / (1 + rest), sharp=False)
+    check(dev, x, [1 - 2.0 ** -24] * 4, k=[V // 2, V // 2, 1000, V - 1], p=[1.0, 1.0, 1.0, 0.9999999], sharp=False)
 
 
 def test_sample_far_logits(dev):
