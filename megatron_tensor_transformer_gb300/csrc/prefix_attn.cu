@@ -84,7 +84,7 @@ __device__ __forceinline__ Tiles tiles_of(const GroupedAttnArgs& a, int g) {
 
 // Chunks [c0, c1) of rows [r0, r0 + rows) of (group, kv head gg); pieces as for paged attention.  g < 0: no more.
 struct __align__(16) Tile {
-  int g, m0, gg, r0, rows, c0, c1, len, a, b, second, pad;
+  int g, m0, gg, r0, rows, c0, c1, len, whole, second, pad[2];
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
@@ -136,18 +136,20 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Waits as in paged_attn.cuh, without a call: registers are dealt out anew by setmaxnreg, and a call's convention knows
-// nothing of it.
+// Waits as in paged_attn.cu: after one that runs out (it sets the error word) the producer issues no more copies, the
+// issuing thread no more MMAs, and both wait for what is in flight; the softmax warps go on without waiting.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
+  const bool ok = tc::mbar_wait(bar, parity);
+  if (!ok) atomicExch(err, code);
+  return !ok;
+}
 struct Waits {
   unsigned* err;
   unsigned code;
   bool failed;
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    if (!failed && !tc::mbar_wait(bar, parity)) {
-      atomicExch(err, code);
-      failed = true;
-    }
+    if (tc::mbar_try_wait(bar, parity) || tc::mbar_try_wait(bar, parity)) return true;
+    if (!failed) failed = wait_long(bar, parity, err, code);
     return !failed;
   }
 };
@@ -281,13 +283,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
   // first block, or even chunks of a tile of one; 1 the odd chunks of those; 2 the second block.
   auto wide = [](const Tile& it) { return C::T == 2 && it.rows > 128; };
 
-  // The softmax threads hold a row of S: registers go from the other warps to them, where the launch's even share is
-  // too few.  (In sum at most what the block was launched with.)
-  constexpr int kSoftRegs = C::T == 2 ? (FP8 ? 168 : 200) : 0, kRestRegs = FP8 ? 88 : 96;
-  static_assert(128 * C::T * kSoftRegs + (C::kThreads - 128 * C::T) * kRestRegs <= 65536 / C::kThreads / 8 * 8 * C::kThreads,
-                "more registers than the launch has");
   if (warp < kSoftWarps) {
-    if constexpr (kSoftRegs > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---- softmax: thread = row
     Waits wait{a.err, 58u, false};
     const int x = warp >> 2, row = tid & 127;
@@ -317,7 +313,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
       uint8_t* dst = sQ + x * C::QBLOCK + row * 128;
       float pow = 1.f;
       if (!FP8) {
-#pragma unroll
+#pragma unroll 4
         for (int c8 = 0; c8 < HD / 8; ++c8)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                            tc::smem_u32(dst + (c8 >> 3) * 16384 + (((c8 & 7) ^ (row & 7)) << 4))),
@@ -368,29 +364,31 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
         tc::tc_fence_after();
         const uint32_t sA = S_at(region) + lanes;
         const uint32_t groups = loaded[(kc + i) % kMasks];
-        float s[128];
+        // The row is read twice, 64 positions at a time in loops: a row in registers takes no fewer cycles, and code
+        // that is long costs where a CTA runs it once or twice (20 cycles an instruction until it is in the cache).
+        float top = flip ? INFINITY : -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          float s[64];
+          tmem_ld32(sA + c, s);
+          tmem_ld32(sA + c + 32, s + 32);
+          landed(s);
+          if (groups != 0xffu) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld32(sA + c, s + c);
-        landed(s);
-        if (groups != 0xffu) {
-          const float out = flip ? INFINITY : -INFINITY;
+            for (int q = 0; q < 64; ++q) s[q] = groups >> (c / 16 + q / 16) & 1 ? s[q] : flip ? INFINITY : -INFINITY;
+          }
+          if (!flip) {
+            float t4[4] = {top, s[61], s[62], s[63]};
 #pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = groups >> (c / 16) & 1 ? s[c] : out;
-        }
-        float top;
-        if (!flip) {
-          float t4[4] = {s[0], s[1], s[2], s[3]};
+            for (int q = 0; q < 60; q += 8) {
 #pragma unroll
-          for (int c = 4; c < 124; c += 8)
+              for (int r = 0; r < 4; ++r) t4[r] = fmaxf(t4[r], q + 4 + r < 61 ? fmaxf(s[q + r], s[q + 4 + r]) : s[q + r]);
+            }
+            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) t4[q] = fmaxf(t4[q], fmaxf(s[c + q], s[c + 4 + q]));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) t4[q] = fmaxf(t4[q], s[124 + q]);
-          top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        } else {
-          top = s[0];
-#pragma unroll
-          for (int c = 1; c < 128; ++c) top = fminf(top, s[c]);
+            for (int q = 0; q < 64; ++q) top = fminf(top, s[q]);
+          }
         }
         top = __fmul_rn(top, sc);
         const bool raise = top > sub + (C::kStep + C::kPLog);
@@ -419,29 +417,40 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
         // s sc - sub, rounded once: what sub's own rounding adds is the same for all of the row's weights under it, and
         // divides out.  Beyond 2^20 it could be large: there the product is rounded by itself.
         const bool far = !(fabsf(sub) < 1048576.f), any_far = __any_sync(kFull, far);
-        if (any_far) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = far ? __fmul_rn(s[c], sc) - sub : fmaf(s[c], sc, -sub);
-        } else {
-          const float2 sc2 = make_float2(sc, sc), sub2 = make_float2(-sub, -sub);
-#pragma unroll
-          for (int c = 0; c < 128; c += 2) {
-            const float2 y = fma2(make_float2(s[c], s[c + 1]), sc2, sub2);
-            s[c] = y.x;
-            s[c + 1] = y.y;
-          }
-        }
+        const float2 sc2 = make_float2(sc, sc), sub2 = make_float2(-sub, -sub);
         float2 l2[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          float s[64];
+          tmem_ld32(sA + c, s);
+          tmem_ld32(sA + c + 32, s + 32);
+          landed(s);
+          if (any_far) {
 #pragma unroll
-        for (int part = 0; part < 4; ++part) {
-          uint32_t p[16];
+            for (int q = 0; q < 64; ++q) s[q] = far ? __fmul_rn(s[q], sc) - sub : fmaf(s[q], sc, -sub);
+          } else {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const float2 y = make_float2(ex2(s[32 * part + 2 * q]), ex2(s[32 * part + 2 * q + 1]));
-            l2[q & 1] = add2(l2[q & 1], y);
-            p[q] = pack16<FP8>(y.x, y.y);
+            for (int q = 0; q < 64; q += 2) {
+              const float2 y = fma2(make_float2(s[q], s[q + 1]), sc2, sub2);
+              s[q] = y.x;
+              s[q + 1] = y.y;
+            }
           }
-          tmem_st16(sA + 16 * part, p);  // over S, which is in registers
+          if (groups != 0xffu) {
+#pragma unroll
+            for (int q = 0; q < 64; ++q) s[q] = groups >> (c / 16 + q / 16) & 1 ? s[q] : -INFINITY;
+          }
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint32_t p[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float2 y = make_float2(ex2(s[32 * part + 2 * q]), ex2(s[32 * part + 2 * q + 1]));
+              l2[q & 1] = add2(l2[q & 1], y);
+              p[q] = pack16<FP8>(y.x, y.y);
+            }
+            tmem_st16(sA + c / 2 + 16 * part, p);  // over columns that have been read
+          }
         }
         l = (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
         tc::tmem_st_wait();
@@ -462,8 +471,8 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
       tc::tc_fence_after();
       const float vs = FP8 && a.v_scale ? a.v_scale[it.gg] : 1.0f;
       const int r = x * 128 + row, RT = a.M * G, R = it.m0 * G + it.r0 + r;
-      const bool whole = it.a == it.b, there = r < it.rows;
-      float* piece = pa.pieces + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == it.a ? it.second : 0)) * pa.piece;
+      const bool whole = it.whole, there = r < it.rows;
+      float* piece = pa.pieces + (size_t)(2 * blockIdx.x + it.second) * pa.piece;
       float4* dst = whole ? pa.whole + (size_t)it.gg * (HD / 4) * RT + R : reinterpret_cast<float4*>(piece) + r;
       const size_t step = whole ? RT : pa.rows;
       if (live) {
@@ -490,7 +499,6 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
       it = next;
     }
   } else {
-    if constexpr (kSoftRegs > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
     if (warp == kProducer) {
       // ---- k and v in the order in which the MMAs take them: a stage is SUB-th of a chunk's k or v
       Waits wait{a.err, 54u, false};
@@ -576,7 +584,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
         }
       }
       const int last = cnt - 1 - lane;  // copies in flight: each stage's last
-      if (lane < C::NT && last >= 0) if (!tc::mbar_wait(B(tfull[last % C::NT]), (last / C::NT) & 1)) atomicExch(a.err, 54u);
+      if (lane < C::NT && last >= 0) wait_long(B(tfull[last % C::NT]), (last / C::NT) & 1, a.err, 54u);
     } else if (warp == kMma) {
       // ---- one thread issues all MMAs; they run in the order of issue, so a region of S is written anew behind the
       // product that read P from it
@@ -591,15 +599,18 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
           ++cnt;
           return there;
         };
-        // The thread has 64 cycles for an MMA: descriptors are a base and constants (addresses do not carry out of
-        // their field).  Loops that computed them took 140.
+        // The thread has 64 cycles for an MMA: descriptors are a base and steps (addresses do not carry out of their
+        // field).  Loops that made each anew took 140.
         auto scores = [&](int x, int region, int st, int sub) {
-          const uint64_t q0 = smem_desc(qA + x * C::QBLOCK, 16, 1024, 2), k0 = smem_desc(rA + st * C::STAGE, 16, 1024, 2);
+          uint64_t q0 = smem_desc(qA + x * C::QBLOCK, 16, 1024, 2), k0 = smem_desc(rA + st * C::STAGE, 16, 1024, 2);
           const uint32_t d = S_at(region) + sub * C::KS;
+#pragma unroll 1
+          for (int i = 0; i < HD / 64; ++i) {  // 64 dims: rows of 128 bytes
 #pragma unroll
-          for (int i = 0; i < HD / 16; ++i)  // 64 dims: rows of 128 bytes
-            tc::mma_bf16(d, q0 + tc::desc_off(i / 4 * 16384 + i % 4 * 32), k0 + tc::desc_off(i / 4 * (C::KS * 128) + i % 4 * 32),
-                         idS, i > 0);
+            for (int k = 0; k < 4; ++k) tc::mma_bf16(d, q0 + tc::desc_off(32 * k), k0 + tc::desc_off(32 * k), idS, i + k > 0);
+            q0 += tc::desc_off(16384);
+            k0 += tc::desc_off(C::KS * 128);
+          }
         };
         auto scores_end = [&](int b) {
           tc::mma_commit(B(s_full[b]));
@@ -610,10 +621,14 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
           const uint64_t v0 = smem_desc(rA + st * C::STAGE, C::KS * 128, 1024, 2);
           const uint32_t p = S_at(region) + 8 * sub * (C::KS / 16), d = O_at(x);
           if (groups == 0xffu) {
+#pragma unroll 1
+            for (int i = 0; i < C::KS / 16; i += 4) {
 #pragma unroll
-            for (int i = 0; i < C::KS / 16; ++i)
-              tc::mma_bf16_tmem_a(d, p + 8 * i, v0 + tc::desc_off(i * 2048), idO, i > 0 || live);
-            live = true;
+              for (int k = i; k < i + 4; ++k) {
+                tc::mma_bf16_tmem_a(d, p + 8 * k, v0 + tc::desc_off(2048) * k, idO, live);
+                live = true;
+              }
+            }
             return;
           }
 #pragma unroll 1
@@ -693,7 +708,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
         }
     mma_end:
         tc::mma_commit(B(mma_done));  // the MMAs in flight
-        if (!tc::mbar_wait(B(mma_done), 0)) atomicExch(a.err, 55u);
+        wait_long(B(mma_done), 0, a.err, 55u);
       }
       __syncwarp();
     } else if (warp == kItems) {
@@ -721,10 +736,10 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
           const int cost = tile < ts.full ? (C::T == 2 ? C::kWide : C::kNarrow) : ts.cost_rest;
           const long long units = ch == 0 ? 0 : C::kEnds + cost * (long long)ch;
           if (ch > 0) {
-            // chunk i begins at unit at + kEnds + cost i
+            // chunk i begins at unit at + kEnds + cost i, and is of the CTA that has this unit
             auto chunks_before = [&](long long u) {
               const long long d = u - at - C::kEnds;
-              return d <= 0 ? 0 : (int)min((long long)ch, quot(d + cost - 1, cost));
+              return d <= 0 ? 0 : d >= cost * (long long)ch ? ch : (int)quot(d + cost - 1, cost);
             };
             it.c0 = chunks_before(u0);
             it.c1 = chunks_before(u1);
@@ -736,11 +751,9 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
             it.r0 = tile * C::ROWS;
             it.rows = tile < ts.full ? C::ROWS : ts.rest;
             it.len = ts.len;
-            const bool split = it.c0 > 0 || it.c1 < ch;
-            it.a = split ? owner(U, nct, at + C::kEnds) : 0;
-            it.b = split ? owner(U, nct, at + C::kEnds + cost * (long long)(ch - 1)) : 0;
-            // whether it is the second item of CTA a, whose run then begins before it
-            it.second = split && split_at(U, nct, it.a) < at;
+            it.whole = it.c0 == 0 && it.c1 == ch;
+            // a piece is the CTA's second where it begins the tile, and the CTA's run begins before
+            it.second = it.c0 == 0 && u0 < at;
           }
           at += units;
           if (++tile >= ntiles || ch == 0) {
@@ -813,8 +826,20 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
   }
 }
 
+// a / b as a call: a division's code is long, and where a block runs once its instructions cost most (20 cycles each
+// until they are in the cache)
+__device__ __noinline__ long long quot_call(long long a, long long b) { return quot(a, b); }
+// The CTAs that hold units u .. v of U in nct shares, and whether the first one's share begins before `at`.
+struct Holders {
+  int a, b, second;
+};
+__device__ __forceinline__ Holders holders(long long U, int nct, long long at, long long u, long long v) {
+  const int a = (int)quot_call((u + 1) * nct + U - 1, U) - 1, b = (int)quot_call((v + 1) * nct + U - 1, U) - 1;
+  return {a, b, quot_call(U * a, nct) < at};
+}
+
 // The parts of a row in order: the pieces of what its group shares, then of its own positions.  One block per (request,
-// kv head), a float4 of a head's dims per thread; kBatch pieces are read at once.
+// kv head), a float4 of a head's dims per thread; kBatch parts are read at once.
 template <int HD, bool FP8>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixArgs pa) {
   using C = XCfg<HD, FP8>;
@@ -833,93 +858,89 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   if (g >= 0) {
     ts = tiles_of<C>(a, g);
     m0 = a.cu_groups[g];
-    base = pa.plan[2 + g];
+    base = pa.plan[2 + g] + gg * ts.per_head;
   }
-  // its own run: CTAs oa .. ob
   const int ch = s.c1 - s.c0;
-  int oa = 0, ob = -1, own_second = 0;
+  Holders own{0, -1, 0};
   if (ch > 0) {
     const long long at = own0 + (long long)gg * (kTailEnds + ch);
-    oa = owner(V, own_nct, at + kTailEnds);
-    ob = owner(V, own_nct, at + kTailEnds + ch - 1);
-    own_second = split_at(V, own_nct, oa) < at;
+    own = holders(V, own_nct, at, at + kTailEnds, at + kTailEnds + ch - 1);
   }
+  const int n_own = own.b - own.a + 1;
+  int tile_was = -1;
+  Holders shared{0, -1, 0};
   for (int e = threadIdx.x; e < G * (HD / 4); e += blockDim.x) {
     const int h = e % G, c4 = e / G;
     const size_t row = (size_t)m * a.n_q + (size_t)gg * G + h;
-    float ref = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    // n parts: at(i, ref, sum, v) says where the i-th is
-    auto add = [&](int n, auto at) {
-      for (int b = 0; b < n; b += kBatch) {
-        float r[kBatch], l[kBatch];
-        float4 v[kBatch];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const float *pr, *pl;
-          const float4* pv;
-          at(min(b + q, n - 1), pr, pl, pv);
-          r[q] = __ldcg(pr);
-          l[q] = __ldcg(pl);
-          v[q] = __ldcg(pv);
-        }
-        float mx = ref;
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          if (b + q >= n || l[q] == 0.f) r[q] = -INFINITY;  // nothing attended to: the rest may hold anything
-          mx = fmaxf(mx, r[q]);
-        }
-        const float f = weight(ref, mx);
-        sum *= f;
-        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          if (r[q] == -INFINITY) continue;
-          const float w = ex2(r[q] - mx);
-          sum += l[q] * w;
-          o.x += v[q].x * w;
-          o.y += v[q].y * w;
-          o.z += v[q].z * w;
-          o.w += v[q].w * w;
-        }
-        ref = mx;
-      }
-    };
+    int r = 0;
     if (g >= 0) {
-      const int R = (m - m0) * G + h, tile = R / C::ROWS, r = R % C::ROWS;
-      const int cost_full = C::T == 2 ? C::kWide : C::kNarrow, cost = tile < ts.full ? cost_full : ts.cost_rest;
-      const long long at = base + gg * ts.per_head + tile * (C::kEnds + cost_full * (long long)ts.chunks);
-      const int ca = owner(U, nct, at + C::kEnds), cb = owner(U, nct, at + C::kEnds + cost * (long long)(ts.chunks - 1));
-      if (ca == cb) {
-        const size_t w = (size_t)m * G + h;
-        add(1, [&](int, const float*& pr, const float*& pl, const float4*& pv) {
-          pr = pa.whole_ref + (size_t)gg * RT + w;
-          pl = pa.whole_l + (size_t)gg * RT + w;
-          pv = pa.whole + ((size_t)gg * (HD / 4) + c4) * RT + w;
-        });
-      } else {
-        const int second = split_at(U, nct, ca) < at;
-        add(cb - ca + 1, [&](int i, const float*& pr, const float*& pl, const float4*& pv) {
-          const float* p = pa.pieces + (size_t)(2 * (ca + i) + (i == 0 ? second : 0)) * pa.piece;
-          pr = p + (size_t)pa.rows * HD + r;
-          pl = p + (size_t)pa.rows * (HD + 1) + r;
-          pv = reinterpret_cast<const float4*>(p) + (size_t)c4 * pa.rows + r;
-        });
+      const int R = (m - m0) * G + h, tile = R / C::ROWS;
+      r = R % C::ROWS;
+      if (tile != tile_was) {
+        const int cost_full = C::T == 2 ? C::kWide : C::kNarrow, cost = tile < ts.full ? cost_full : ts.cost_rest;
+        const long long at = base + tile * (C::kEnds + cost_full * (long long)ts.chunks);
+        shared = holders(U, nct, at, at + C::kEnds, at + C::kEnds + cost * (long long)(ts.chunks - 1));
+        tile_was = tile;
       }
     }
-    if (oa == ob) {
-      add(1, [&](int, const float*& pr, const float*& pl, const float4*& pv) {
-        pr = a.part_ref + row;
-        pl = a.part_l + row;
-        pv = reinterpret_cast<const float4*>(a.part_o + row * HD) + c4;
-      });
-    } else {
-      add(ob - oa + 1, [&](int i, const float*& pr, const float*& pl, const float4*& pv) {
-        const float* p = a.own_pieces + (size_t)(2 * (oa + i) + (i == 0 ? own_second : 0)) * a.own_piece;
-        pr = p + G * HD + h;
-        pl = p + G * HD + G + h;
-        pv = reinterpret_cast<const float4*>(p + h * HD) + c4;
-      });
+    const int n_shared = shared.b - shared.a + 1, n = n_shared + n_own;
+    float ref = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = 0; b < n; b += kBatch) {
+      float pr[kBatch], pl[kBatch];
+      float4 pv[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int i = min(b + q, n - 1);
+        const float *refs, *sums;
+        const float4* at;
+        if (i < n_shared) {
+          const float* p = pa.pieces + (size_t)(2 * (shared.a + i) + (i == 0 ? shared.second : 0)) * pa.piece;
+          refs = p + (size_t)pa.rows * HD + r;
+          sums = refs + pa.rows;
+          at = reinterpret_cast<const float4*>(p) + (size_t)c4 * pa.rows + r;
+          if (n_shared == 1) {
+            const size_t w = (size_t)m * G + h;
+            refs = pa.whole_ref + (size_t)gg * RT + w;
+            sums = pa.whole_l + (size_t)gg * RT + w;
+            at = pa.whole + ((size_t)gg * (HD / 4) + c4) * RT + w;
+          }
+        } else {
+          const int k = i - n_shared;
+          const float* p = a.own_pieces + (size_t)(2 * (own.a + k) + (k == 0 ? own.second : 0)) * a.own_piece;
+          refs = p + G * HD + h;
+          sums = refs + G;
+          at = reinterpret_cast<const float4*>(p + h * HD) + c4;
+          if (n_own == 1) {
+            refs = a.part_ref + row;
+            sums = a.part_l + row;
+            at = reinterpret_cast<const float4*>(a.part_o + row * HD) + c4;
+          }
+        }
+        pr[q] = __ldcg(refs);
+        pl[q] = __ldcg(sums);
+        pv[q] = __ldcg(at);
+      }
+      float mx = ref;
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        if (b + q >= n || pl[q] == 0.f) pr[q] = -INFINITY;  // nothing attended to: the rest may hold anything
+        mx = fmaxf(mx, pr[q]);
+      }
+      const float f = weight(ref, mx);
+      sum *= f;
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        if (pr[q] == -INFINITY) continue;
+        const float w = ex2(pr[q] - mx);
+        sum += pl[q] * w;
+        o.x += pv[q].x * w;
+        o.y += pv[q].y * w;
+        o.z += pv[q].z * w;
+        o.w += pv[q].w * w;
+      }
+      ref = mx;
     }
     const float f = sum == 0.f ? 0.f : 1.0f / sum;
     *reinterpret_cast<uint2*>(a.o + row * HD + 4 * c4) = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));

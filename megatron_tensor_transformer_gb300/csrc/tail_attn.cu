@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, TCfg<HD, FP8>::kPerSm)
         if (cur.m >= 0) {
           d.flags = (cur.first ? kFirst : 0) | (run & 1 ? kQ : 0);
           if (cur.c + 1 == cur.c1) {
-            const long long f0 = cur.at + kTailEnds;
-            const int ca = owner(U, nct, f0);
-            d.flags |= kLast | (ca == owner(U, nct, f0 + cur.ch - 1) ? kWhole : 0) |
-                       ((int)blockIdx.x == ca && split_at(U, nct, ca) < cur.at ? kSecond : 0);
+            // the run's first stage is this CTA's, and its last one: all of it; a piece is the CTA's second where it
+            // begins the run, and the CTA's list begins before
+            const bool begins = u0 <= cur.at + kTailEnds, ends = u1 >= cur.at + kTailEnds + cur.ch;
+            d.flags |= kLast | (begins && ends ? kWhole : 0) | (begins && u0 < cur.at ? kSecond : 0);
           }
         }
         s_desc[st] = d;
