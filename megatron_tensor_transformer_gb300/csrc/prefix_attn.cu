@@ -136,6 +136,30 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// MMAs and what follows them, from a converged warp: one lane, always the same, issues.  (From code that only this lane runs,
+// operands are not uniform to the compiler, and moving them took 100 cycles an MMA.)
+__device__ __forceinline__ void warp_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(kFull, v, 0); }
+
 // Waits as in paged_attn.cu: after one that runs out (it sets the error word) the producer issues no more copies, the
 // issuing thread no more MMAs, and both wait for what is in flight; the softmax warps go on without waiting.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
@@ -586,12 +610,16 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
       const int last = cnt - 1 - lane;  // copies in flight: each stage's last
       if (lane < C::NT && last >= 0) wait_long(B(tfull[last % C::NT]), (last / C::NT) & 1, a.err, 54u);
     } else if (warp == kMma) {
-      // ---- one thread issues all MMAs; they run in the order of issue, so a region of S is written anew behind the
+      // ---- one warp issues all MMAs; they run in the order of issue, so a region of S is written anew behind the
       // product that read P from it
-      if (lane == 0) {
-        Waits wait{a.err, 55u, false};
+      {
+        Waits wait_lane{a.err, 55u, false};
+        auto wait = [&](uint32_t bar, uint32_t parity) { return !__any_sync(kFull, !wait_lane(bar, parity)); };
+        const uint32_t tmem_u = uniform(tmem);
+        auto S_at = [&](int r) { return tmem_u + 128 * r; };
+        auto O_at = [&](int x) { return tmem_u + 256 + HD * x; };
         constexpr uint32_t idS = idesc16<FP8>(128, C::KS), idO = idesc16<FP8>(128, HD) | kBTransposed;
-        const uint32_t qA = tc::smem_u32(sQ), rA = tc::smem_u32(ring);
+        const uint32_t qA = uniform(tc::smem_u32(sQ)), rA = uniform(tc::smem_u32(ring));
         int cnt = 0, kc = 0, uses[3] = {0, 0, 0}, done[2] = {0, 0};  // stages, chunks, S by barrier, blocks' items
         auto take = [&](int& st) {
           st = cnt % C::NS;
@@ -607,14 +635,14 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < HD / 64; ++i) {  // 64 dims: rows of 128 bytes
 #pragma unroll
-            for (int k = 0; k < 4; ++k) tc::mma_bf16(d, q0 + tc::desc_off(32 * k), k0 + tc::desc_off(32 * k), idS, i + k > 0);
+            for (int k = 0; k < 4; ++k) warp_mma(d, q0 + tc::desc_off(32 * k), k0 + tc::desc_off(32 * k), idS, i + k > 0);
             q0 += tc::desc_off(16384);
             k0 += tc::desc_off(C::KS * 128);
           }
         };
         auto scores_end = [&](int b) {
-          tc::mma_commit(B(s_full[b]));
-          tc::mbar_arrive(B(s_full[b]));  // releases what this thread has seen: the chunk's mask, q's powers
+          warp_commit(B(s_full[b]));
+          if (lane == 0) tc::mbar_arrive(B(s_full[b]));  // releases what this thread has seen: the chunk's mask, q's powers
           b == 0 ? ++uses[0] : b == 1 ? ++uses[1] : ++uses[2];
         };
         auto values = [&](int x, int region, int st, int sub, uint32_t groups, bool& live) {
@@ -625,7 +653,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
             for (int i = 0; i < C::KS / 16; i += 4) {
 #pragma unroll
               for (int k = i; k < i + 4; ++k) {
-                tc::mma_bf16_tmem_a(d, p + 8 * k, v0 + tc::desc_off(2048) * k, idO, live);
+                warp_mma_tmem_a(d, p + 8 * k, v0 + tc::desc_off(2048) * k, idO, live);
                 live = true;
               }
             }
@@ -634,19 +662,20 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < C::KS / 16; ++i) {
             if (!(groups >> (sub * (C::KS / 16) + i) & 1)) continue;  // what was not loaded may hold anything
-            tc::mma_bf16_tmem_a(d, p + 8 * i, v0 + tc::desc_off(i * 2048), idO, live);
+            warp_mma_tmem_a(d, p + 8 * i, v0 + tc::desc_off(i * 2048), idO, live);
             live = true;
           }
         };
         for (int j = 0;; ++j) {
-          const Tile it = next_item(wait, j, false);
-          if (it.g < 0) break;
+          const Tile it = next_item(wait_lane, j, true);
+          if (__any_sync(kFull, it.g < 0)) break;
           if (!wait(B(q_full[0]), done[0] & 1)) break;
-          if (wide(it) && !wait(B(q_full[1]), done[1] & 1)) break;
-          const int n = it.c1 - it.c0;
+          const int n = (int)uniform(it.c1 - it.c0);
+          const bool two = uniform(wide(it)) != 0;
+          if (two && !wait(B(q_full[1]), done[1] & 1)) break;
           bool live[2] = {false, false};
           int st, sv;
-          if (wide(it)) {
+          if (two) {
             if (!take(st)) goto mma_end;
             tc::tc_fence_after();
 #pragma unroll
@@ -654,24 +683,24 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
               scores(x, x, st, 0);
               scores_end(2 * x);
             }
-            tc::mma_commit(B(empty[st]));
+            warp_commit(B(empty[st]));
             for (int i = 0; i < n; ++i) {
               if (!take(sv)) goto mma_end;
-              const uint32_t groups = loaded[(kc + i) % kMasks];
+              const uint32_t groups = uniform(loaded[(kc + i) % kMasks]);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 if (!wait(B(p_full[2 * x]), (uses[2 * x] - 1) & 1)) goto mma_end;
                 tc::tc_fence_after();
                 values(x, x, sv, 0, groups, live[x]);
-                if (x == 1) tc::mma_commit(B(empty[sv]));
+                if (x == 1) warp_commit(B(empty[sv]));
                 if (i + 1 < n) {
                   if (x == 0 && !take(st)) goto mma_end;
                   tc::tc_fence_after();
                   scores(x, x, st, 0);
                   scores_end(2 * x);
-                  if (x == 1) tc::mma_commit(B(empty[st]));
+                  if (x == 1) warp_commit(B(empty[st]));
                 } else {
-                  tc::mma_commit(B(o_full[x]));
+                  warp_commit(B(o_full[x]));
                   ++done[x];
                 }
               }
@@ -682,7 +711,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
                 if (!take(st)) return false;
                 tc::tc_fence_after();
                 scores(0, i & 1, st, sub);
-                tc::mma_commit(B(empty[st]));
+                warp_commit(B(empty[st]));
               }
               scores_end(i & 1);
               return true;
@@ -692,23 +721,23 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
               const int p_use = (i & 1 ? uses[1] : uses[0]) - 1;
               if (i + 1 < n && !next_scores(i + 1)) goto mma_end;
               if (!wait(B(p_full[i & 1]), p_use & 1)) goto mma_end;
-              const uint32_t groups = loaded[(kc + i) % kMasks];
+              const uint32_t groups = uniform(loaded[(kc + i) % kMasks]);
               for (int sub = 0; sub < C::SUB; ++sub) {
                 if (!take(sv)) goto mma_end;
                 tc::tc_fence_after();
                 values(0, i & 1, sv, sub, groups, live[0]);
-                tc::mma_commit(B(empty[sv]));
+                warp_commit(B(empty[sv]));
               }
-              tc::mma_commit(B(pv_done));
+              warp_commit(B(pv_done));
             }
-            tc::mma_commit(B(o_full[0]));
+            warp_commit(B(o_full[0]));
             ++done[0];
           }
           kc += n;
         }
     mma_end:
-        tc::mma_commit(B(mma_done));  // the MMAs in flight
-        wait_long(B(mma_done), 0, a.err, 55u);
+        warp_commit(B(mma_done));  // the MMAs in flight
+        if (lane == 0) wait_long(B(mma_done), 0, a.err, 55u);
       }
       __syncwarp();
     } else if (warp == kItems) {
