@@ -855,64 +855,63 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
   }
 }
 
-// a / b as a call: a division's code is long, and where a block runs once its instructions cost most (20 cycles each
-// until they are in the cache)
-__device__ __noinline__ long long quot_call(long long a, long long b) { return quot(a, b); }
-// The CTAs that hold units u .. v of U in nct shares, and whether the first one's share begins before `at`.
-struct Holders {
-  int a, b, second;
-};
-__device__ __forceinline__ Holders holders(long long U, int nct, long long at, long long u, long long v) {
-  const int a = (int)quot_call((u + 1) * nct + U - 1, U) - 1, b = (int)quot_call((v + 1) * nct + U - 1, U) - 1;
-  return {a, b, quot_call(U * a, nct) < at};
-}
-
 // The parts of a row in order: the pieces of what its group shares, then of its own positions.  One block per (request,
 // kv head), a float4 of a head's dims per thread; kBatch parts are read at once.
 template <int HD, bool FP8>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixArgs pa) {
   using C = XCfg<HD, FP8>;
   constexpr int SP = C::OWN, kBatch = 4;
-  tc::griddep_wait();
-  tc::griddep_launch_dependents();
+  // What the call was given may be read before the kernels ahead have ended (the first of them waited for all work
+  // before); what they leave, only after.
   const GroupedAttnArgs& a = pa.a;
   const int m = blockIdx.x / a.n_kv, gg = blockIdx.x % a.n_kv, G = a.n_q / a.n_kv, RT = a.M * G;
-  const long long U = pa.plan[0], V = a.own_plan[0], own0 = a.own_plan[2 + m];
-  const int nct = (int)pa.plan[1], own_nct = (int)a.own_plan[1];
-  const Span s = own_span<SP>(a, m, U > 0);
-  int g = U > 0 ? group_of(a, m) : -1, m0 = 0;
+  const bool ok = __syncthreads_and(groups_in_order(a, threadIdx.x, blockDim.x));
+  const Span s = own_span<SP>(a, m, ok);
+  int g = ok ? group_of(a, m) : -1, m0 = 0;
   if (g >= 0 && (s.n < 1 || (long long)s.n > ((long long)a.max_pages << a.page_shift) || left_to_group(a, g, s.n) == 0)) g = -1;
   Tiles ts{};
-  long long base = 0;
   if (g >= 0) {
     ts = tiles_of<C>(a, g);
     m0 = a.cu_groups[g];
-    base = pa.plan[2 + g] + gg * ts.per_head;
   }
-  const int ch = s.c1 - s.c0;
-  Holders own{0, -1, 0};
-  if (ch > 0) {
-    const long long at = own0 + (long long)gg * (kTailEnds + ch);
-    own = holders(V, own_nct, at, at + kTailEnds, at + kTailEnds + ch - 1);
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  // Which CTAs have parts: of the request's own run, and of the one or two tiles that its rows lie in.  Divisions of 64
+  // bits are long, so one warp makes them, a lane each.
+  __shared__ int s_cta[3][2], s_second[3];
+  const int R0 = (m - m0) * G, tile0 = R0 / C::ROWS;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, what = lane >> 1, tile = tile0 + what - 1;
+    long long U = 0, at = 0, u = -1;  // units and CTAs of its list, its first unit, the unit asked for
+    int nct = 1;
+    if (what == 0) {
+      const int ch = s.c1 - s.c0;
+      U = a.own_plan[0];
+      nct = (int)a.own_plan[1];
+      at = a.own_plan[2 + m] + (long long)gg * (kTailEnds + ch);
+      if (ch > 0) u = at + kTailEnds + (lane & 1) * (ch - 1);
+    } else if (what < 3 && g >= 0 && tile < ts.full + (ts.rest > 0)) {
+      const int cost_full = C::T == 2 ? C::kWide : C::kNarrow, cost = tile < ts.full ? cost_full : ts.cost_rest;
+      U = pa.plan[0];
+      nct = (int)pa.plan[1];
+      at = pa.plan[2 + g] + gg * ts.per_head + tile * (C::kEnds + cost_full * (long long)ts.chunks);
+      u = at + C::kEnds + (lane & 1) * (cost * (long long)(ts.chunks - 1));
+    }
+    const int cta = u >= 0 ? owner(U, nct, u) : -(lane & 1);  // none: 0 .. -1
+    const bool second = u >= 0 && split_at(U, nct, cta) < at;
+    if (lane < 6) {
+      s_cta[what][lane & 1] = cta;
+      if (!(lane & 1)) s_second[what] = second;
+    }
   }
-  const int n_own = own.b - own.a + 1;
-  int tile_was = -1;
-  Holders shared{0, -1, 0};
+  __syncthreads();
+  const int own_a = s_cta[0][0], n_own = s_cta[0][1] - own_a + 1, own_second = s_second[0];
   for (int e = threadIdx.x; e < G * (HD / 4); e += blockDim.x) {
     const int h = e % G, c4 = e / G;
     const size_t row = (size_t)m * a.n_q + (size_t)gg * G + h;
-    int r = 0;
-    if (g >= 0) {
-      const int R = (m - m0) * G + h, tile = R / C::ROWS;
-      r = R % C::ROWS;
-      if (tile != tile_was) {
-        const int cost_full = C::T == 2 ? C::kWide : C::kNarrow, cost = tile < ts.full ? cost_full : ts.cost_rest;
-        const long long at = base + tile * (C::kEnds + cost_full * (long long)ts.chunks);
-        shared = holders(U, nct, at, at + C::kEnds, at + C::kEnds + cost * (long long)(ts.chunks - 1));
-        tile_was = tile;
-      }
-    }
-    const int n_shared = shared.b - shared.a + 1, n = n_shared + n_own;
+    const int R = R0 + h, r = R % C::ROWS, t = 1 + R / C::ROWS - tile0;
+    const int shared_a = g >= 0 ? s_cta[t][0] : 0, n_shared = g >= 0 ? s_cta[t][1] - shared_a + 1 : 0, n = n_shared + n_own;
+    const int shared_second = s_second[t];
     float ref = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int b = 0; b < n; b += kBatch) {
@@ -924,7 +923,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
         const float *refs, *sums;
         const float4* at;
         if (i < n_shared) {
-          const float* p = pa.pieces + (size_t)(2 * (shared.a + i) + (i == 0 ? shared.second : 0)) * pa.piece;
+          const float* p = pa.pieces + (size_t)(2 * (shared_a + i) + (i == 0 ? shared_second : 0)) * pa.piece;
           refs = p + (size_t)pa.rows * HD + r;
           sums = refs + pa.rows;
           at = reinterpret_cast<const float4*>(p) + (size_t)c4 * pa.rows + r;
@@ -936,7 +935,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
           }
         } else {
           const int k = i - n_shared;
-          const float* p = a.own_pieces + (size_t)(2 * (own.a + k) + (k == 0 ? own.second : 0)) * a.own_piece;
+          const float* p = a.own_pieces + (size_t)(2 * (own_a + k) + (k == 0 ? own_second : 0)) * a.own_piece;
           refs = p + G * HD + h;
           sums = refs + G;
           at = reinterpret_cast<const float4*>(p + h * HD) + c4;

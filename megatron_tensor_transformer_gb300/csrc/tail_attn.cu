@@ -275,10 +275,21 @@ __global__ void __launch_bounds__(kThreads, TCfg<HD, FP8>::kPerSm)
         failed = true;
       }
       if (__any_sync(kFull, failed)) break;
-      if (cur.m >= 0 && cur.first) store_q(run & 1);
       const bool load = id >= 0 && id < a.n_pages;
       const unsigned boxes = __ballot_sync(kFull, load);
       const unsigned in = __ballot_sync(kFull, lane < C::SP / 16 && (boxes >> ((lane * 16 / box_rows) & 31) & 1));
+      if (lane == 0) tc::mbar_expect_tx(B(full[st]), 2 * __popc(boxes) * box_rows * C::INB);
+      __syncwarp();
+      if (load) {
+        const int p = cur.c * C::SP + box * box_rows;
+        const int row = ((((cur.gg / nkvs) * a.n_pages + id) * nkvs + cur.gg % nkvs) << a.page_shift) +
+                        (p & ((1 << a.page_shift) - 1));
+        const uint32_t dst = tc::smem_u32(smem + st * C::STAGE) + (side * C::SP + box * box_rows) * C::INB;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+          tc::tma_load_2d_hint(dst + kv * C::SIDE, kv ? &tmV : &tmK, side * (C::INB / (FP8 ? 1 : 2)), row, B(full[st]), pol);
+      }
+      if (cur.m >= 0 && cur.first) store_q(run & 1);  // beside the copies
       __syncwarp();
       if (lane == 0) {
         Desc d{cur.m, cur.gg, cur.c * C::SP, cur.lo, cur.n, 0, in, 0};
@@ -292,21 +303,11 @@ __global__ void __launch_bounds__(kThreads, TCfg<HD, FP8>::kPerSm)
           }
         }
         s_desc[st] = d;
-        tc::mbar_arrive_expect_tx(B(full[st]), 2 * __popc(boxes) * box_rows * C::INB);
+        tc::mbar_arrive(B(full[st]));
       }
       if (cur.m < 0) {
         ++s;
         break;
-      }
-      __syncwarp();
-      if (load) {
-        const int p = cur.c * C::SP + box * box_rows;
-        const int row = ((((cur.gg / nkvs) * a.n_pages + id) * nkvs + cur.gg % nkvs) << a.page_shift) +
-                        (p & ((1 << a.page_shift) - 1));
-        const uint32_t dst = tc::smem_u32(smem + st * C::STAGE) + (side * C::SP + box * box_rows) * C::INB;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-          tc::tma_load_2d_hint(dst + kv * C::SIDE, kv ? &tmV : &tmK, side * (C::INB / (FP8 ? 1 : 2)), row, B(full[st]), pol);
       }
       cur = nxt;
       id = id_next;
