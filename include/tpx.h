@@ -475,10 +475,12 @@ tp_status tp_paged_attn_decode(const tp_shape* shape /* host */, const tp_pages*
  * cu_groups [n_groups + 1] and prefix_lens [n_groups]: int32 on the device; 0 <= cu_groups[0] <= cu_groups[1] <= .. <= M
  * (a group may be empty; a group that breaks this, or whose prefix is negative or longer than a row of the table,
  * counts as having no prefix).  n_groups is at most M; 0: as tp_paged_attn_decode (the two may then be NULL).
- * Scores, softmax statistics and sums are fp32.  The shared positions' weights enter the product rounded to bf16 over
- * bf16 pages (2^-8 of a weight, the tensor cores' operand type) and to fp16 over e4m3 pages (2^-11 of a weight and
- * 2^-32 of the largest; q is there fp16 after a power of two per head, exact down to 2^-24 of the head's largest |q|),
- * and the parts' sums are joined in fp32.
+ * Where the table's M rows can name no more than 96 MB of cache (M max_pages page_size positions), sharing is not looked
+ * at: that takes less time.
+ * Scores, softmax statistics and sums are fp32.  With sharing the weights enter the product rounded once, to bf16 over
+ * bf16 pages (2^-8 of a weight, the tensor cores' operand type) and to fp16 over e4m3 pages (2^-11 of a weight and 2^-32
+ * of the largest; q is there fp16 after a power of two per head, exact down to 2^-24 of the head's largest |q|), and the
+ * parts' sums are joined in fp32.
  * ws: tp_prefix_attn_workspace_bytes(shape, M) bytes, zero-filled once before first use (and after a
  * TP_ERR_DEVICE_TIMEOUT), left reusable by every call whose size it covers, tp_paged_attn_decode's included; calls that
  * share it must not overlap on the GPU (replays of two captured graphs included).  Up to three kernel launches; runs

@@ -52,7 +52,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int kv_dtype, int hd, cons
                               cudaStream_t st);
 
 // Requests that share prefixes.  What a request attends to is split between its group and itself; the parts are sum p v,
-// their reference and sum p (0: nothing attended to, and the other two may hold anything).
+// their reference and sum p (0: nothing counted, and the other two may hold anything).
 struct GroupedAttnArgs : PagedAttnArgs {
   const int32_t *cu_groups, *prefix_lens;
   int32_t n_groups;

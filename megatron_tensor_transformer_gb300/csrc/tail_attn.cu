@@ -3,7 +3,7 @@
 //
 // Per (request, kv head), up to 16 q heads as the rows of mma.sync products, over stages of 32 to 128 positions.  It is
 // HBM-bound, and with short runs bound by the chain of a run's beginning and end: page look-up, copies, products, sums.  So
-// three small CTAs share an SM, whose chains overlap, in place of one with many roles.  A CTA takes an even share of all
+// two or three small CTAs share an SM, whose chains overlap, in place of one with many roles.  A CTA takes an even share of all
 // stages: one warp walks them, looks up pages, issues the TMA copies and brings the q of each run, four compute.
 //
 // Both products permute their summed index, so that a thread's operands lie side by side: for the scores a thread
@@ -154,11 +154,8 @@ __global__ void __launch_bounds__(kThreads, TCfg<HD, FP8>::kPerSm)
     }
     long long at = base;
     for (int m = r0; m < r1; ++m) {
-      const Span s = span(m);
       a.own_plan[2 + m] = at;
-      at += (long long)units(s) * a.n_kv;
-      if (s.c0 == s.c1)  // no positions of its own
-        for (int i = 0; i < a.n_q; ++i) a.part_l[(size_t)m * a.n_q + i] = 0.f;
+      at += (long long)units(span(m)) * a.n_kv;
     }
   }
   if (u0 < u1 && u0 >= base && u0 < base + here) {  // this thread's requests hold unit u0

@@ -427,6 +427,8 @@ def tp_prefix_attn_decode(shape, pages, q, k_pages, v_pages, block_table, lens, 
                           lse=None, scale=0.0, window=0, k_scale=None, v_scale=None, stream=None):
     """As tp_paged_attn_decode, with the requests cu_groups[g] .. cu_groups[g + 1] - 1 sharing their first
     prefix_lens[g] positions' whole pages; cu_groups [n + 1], prefix_lens [n]: int32 on the device."""
+    if cu_groups.shape[0] != prefix_lens.shape[0] + 1:
+        raise TpxError(TP_ERR_INVALID_ARG, "tp_prefix_attn_decode: cu_groups and prefix_lens")
     _check(lib().tp_prefix_attn_decode(ctypes.byref(shape), ctypes.byref(pages), _ptr(q), _ptr(k_pages), _ptr(v_pages),
                                        _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(lens), q.shape[0],
                                        _ptr(cu_groups), _ptr(prefix_lens), prefix_lens.shape[0], scale, window,

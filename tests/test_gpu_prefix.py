@@ -15,12 +15,19 @@ from tests.test_gpu_parity import bits
 pytestmark = pytest.mark.gpu
 
 
+SMALL = 96 << 20  # bytes of cache that a table can name, up to which sharing is not looked at
+
+
 class Shared(Case):
     """groups: (requests, prefix) one after another; lens of all requests; rows of a group name the same pages first."""
 
     def __init__(self, dev, t, n_q, n_kv, hd, page, groups, lens, kv=tpx.TP_BF16, seed=0, poison=True, std=1.0, stride_pad=0,
-                 room=0):
+                 small=False):
         super().__init__(dev, t, n_q, n_kv, hd, page, lens, kv, seed, poison=False, std=std, stride_pad=stride_pad)
+        # Where all that M rows of the table can hold is little, the call attends to each request by itself: such a table,
+        # or one with room for more.
+        held = len(lens) * n_kv * hd * 2 * (2 if kv == tpx.TP_BF16 else 1) * page
+        room = 0 if small else max(0, SMALL // held + 1 - self.max_pages)
         self.max_pages += room
         if room:
             self.table = np.concatenate([self.table, np.full((len(lens), room), 2 ** 31 - 1, np.int64)], 1)
@@ -117,6 +124,20 @@ BOTH = [tpx.TP_BF16, tpx.TP_FP8_E4M3]
 def test_prefix_attention_groups(dev, kv, t, n_q, n_kv, hd, page):
     groups = [(3, 300), (1, 200), (2, 16), (5, 128), (2, 1), (2, 0), (4, 513), (2, page), (3, 2 * page - 1)]
     Shared(dev, t, n_q, n_kv, hd, page, groups, tails(groups, page + hd), kv, seed=page + hd, stride_pad=page // 16).check()
+
+
+@pytest.mark.parametrize("kv", BOTH)
+@pytest.mark.parametrize("t,n_q,n_kv,hd,page", [(1, 8, 4, 64, 16), (2, 16, 4, 128, 32), (1, 5, 1, 256, 64)])
+def test_prefix_attention_small_tables(dev, kv, t, n_q, n_kv, hd, page):
+    """Tables that hold little: each request by itself, the bits of tp_paged_attn_decode."""
+    groups = [(3, 300), (1, 200), (5, 128)]
+    c = Shared(dev, t, n_q, n_kv, hd, page, groups, tails(groups, hd), kv, seed=hd, small=True)
+    o, lse = c.check()
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    pages = tpx.make_pages(page, c.n_pages, c.max_pages, kv, c.table.shape[1])
+    tpx.tp_paged_attn_decode(c.sh, pages, c.q, c.k, c.v, c.table_d, c.lens_d, o2, c.ws, lse=lse2, k_scale=c.ks, v_scale=c.vs)
+    sync()
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("kv", BOTH)
@@ -394,8 +415,9 @@ def test_prefix_attention_past_4_gib(dev):
     n_kv, hd, page, n_pages = 8, 128, 256, 10400
     sh = tpx.make_shape(1024, n_q=16, n_kv=n_kv, hd=hd)
     k, v = (torch.empty((1, n_pages, n_kv, page, hd), dtype=torch.bfloat16, device=dev) for _ in range(2))
-    pages = tpx.make_pages(page, n_pages, 4)
-    small = tpx.make_pages(page, 5, 4)
+    room = SMALL // (2 * n_kv * hd * 4 * page) + 4
+    pages = tpx.make_pages(page, n_pages, 4 + room)
+    small = tpx.make_pages(page, 5, 4 + room)
     at = [n_pages - 1, n_pages - 3, 17, n_pages - 2, 9000]
     ks, vs = (torch.empty((1, 5, n_kv, page, hd), dtype=torch.bfloat16, device=dev) for _ in range(2))
     for j, p in enumerate(at):
@@ -406,7 +428,7 @@ def test_prefix_attention_past_4_gib(dev):
     ws = tpx.new_prefix_attn_workspace(sh, 2, dev)
     lens, cu, prefix = i32([1000, 900], dev), i32([0, 2], dev), i32([600], dev)
     for pg, kk, vv, table, out in ((pages, k, v, [at[:4], at[:2] + at[3:]], o), (small, ks, vs, [[0, 1, 2, 3], [0, 1, 3, 4]], o2)):
-        tpx.tp_prefix_attn_decode(sh, pg, q, kk, vv, i32(table, dev), lens, cu, prefix, out, ws)
+        tpx.tp_prefix_attn_decode(sh, pg, q, kk, vv, i32(np.pad(table, ((0, 0), (0, room))), dev), lens, cu, prefix, out, ws)
     sync()
     assert torch.isfinite(o.float()).all() and torch.equal(o.view(torch.int16), o2.view(torch.int16))
 
@@ -417,7 +439,8 @@ def test_samples_to_one_prompt(dev, kv):
     written for each), and step by step: tables, QKV, append, attention, o_proj, logits, sampled tokens, their log
     probabilities, the next embeddings; captured once and replayed, nothing read by the host in between.  The steps' attention
     agrees with paged attention by itself, and the samples differ."""
-    d, n_q, n_kv, hd, t, page, V, n, P, steps = 512, 8, 4, 64, 2, 16, 1024, 6, 20, 12
+    d, n_q, n_kv, hd, t, page, V, n, steps = 512, 8, 4, 64, 2, 16, 1024, 6, 12
+    P = SMALL // (n * n_kv * hd * 2 * page) + 20                       # pages that a row of the table can name
     sh = tpx.make_shape(d, n_q=n_q, n_kv=n_kv, hd=hd, t=t, vocab=V)
     rnd = lambda *s, std=1.0, seed=0: inputs.normal_bf16(s, std, seed, 60, dev)
     wq, dq = tpx.tp_partition_weights(sh, tpx.TP_W_QKV, rnd(d, (n_q + 2 * n_kv) * hd, std=0.05, seed=1))

@@ -57,6 +57,15 @@ def test_prefix_attention_workspace_sizes():
     assert tpx.tp_prefix_attn_workspace_bytes(SH, -1) == 0
 
 
+def test_prefix_attention_binding_refusals():
+    """Group bounds that are not one more than the prefixes, which the C call cannot see."""
+    x, n = torch.zeros((4, 1024), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    for cu, prefix in ((n[:2], n[:2]), (n[:3], n[:1]), (n[:1], n[:3])):
+        with pytest.raises(tpx.TpxError) as e:
+            tpx.tp_prefix_attn_decode(SH, PG, x, x, x, n, n, cu, prefix, x, x)
+        assert e.value.status == tpx.TP_ERR_INVALID_ARG
+
+
 def test_sample_refusals():
     E = tpx.TP_ERR_INVALID_ARG
     for kw in (dict(M=-1), dict(V=0), dict(ldl=99), dict(logits=None), dict(u=None), dict(ids=None)):
