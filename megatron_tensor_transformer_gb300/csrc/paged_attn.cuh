@@ -103,6 +103,9 @@ __device__ __forceinline__ Span own_span(const GroupedAttnArgs& a, int m, bool g
 __device__ __forceinline__ long long quot(long long x, long long y) {  // x / y, both >= 0: a 64-bit division only if it must be
   return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
 }
+// The same as a call, for code that a CTA runs once: there an instruction takes some 20 cycles until it is in the cache,
+// and a division's are many.
+__device__ __noinline__ long long quot_call(long long x, long long y) { return quot(x, y); }
 __device__ __forceinline__ long long split_at(long long U, int nct, int i) { return quot(U * i, nct); }
 __device__ __forceinline__ int owner(long long U, int nct, long long u) {
   return (int)quot((u + 1) * nct + U - 1, U) - 1;

@@ -67,7 +67,7 @@ struct Tiles {
   long long per_head;  // units
 };
 template <class C>
-__device__ __forceinline__ Tiles tiles_of(const GroupedAttnArgs& a, int g) {
+__device__ __noinline__ Tiles tiles_of(const GroupedAttnArgs& a, int g) {
   Tiles t{};
   const int size = a.cu_groups[g + 1] - a.cu_groups[g];
   t.len = shared_len(a, size, a.prefix_lens[g]);
@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
     U += s_part[w];
   }
   const int nct = (int)min((long long)gridDim.x, U / C::kWide);
-  const long long u0 = nct == 0 ? 0 : split_at(U, nct, min((int)blockIdx.x, nct)),
-                  u1 = nct == 0 ? 0 : split_at(U, nct, min((int)blockIdx.x + 1, nct));
+  const long long u0 = nct == 0 ? 0 : quot_call(U * min((int)blockIdx.x, nct), nct),
+                  u1 = nct == 0 ? 0 : quot_call(U * min((int)blockIdx.x + 1, nct), nct);
   if (blockIdx.x == 0) {  // for the join
     if (tid == 0) {
       pa.plan[0] = U;
@@ -748,11 +748,11 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
       Tiles ts{};
       if (u0 < u1) {  // the tile that holds u0
         ts = tiles_of<C>(a, g);
-        gg = (int)quot(u0 - at, ts.per_head);
+        gg = (int)quot_call(u0 - at, ts.per_head);
         at += (long long)gg * ts.per_head;
         if (ts.full) {
           const long long one = C::kEnds + (C::T == 2 ? C::kWide : C::kNarrow) * (long long)ts.chunks;
-          tile = (int)min((long long)ts.full, quot(u0 - at, one));
+          tile = (int)min((long long)ts.full, quot_call(u0 - at, one));
           at += tile * one;
         }
       }
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
             // chunk i begins at unit at + kEnds + cost i, and is of the CTA that has this unit
             auto chunks_before = [&](long long u) {
               const long long d = u - at - C::kEnds;
-              return d <= 0 ? 0 : d >= cost * (long long)ch ? ch : (int)quot(d + cost - 1, cost);
+              return d <= 0 ? 0 : d >= cost * (long long)ch ? ch : (int)quot_call(d + cost - 1, cost);
             };
             it.c0 = chunks_before(u0);
             it.c1 = chunks_before(u1);

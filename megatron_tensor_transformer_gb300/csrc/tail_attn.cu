@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kThreads, TCfg<HD, FP8>::kPerSm)
     U += s_part[w];
   }
   const int nct = (int)min((long long)gridDim.x, U);
-  const long long u0 = nct == 0 ? 0 : split_at(U, nct, min((int)blockIdx.x, nct)),
-                  u1 = nct == 0 ? 0 : split_at(U, nct, min((int)blockIdx.x + 1, nct));
+  const long long u0 = nct == 0 ? 0 : quot_call(U * min((int)blockIdx.x, nct), nct),
+                  u1 = nct == 0 ? 0 : quot_call(U * min((int)blockIdx.x + 1, nct), nct);
   if (blockIdx.x == 0) {  // for the join
     if (tid == 0) {
       a.own_plan[0] = U;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, TCfg<HD, FP8>::kPerSm)
       wm = s_m;
       ws = span(wm);
       const int n = units(ws);
-      wg = (int)quot(u0 - s_base, n);
+      wg = (int)quot_call(u0 - s_base, n);
       wat = s_base + (long long)wg * n;
     }
     Step last{};
