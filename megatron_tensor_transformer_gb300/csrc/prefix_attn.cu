@@ -329,45 +329,44 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
         kc += it.c1 - it.c0;
       }
     };
-    // q's row to shared memory: nothing reads the block's q any more once its last S is there.  Returns 2^e by which
-    // the row was divided.
+    // The warp's 32 rows of q to shared memory, neighbouring lanes along a row (a row per thread took 2 us more): nothing
+    // reads the block's q any more once its last S is there.  Returns 2^e by which the thread's row was divided.
     auto bring_q = [&](const Tile& it) {
+      constexpr int RP = HD / 8, kRows = 32 / RP;  // 16-byte pieces of a row, rows at once
       const int r = x * 128 + row, R = it.r0 + min(r, it.rows - 1), m = R / G;
-      const __nv_bfloat16* src = a.q + ((size_t)(it.m0 + m) * a.n_q + (size_t)it.gg * G + (R - m * G)) * HD;
-      uint8_t* dst = sQ + x * C::QBLOCK + row * 128;
+      const int at = (it.m0 + m) * a.n_q + it.gg * G + (R - m * G);  // the thread's row of q
+      const int c8 = lane % RP, sub = lane / RP;
       float pow = 1.f;
-      if (!FP8) {
-#pragma unroll 4
-        for (int c8 = 0; c8 < HD / 8; ++c8)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                           tc::smem_u32(dst + (c8 >> 3) * 16384 + (((c8 & 7) ^ (row & 7)) << 4))),
-                       "l"(src + 8 * c8), "r"(r < it.rows ? 16 : 0)
+#pragma unroll 2
+      for (int i = 0; i < 32; i += kRows) {
+        const int l = i + sub, rr = (row & ~31) + l;  // the lane whose row it is, in the block
+        const bool there = x * 128 + rr < it.rows;
+        const __nv_bfloat16* src = a.q + (size_t)__shfl_sync(kFull, at, l) * HD + 8 * c8;
+        uint8_t* dst = sQ + x * C::QBLOCK + (c8 >> 3) * 16384 + rr * 128 + (((c8 & 7) ^ (rr & 7)) << 4);
+        if (!FP8) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
                        : "memory");
-        asm volatile("cp.async.wait_all;" ::: "memory");
-      } else {  // q / 2^e below 2^15, as fp16
-        uint32_t top = 0;
-#pragma unroll 4
-        for (int c8 = 0; c8 < HD / 8; ++c8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * c8);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) top = max(top, max((w[q] >> 7) & 0xffu, (w[q] >> 23) & 0xffu));
+          continue;
         }
+        // q / 2^e below 2^15, as fp16
+        const uint4 v = there ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t top = 0, h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) top = max(top, max((w[q] >> 7) & 0xffu, (w[q] >> 23) & 0xffu));
+#pragma unroll
+        for (int o = 1; o < RP; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
         // exponent field of the largest value, less 14 for 2^14 <= q / 2^e < 2^15; both factors stay normal
         const int e = min(max((int)top, 15), 254) - 14;
         // an infinity makes the row NaN, as its scores would
         const float inv = top == 255u ? NAN : __uint_as_float((uint32_t)(254 - e) << 23);
-        pow = __uint_as_float((uint32_t)e << 23);
-#pragma unroll 4
-        for (int c8 = 0; c8 < HD / 8; ++c8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * c8);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) h[q] = pack16<true>(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
-          *reinterpret_cast<uint4*>(dst + (c8 >> 3) * 16384 + (((c8 & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
+        for (int q = 0; q < 4; ++q) h[q] = pack16<true>(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+        const int mine = __shfl_sync(kFull, e, lane % kRows * RP);
+        if (lane / kRows * kRows == i) pow = __uint_as_float((uint32_t)mine << 23);
       }
+      if (!FP8) asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(B(q_full[x]));
