@@ -149,6 +149,11 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
+// Four logits by number, without an array.
+struct Four {
+  float4 v;
+  __device__ __forceinline__ float operator[](int q) const { return q & 2 ? (q & 1 ? v.w : v.z) : (q & 1 ? v.y : v.x); }
+};
 // 2^64 p for p in [0, 1), rounded down (exact from 2^-40 on)
 __device__ __forceinline__ uint64_t frac64(float p) {
   const uint32_t b = __float_as_uint(p);
@@ -177,21 +182,17 @@ struct Bins {
   uint64_t low, high;  // keys [low, high] are divided, the others have no bin
   int shift;           // < 0: by the weight
 };
-// The bin, by the weight, of an exponent below kLightest: the nearest 64th up to 15 octaves, then half octaves.  Monotone.
-constexpr int kPerOctave = 64, kOctaves = 16, kFine = (kOctaves - 1) * kPerOctave;
+// The bin, by the weight, of an exponent below kLightest: the nearest 64th.
+constexpr int kPerOctave = 64, kOctaves = 16;            // octaves that are summed at a time, the last with all that follow
+constexpr int kLast = (int)kLightest;                    // the last octave with a bin
 __device__ __forceinline__ int nearest_64th(float p) {  // large for a large exponent and an infinite one
   return __float_as_int(fmaf(p, (float)kPerOctave, kWhole)) - kWholeBits;
 }
-__device__ __forceinline__ int weight_bin(float p) {
-  const int b = nearest_64th(p);
-  return b < kFine ? b : kFine + ((b - kFine) >> 5);
-}
-static_assert(kFine + ((46 - 15) * kPerOctave >> 5) < kOctaves * kPerOctave, "kLightest has a bin");
 // What the first CTA tells the others, and what it is told.
 struct Shared {
   float top[kMaxC];
   uint32_t hist[kBins], fine[2][kMaxC][kPerOctave];  // of the search for top-k's border, and for top-p's: no CTA may still
-  float octave[2][kMaxC][kOctaves];                  // be reading what another one writes
+  float octave[2][kMaxC][kOctaves];                  // be reading what another one writes; these, two sums in turn
   uint64_t key[kList], weight[kList];
   int listed;                    // tokens of the bin, of which the first kList are listed
   uint64_t above[kMaxC], in[kMaxC], all[kMaxC], least[kMaxC], most[kMaxC];  // of each CTA
@@ -205,6 +206,9 @@ enum { kFound, kAgain, kDivide };  // the border is known; it lies in another bi
 template <int kNT, int kPerSm>
 __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a, int per_cta, int in_shared) {
   constexpr int kNW = kNT / 32;
+  // Steps of a loop over four logits laid out side by side.  CTAs of few rows run each pass once, and the time that their
+  // code takes to come (some 20 cycles an instruction) is most of it.
+  constexpr int kFour = kNT == 1024 ? 1 : 4;
   static_assert(kBins % kNT == 0, "bins per thread");
   extern __shared__ __align__(16) float s_row[];
   __shared__ Shared sh;
@@ -300,6 +304,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   const int v0 = min(vectors, warp * per_warp), v1 = min(vectors, v0 + per_warp);
   int summed = -1;  // >= 0: s_above holds the warps' exact sums of all tokens kept so far above that bin, by the weight
 
+  int turn = 0;
   // Of the keys from `from` on: the lowest before which fewer than k of them lie (share < 0), or before which less than
   // `share` of their sum does.
   auto lowest = [&](uint64_t from, int k, float share) {
@@ -313,11 +318,10 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         return key >= bins.low && key <= bins.high ? (int)((bins.high - key) >> bins.shift) : -1;
       }
       const float p = exponent_of(x, s);
-      return p < kLightest && low.reached(x, place - lead) ? weight_bin(p) : -1;
+      return p < kLightest && low.reached(x, place - lead) ? nearest_64th(p) : -1;
     };
     auto bin_exponent = [&](int b) {  // by key: of a bin's highest key
-      if (bins.shift < 0)
-        return b < kFine ? (float)b * (1.f / kPerOctave) : (float)(kFine / kPerOctave) + 0.5f * (float)(b - kFine);
+      if (bins.shift < 0) return (float)b * (1.f / kPerOctave);
       return exponent_of(logit_of((uint32_t)((bins.high - ((uint64_t)b << bins.shift)) >> 32)), s);
     };
     const bool plain = from == 0;  // the usual case, in fewer steps
@@ -325,39 +329,6 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
     // took 26 cycles a warp), then its bins.  Every CTA comes to the same conclusion from the same numbers.
     {
       float* mine = s_row + own + tid;
-#pragma unroll
-      for (int o = 0; o < kOctaves; ++o) mine[o * kNT] = 0.f;
-      if (plain) {
-        each(i0 + 4 * tid, i1, 4 * kNT, [&](int, float4 v4) {
-          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float p = exponent_of(v[q], s);
-            const int o = min(nearest_64th(p) >> 6, kOctaves - 1);
-            mine[o * kNT] += by_weight ? ex2(-p) : p < kLightest ? 1.f : 0.f;
-          }
-        });
-      } else {
-      each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
-        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float p = exponent_of(v[q], s);
-          if (!(p < kLightest) || (from != 0 && !low.reached(v[q], i + q - lead))) continue;
-          mine[(weight_bin(p) / kPerOctave) * kNT] += by_weight ? ex2(-p) : 1.f;
-        }
-      });
-      }
-      __syncthreads();
-      for (int o = warp; o < kOctaves; o += kNW) {
-        float sum = 0.f;
-        for (int t = lane; t < kNT; t += 32) sum += s_row[own + o * kNT + t];
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
-        if (lane < C) cl.map_shared_rank(&sh, lane)->octave[by_weight][c][o] = sum;
-      }
-      if (tid < kPerOctave) fine[tid] = 0;
-      cl.sync();
       auto find = [&](float v, float goal, float& before) {  // the lane whose part of the sum holds goal, and what is before
         float upto = v;
 #pragma unroll
@@ -370,19 +341,66 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         before = __shfl_sync(kFull, upto - v, l);
         return l;
       };
-      float part = 0.f, before, before2;
-      if (lane < kOctaves)
-        for (int r = 0; r < C; ++r) part += sh.octave[by_weight][r][lane];
-      float all = part;
+      float goal = 0.f, before;
+      int octave;
+#pragma unroll 1
+      for (int begin = 0;; begin += kOctaves - 1) {  // nearly always one or two times
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) all += __shfl_xor_sync(kFull, all, x);
-      if (!by_weight && all < (float)k) return from;  // fewer than k tokens have a weight: all are kept
-      const float goal = by_weight ? all * share : (float)k;
-      const int octave = find(part, goal, before);
-      if (plain && octave < kOctaves - 1) {
+        for (int o = 0; o < kOctaves; ++o) mine[o * kNT] = 0.f;
+        if (plain) {
+          each(i0 + 4 * tid, i1, 4 * kNT, [&](int, float4 v4) {
+            const Four v{v4};
+#pragma unroll kFour
+            for (int q = 0; q < 4; ++q) {
+              const float p = exponent_of(v[q], s);
+              const int o = min((nearest_64th(p) >> 6) - begin, kOctaves - 1);
+              if (o >= 0) mine[o * kNT] += by_weight ? ex2(-p) : p < kLightest ? 1.f : 0.f;
+            }
+          });
+        } else {
+          each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+            const Four v{v4};
+#pragma unroll kFour
+            for (int q = 0; q < 4; ++q) {
+              const float p = exponent_of(v[q], s);
+              if (!(p < kLightest) || !low.reached(v[q], i + q - lead)) continue;
+              const int o = min((nearest_64th(p) >> 6) - begin, kOctaves - 1);
+              if (o >= 0) mine[o * kNT] += by_weight ? ex2(-p) : 1.f;
+            }
+          });
+        }
+        __syncthreads();
+        turn ^= 1;
+        for (int o = warp; o < kOctaves; o += kNW) {
+          float sum = 0.f;
+          for (int t = lane; t < kNT; t += 32) sum += s_row[own + o * kNT + t];
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
+          if (lane < C) cl.map_shared_rank(&sh, lane)->octave[turn][c][o] = sum;
+        }
+        if (tid < kPerOctave) fine[tid] = 0;
+        cl.sync();
+        float part = 0.f;
+        if (lane < kOctaves)
+          for (int r = 0; r < C; ++r) part += sh.octave[turn][r][lane];
+        if (begin == 0) {
+          float all = part;
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) all += __shfl_xor_sync(kFull, all, x);
+          if (!by_weight && all < (float)k) return from;  // fewer than k tokens have a weight: all are kept
+          goal = by_weight ? all * share : (float)k;
+        }
+        octave = find(part, goal, before);
+        goal -= before;
+        if (octave < kOctaves - 1 || begin + kOctaves - 1 > kLast) {
+          octave = min(begin + octave, kLast);
+          break;
+        }
+      }
+      if (plain) {
         each(i0 + 4 * tid, i1, 4 * kNT, [&](int, float4 v4) {
-          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+          const Four v{v4};
+#pragma unroll kFour
           for (int q = 0; q < 4; ++q) {
             const float p = exponent_of(v[q], s), near = fmaf(p, (float)kPerOctave, kWhole);
             const unsigned b = (unsigned)(__float_as_int(near) - (kWholeBits + octave * kPerOctave));
@@ -394,13 +412,13 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         });
       } else {
       each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
-        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+        const Four v{v4};
+#pragma unroll kFour
         for (int q = 0; q < 4; ++q) {
           const float p = exponent_of(v[q], s);
           if (!(p < kLightest)) continue;
-          const int b = weight_bin(p);
-          if (b / kPerOctave != octave || (from != 0 && !low.reached(v[q], i + q - lead))) continue;
+          const int b = nearest_64th(p);
+          if (b / kPerOctave != octave || !low.reached(v[q], i + q - lead)) continue;
           const uint32_t n = by_weight ? __float2uint_rn(ex2(bin_exponent(b) - p) * kUnit) : 1u;
           if (n) atomicAdd(&fine[b % kPerOctave], n);
         }
@@ -419,9 +437,9 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         for (int r = 0; r < C; ++r) n += sh.fine[by_weight][r][b];
         two[q] = !by_weight || n == 0 ? (float)n : (float)n * ex2(-bin_exponent(octave * kPerOctave + b)) * (1.f / kUnit);
       }
-      const int l = find(two[0] + two[1], goal - before, before2);
+      const int l = find(two[0] + two[1], goal, before);
       const float first_of = __shfl_sync(kFull, two[0], l);
-      const int b = octave * kPerOctave + 2 * l + (first_of > 0.f && before + before2 + first_of >= goal ? 0 : 1);
+      const int b = octave * kPerOctave + 2 * l + (first_of > 0.f && before + first_of >= goal ? 0 : 1);
       __syncthreads();
       if (tid == 0) sh.bin = b;
       __syncthreads();
@@ -431,8 +449,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
       // any order).
       if (bins.shift >= 0) {
       each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
-        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+        const Four v{v4};
+#pragma unroll kFour
         for (int q = 0; q < 4; ++q) {
           const int b = bin_of(v[q], i + q);
           if (b < 0) continue;
@@ -506,9 +524,9 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
             sh.weight[at] = w;
           }
         };
-        if (plain && by_weight && bins.shift < 0 && bin < kFine && s.whole != kFar) {
+        if (plain && by_weight && bins.shift < 0 && bin < kLast * kPerOctave && s.whole != kFar) {
           each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
-            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+            const Four v{v4};
             uint64_t w[4];
             int b[4];
             bool any = false;
@@ -527,8 +545,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
               if (b[q] == bin) list(v[q], i + q, w[q]);
           });
         } else each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
-          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+          const Four v{v4};
+#pragma unroll kFour
           for (int q = 0; q < 4; ++q) {
             const int b = bin_of(v[q], i + q);
             const uint64_t w = by_weight ? weight_of(v[q], s, table) : 1;
@@ -630,7 +648,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         limit = sh.all[0];
         first_sums = false;
         if (sh.state == kFound) {
-          summed = by_weight && bins.shift < 0 && bin < kFine ? bin : -1;
+          summed = by_weight && bins.shift < 0 ? bin : -1;
           return sh.border;
         }
         if (sh.state == kDivide) {
@@ -656,9 +674,9 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   // The sums of the kept weights.
   const Edge edge{from};
   auto kept_sum = [&](int i, float4 v4) {
-    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+    const Four v{v4};
     uint64_t w = 0;
-#pragma unroll
+#pragma unroll kFour
     for (int q = 0; q < 4; ++q)
       if (edge.reached(v[q], i + q - lead)) w += weight_of(v[q], s, table);
     return w;
@@ -666,15 +684,15 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   uint64_t mine = 0;
   if (summed >= 0 && from == border) {  // known but for the border's bin
     each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
-      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+      const Four v{v4};
+#pragma unroll kFour
       for (int q = 0; q < 4; ++q)
         if (nearest_64th(exponent_of(v[q], s)) == summed && edge.reached(v[q], i + q - lead)) mine += weight_of(v[q], s, table);
     });
   } else if (from == 0 && s.whole != kFar) {
     each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int, float4 v4) {
-      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+      const Four v{v4};
+#pragma unroll kFour
       for (int q = 0; q < 4; ++q) {
         const uint64_t w = near_weight(v[q], s, table);
         if (exponent_of(v[q], s) < kLightest) mine += w;
@@ -726,8 +744,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
     }
     __syncthreads();
     if (target < start || target >= start + here) continue;
-    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
+    const Four v{v4};
+#pragma unroll kFour
     for (int q = 0; q < 4; ++q) {
       if (!edge.reached(v[q], at + q - lead)) continue;
       const uint64_t w = weight_of(v[q], s, table);

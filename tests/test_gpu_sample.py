@@ -237,3 +237,29 @@ def test_sample_repeats_and_streams(dev):
     for x in (big, few):
         for ids, lp in outs[x]:
             assert torch.equal(ids, want[x][0]) and torch.equal(lp, want[x][1])
+
+
+@pytest.mark.parametrize("low,high", [(14.9, 15.1), (15.0, 19.0), (22.0, 31.0), (29.9, 30.1), (30.0, 33.0), (40.0, 47.0)])
+@pytest.mark.parametrize("kind", ["k", "p", "both"])
+def test_sample_border_many_octaves_down(dev, low, high, kind):
+    """A few heavy tokens and very many that weigh 2^-low to 2^-high: the border lies among these, and u chooses there."""
+    V, M = 100003, 8
+    rng = np.random.default_rng(int(low * 10))
+    E = np.sort(rng.uniform(low, high, (M, V)), axis=1)
+    E[:, :3] = (0.0, 1.0, 2.5)
+    x = (-E * np.log(2.0)).astype(np.float32)
+    tail = 2.0 ** -np.float64(E[:, 3:]).mean(1) * (V - 3)
+    whole = 1.0 + 0.5 + 2.0 ** -2.5 + tail
+    k = np.array([4, 5, 100, V // 3, V // 2, V - 2, V - 1, V]) if kind != "p" else 0
+    p = np.float32(1.0 - tail / whole * np.linspace(0.02, 0.98, M)) if kind != "k" else 1.0
+    u = np.float32(1.0 - tail / whole * np.linspace(0.9, 0.1, M))
+    u = np.minimum(u, np.float32(1.0 - 2.0 ** -24))
+    ids, lp = run(dev, x, u, 1.0, k, p)
+    k, p = np.broadcast_to(k, M), np.broadcast_to(np.float64(p), M)
+    for m in range(M):
+        # Tokens here are lighter than the slack of a sum: the oracle names those at its two ends, and each one between
+        # them is as near to the border, since the sum of the kept weights grows with the id.
+        may, want = PO.sample(x[m], np.float64(u[m]), 1.0, int(k[m]), p[m], 0.0, SLACK)
+        assert min(may) <= ids[m] <= max(may), (m, ids[m], may)
+        ref = want[0] + np.float64(x[m, ids[m]]) - np.float64(x[m, may[0]])
+        assert abs(float(lp[m]) - ref) <= 2.0 ** -24 * abs(ref) + 2.0 ** -24, (m, lp[m], ref)
