@@ -34,7 +34,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kMaxC = 8;
+constexpr int kNT = 512, kPerSm = 2;                     // threads of a CTA, CTAs that an SM holds
+constexpr int kMaxC = 8;                                 // CTAs of a row
 constexpr int kBins = 1024;                              // of a division by key, and by the weight
 constexpr float kUnit = 4096.f;                          // of the approximate weights
 constexpr int kList = 256;                               // tokens that are listed
@@ -149,11 +150,6 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
-// Four logits by number, without an array.
-struct Four {
-  float4 v;
-  __device__ __forceinline__ float operator[](int q) const { return q & 2 ? (q & 1 ? v.w : v.z) : (q & 1 ? v.y : v.x); }
-};
 // 2^64 p for p in [0, 1), rounded down (exact from 2^-40 on)
 __device__ __forceinline__ uint64_t frac64(float p) {
   const uint32_t b = __float_as_uint(p);
@@ -203,12 +199,8 @@ struct Shared {
 enum { kFound, kAgain, kDivide };  // the border is known; it lies in another bin; divide the bin
 
 // Grid: M clusters of C CTAs.
-template <int kNT, int kPerSm>
 __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a, int per_cta, int in_shared) {
   constexpr int kNW = kNT / 32;
-  // Steps of a loop over four logits laid out side by side.  CTAs of few rows run each pass once, and the time that their
-  // code takes to come (some 20 cycles an instruction) is most of it.
-  constexpr int kFour = kNT == 1024 ? 1 : 4;
   static_assert(kBins % kNT == 0, "bins per thread");
   extern __shared__ __align__(16) float s_row[];
   __shared__ Shared sh;
@@ -349,8 +341,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         for (int o = 0; o < kOctaves; ++o) mine[o * kNT] = 0.f;
         if (plain) {
           each(i0 + 4 * tid, i1, 4 * kNT, [&](int, float4 v4) {
-            const Four v{v4};
-#pragma unroll kFour
+            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float p = exponent_of(v[q], s);
               const int o = min((nearest_64th(p) >> 6) - begin, kOctaves - 1);
@@ -359,8 +351,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
           });
         } else {
           each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
-            const Four v{v4};
-#pragma unroll kFour
+            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float p = exponent_of(v[q], s);
               if (!(p < kLightest) || !low.reached(v[q], i + q - lead)) continue;
@@ -399,8 +391,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
       }
       if (plain) {
         each(i0 + 4 * tid, i1, 4 * kNT, [&](int, float4 v4) {
-          const Four v{v4};
-#pragma unroll kFour
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float p = exponent_of(v[q], s), near = fmaf(p, (float)kPerOctave, kWhole);
             const unsigned b = (unsigned)(__float_as_int(near) - (kWholeBits + octave * kPerOctave));
@@ -412,8 +404,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         });
       } else {
       each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
-        const Four v{v4};
-#pragma unroll kFour
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float p = exponent_of(v[q], s);
           if (!(p < kLightest)) continue;
@@ -449,8 +441,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
       // any order).
       if (bins.shift >= 0) {
       each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
-        const Four v{v4};
-#pragma unroll kFour
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int b = bin_of(v[q], i + q);
           if (b < 0) continue;
@@ -526,7 +518,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         };
         if (plain && by_weight && bins.shift < 0 && bin < kLast * kPerOctave && s.whole != kFar) {
           each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
-            const Four v{v4};
+            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
             uint64_t w[4];
             int b[4];
             bool any = false;
@@ -545,8 +537,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
               if (b[q] == bin) list(v[q], i + q, w[q]);
           });
         } else each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
-          const Four v{v4};
-#pragma unroll kFour
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int b = bin_of(v[q], i + q);
             const uint64_t w = by_weight ? weight_of(v[q], s, table) : 1;
@@ -674,9 +666,9 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   // The sums of the kept weights.
   const Edge edge{from};
   auto kept_sum = [&](int i, float4 v4) {
-    const Four v{v4};
+    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
     uint64_t w = 0;
-#pragma unroll kFour
+#pragma unroll
     for (int q = 0; q < 4; ++q)
       if (edge.reached(v[q], i + q - lead)) w += weight_of(v[q], s, table);
     return w;
@@ -684,15 +676,15 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   uint64_t mine = 0;
   if (summed >= 0 && from == border) {  // known but for the border's bin
     each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
-      const Four v{v4};
-#pragma unroll kFour
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
       for (int q = 0; q < 4; ++q)
         if (nearest_64th(exponent_of(v[q], s)) == summed && edge.reached(v[q], i + q - lead)) mine += weight_of(v[q], s, table);
     });
   } else if (from == 0 && s.whole != kFar) {
     each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int, float4 v4) {
-      const Four v{v4};
-#pragma unroll kFour
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint64_t w = near_weight(v[q], s, table);
         if (exponent_of(v[q], s) < kLightest) mine += w;
@@ -744,8 +736,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
     }
     __syncthreads();
     if (target < start || target >= start + here) continue;
-    const Four v{v4};
-#pragma unroll kFour
+    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (!edge.reached(v[q], at + q - lead)) continue;
       const uint64_t w = weight_of(v[q], s, table);
@@ -763,16 +755,22 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   }
 }
 
-template <int NT, int PER_SM>
-cudaError_t launch(const SampleArgs& a, int c, int per, cudaStream_t st) {
-  auto kernel = sample_kernel<NT, PER_SM>;
-  const int in_shared = per <= kMostShared;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kMostShared + kOctaves * NT) * 4);
+}  // namespace
+
+cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t st) {
+  // CTAs per row: as few as keep it in shared memory, and twice as many while each has an SM to itself (clusters do not
+  // fill every SM, so up to 128 in all).  32000 tokens: 1 row 22 us with 2 CTAs and 17 with 8; 76 rows 24 with 2 and 36 with 4.
+  int c = 1;
+  auto per_cta = [&](int n) { return ((a.vocab + 3 + 3) / 4 + n - 1) / n * 4; };  // places, the row's lead among them
+  while (c < kMaxC && (per_cta(c) > 16 * 1024 || ((int64_t)a.M * 2 * c <= 128 && per_cta(2 * c) >= 2048))) c *= 2;
+  const int per = per_cta(c), in_shared = per <= kMostShared;
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (kMostShared + kOctaves * kNT) * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.M * c);
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = ((in_shared ? (size_t)per : 0) + kOctaves * NT) * 4;
+  cfg.blockDim = dim3(kNT);
+  cfg.dynamicSmemBytes = ((in_shared ? (size_t)per : 0) + kOctaves * kNT) * 4;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -782,21 +780,9 @@ cudaError_t launch(const SampleArgs& a, int c, int per, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, per, in_shared);
+  e = cudaLaunchKernelEx(&cfg, sample_kernel, a, per, in_shared);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_sample_tokens(const SampleArgs& a, cudaStream_t st) {
-  // CTAs per row: as few as keep it in shared memory, and more while all rows' CTAs are resident at once
-  int c = 1;
-  auto per_cta = [&](int n) { return ((a.vocab + 3 + 3) / 4 + n - 1) / n * 4; };  // places, the row's lead among them
-  while (c < kMaxC && (per_cta(c) > 16 * 1024 || ((int64_t)a.M * 2 * c <= 2 * 152 && per_cta(2 * c) >= 2048))) c *= 2;
-  const int per = per_cta(c);
-  // one CTA of many threads per SM where there are no more CTAs than SMs
-  return (int64_t)a.M * c <= 152 && per > 4096 ? launch<1024, 1>(a, c, per, st) : launch<512, 2>(a, c, per, st);
 }
 
 }  // namespace tpx
