@@ -42,7 +42,7 @@ struct TCfg {
   static constexpr int SMEM = NST * STAGE + 2 * 16 * QROW;
   static constexpr float kPLog = FP8 ? 7.f : 0.f;              // weights are held times 2^this
   static constexpr int kPerSm = HD == 256 ? 2 : 3;             // CTAs that an SM holds
-  static_assert(kPerSm * (SMEM + 3072) <= 228 * 1024, "shared memory of an SM");
+  static_assert(kPerSm * (SMEM + (3 << 10)) <= 228 * 1024, "shared memory of an SM");
   static_assert(STAGE % 1024 == 0, "swizzle atoms");
 };
 constexpr int kCompute = 128, kThreads = kCompute + 32;
