@@ -263,3 +263,17 @@ def test_sample_border_many_octaves_down(dev, low, high, kind):
         assert min(may) <= ids[m] <= max(may), (m, ids[m], may)
         ref = want[0] + np.float64(x[m, ids[m]]) - np.float64(x[m, may[0]])
         assert abs(float(lp[m]) - ref) <= 2.0 ** -24 * abs(ref) + 2.0 ** -24, (m, lp[m], ref)
+
+
+@pytest.mark.parametrize("V", [129, 257, 1001, 40003, 128256])
+def test_sample_few_and_many_of_top_k(dev, V):
+    """Top-k's tokens are taken from a list up to some number: on both sides of it, with the other filters and with ties."""
+    ks = [1, 2, 31, 32, 33, 100, 128, 129, 200, 255, 256, 257, 300]
+    settings = [dict(), dict(p=0.9), dict(p=0.4, q=0.03), dict(q=0.2), dict(p=0.0), dict(q=1.0), dict(p=0.7, T=2.0), dict(T=0.0)]
+    rows = [(k, s) for k in ks for s in settings]
+    x = normal(len(rows), V, V + 5)
+    x[::3] = np.round(x[::3] * 2.0) / 2.0                              # ties across the border
+    x[1::5] = np.where(np.random.default_rng(V).random(x[1::5].shape) < 0.3, -np.inf, x[1::5])
+    x[1::5, 5] = 1.0
+    f = lambda key, d: np.array([s.get(key, d) for _, s in rows], np.float32)
+    check(dev, x, us(len(rows), V), T=f("T", 1.0), k=np.array([k for k, _ in rows]), p=f("p", 1.0), q=f("q", 0.0), sharp=False)
