@@ -20,8 +20,8 @@
 // that bin's tokens, among which the first CTA finds the border.  Where they are too many to list (flat rows, ties) the
 // bin is divided again by key.
 //
-// Measured (128256 tokens): one row with top-p 24 us (256 threads a CTA 30, 1024 29: seven barriers of the cluster, and code that
-// is run once); 256 rows with a temperature and min-p 104 us, 1.3 TB/s, half of the issue slots; 1000 rows with top-p 942 us, 0.5 TB/s,
+// Measured (128256 tokens): one row with top-p 23 us (256 threads a CTA 30, 1024 29: seven barriers of the cluster, and code that
+// is run once); 256 rows with a temperature and min-p 104 us, 1.3 TB/s, half of the issue slots; 1000 rows with top-p 884 us, 0.6 TB/s,
 // 53% of the issue slots.  Bound by issue and by the barriers between the passes, of which the exact sums are the
 // longest; two CTAs per SM overlap.
 #include <cooperative_groups.h>
@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   // Exact sums: each warp those of a run of vectors, so that they add up in the order of ids.
   const int vectors = (i1 - i0) / 4, per_warp = (vectors + kNW - 1) / kNW;
   const int v0 = min(vectors, warp * per_warp), v1 = min(vectors, v0 + per_warp);
-  int summed = -1;  // >= 0: s_above holds the warps' exact sums of all tokens kept so far above that bin, by the weight
+  bool summed = false;  // s_above holds the warps' exact sums of all tokens kept so far above the border's bin, and
+  int in_list = 0;      // sh.key and sh.weight (the first CTA's and this one's, at least) those in it
 
   int turn = 0;
   // Of the keys from `from` on: the lowest before which fewer than k of them lie (share < 0), or before which less than
@@ -585,6 +586,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         if (c != 0) {  // what is listed goes behind what the first CTA has
           const int n = sh.listed;
           if (tid == 0) s_at = n ? atomicAdd(&first->listed, n) : 0;
+          in_list = n;
           __syncthreads();
           for (int i = tid; i < min(n, kList - s_at); i += kNT) {
             first->key[s_at + i] = sh.key[i];
@@ -606,6 +608,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
           }
           if (by_weight && first_sums) limit = max(uint64_t(1), share_up(share, all));
           const int listed = sh.listed;
+          in_list = listed;
           int state = kFound, to = bin;
           if (above >= limit) {
             state = kAgain;
@@ -646,7 +649,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
         limit = sh.all[0];
         first_sums = false;
         if (sh.state == kFound) {
-          summed = by_weight && bins.shift < 0 ? bin : -1;
+          summed = by_weight && bins.shift < 0;
           return sh.border;
         }
         if (sh.state == kDivide) {
@@ -737,30 +740,32 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
       if (edge.reached(v[q], i + q - lead)) w += weight_of(v[q], s, table);
     return w;
   };
-  uint64_t mine = 0;
-  if (summed >= 0 && from == border) {  // known but for the border's bin
-    each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v4) {
-      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (nearest_64th(exponent_of(v[q], s)) == summed && edge.reached(v[q], i + q - lead)) mine += weight_of(v[q], s, table);
-    });
-  } else if (from == 0 && s.whole != kFar) {
-    each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int, float4 v4) {
-      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint64_t w = near_weight(v[q], s, table);
-        if (exponent_of(v[q], s) < kLightest) mine += w;
-      }
-    });
-  } else {
-    each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v) { mine += kept_sum(i, v); });
-  }
-  mine = warp_sum(mine);
-  if (summed >= 0 && from == border) mine += s_above[warp];
   __syncthreads();  // (s_sum may still be read)
-  if (lane == 0) s_sum[warp] = mine;
+  if (summed && from == border) {  // known but for the border's bin, which is listed
+    if (tid < kNW) s_sum[tid] = s_above[tid];
+    __syncthreads();
+    if (tid < in_list && sh.key[tid] >= border) {
+      const int place = (int)~(uint32_t)sh.key[tid] + lead;
+      if (place >= i0 && place < i1)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s_sum[(place - i0) / 4 / per_warp]), sh.weight[tid]);
+    }
+  } else {
+    uint64_t mine = 0;
+    if (from == 0 && s.whole != kFar) {
+      each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int, float4 v4) {
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint64_t w = near_weight(v[q], s, table);
+          if (exponent_of(v[q], s) < kLightest) mine += w;
+        }
+      });
+    } else {
+      each(i0 + 4 * (v0 + lane), i0 + 4 * v1, 128, [&](int i, float4 v) { mine += kept_sum(i, v); });
+    }
+    mine = warp_sum(mine);
+    if (lane == 0) s_sum[warp] = mine;
+  }
   __syncthreads();
   if (warp == 0) {
     const uint64_t sum = warp_sum(lane < kNW ? s_sum[lane] : 0);
