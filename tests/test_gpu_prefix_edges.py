@@ -1,0 +1,67 @@
+"""Decode attention with shared prefixes where the tests against the paged call's tolerances would not tell: the bits that
+weights keep, long runs of one CTA, long sums.  The reference is the formula in 64 bits, on the device."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from megatron_tensor_transformer_gb300 import tpx
+from oracle import tp_oracle as O
+from tests.test_gpu_paged import HALF, assert_within, dev, i32, sync  # noqa: F401
+from tests.test_gpu_parity import bits
+from tests.test_gpu_prefix import BOTH, Shared, tails
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(c, scale=0.0, window=0):
+    """o [M, n_q, hd] and lse [M, n_q] of a Shared case whose requests' pages are all there; sum p |v| and the largest sum
+    |q| |k| times the scale, for the bounds."""
+    M, G = len(c.lens), c.n_q // c.n_kv
+    q = c.q.double().view(M, c.n_kv, G, c.hd) * (scale or 1 / math.sqrt(c.hd))
+    out = [[], [], [], []]
+    for m, n in enumerate(c.lens):
+        ids = torch.tensor(c.table[m, : -(-n // c.page)], device=c.dev)
+
+        def rows(x, s):
+            raw = x if c.kv == tpx.TP_BF16 else x.view(torch.uint8)
+            y = raw[:, ids].view(x.dtype).double().permute(0, 2, 1, 3, 4).reshape(c.n_kv, -1, c.hd)[:, max(0, n - window) if window else 0: n]
+            return y if s is None else y * s.double()[:, None, None]
+        k, v = rows(c.k, c.ks), rows(c.v, c.vs)
+        s = q[m] @ k.transpose(1, 2)
+        lse = torch.logsumexp(s, -1)
+        p = torch.exp(s - lse[..., None])
+        B = (q[m].abs() @ k.abs().transpose(1, 2)).amax(-1)
+        for to, x in zip(out, (p @ v, lse, p @ v.abs(), B)):
+            to.append(x.reshape(c.n_q, -1).cpu().numpy())
+    o, lse, A, B = (np.stack(x) for x in out)
+    return o, lse[..., 0], A, B[..., 0]
+
+
+def check(c, o, lse, scale=0.0, window=0, dims=None):
+    """As Shared.check, with the weights' own bits: 2^-16 of a weight over bf16 pages (two bf16: what the first leaves is
+    below 2^-7 of it, and half a step of that), 2^-11 over e4m3 pages.  dims: how many of q's elements are not zero."""
+    ro, rl, A, B = reference(c, scale, window)
+    got, got_l = O.as_f64(bits(o)).reshape(ro.shape), lse.cpu().numpy().astype(np.float64)
+    bf16 = c.kv == tpx.TP_BF16
+    n = np.array([min(x, window) if window else x for x in c.lens], np.float64)[:, None]
+    # a score within (dims + 8) 2^-23 B (adding zeros is exact), e^x 2^-21, sums n / 16 + 300 steps of 2^-24
+    ps = ((dims or c.hd) + 8) * 2.0 ** -23 * B + 2.0 ** -21 + (n / 16 + 300) * 2.0 ** -24
+    vmax = float(c.v.float().nan_to_num().abs().max()) * (1.0 if c.vs is None else float(c.vs.max()))
+    e = A * (2 * ps[..., None] + (2.0 ** -16 if bf16 else 2.0 ** -11)) + (0 if bf16 else n[..., None] * 2.0 ** -25 * vmax)
+    assert_within(got, ro, e + HALF * (np.abs(ro) + e), "o")
+    assert_within(got_l, rl, ps + 2.0 ** -21 * (1 + np.abs(rl)), "lse")
+
+
+@pytest.mark.parametrize("kv", BOTH)
+@pytest.mark.parametrize("hd,n_q", [(64, 16), (128, 32), (256, 8)])
+@pytest.mark.parametrize("groups,lens", [([(1, 0)] * 6, [700, 33, 1000, 5, 129, 2500])])               # each request by itself
+def test_prefix_attention_weights_keep_their_bits(dev, kv, hd, n_q, groups, lens):
+    """o is off by its own rounding and what tp_paged_attn_decode's weights are off by, whether a request's positions are
+    shared or its own.  One element of q is not zero, so that scores are exact and spread over some ten powers of e."""
+    c = Shared(dev, 1, n_q, 2, hd, 32, groups, lens, kv, seed=hd)
+    q = c.q.view(len(lens), n_q, hd)
+    q[:, :, :3] = q[:, :, 4:] = 0
+    q[:, :, 3] = 3.0 * q[:, :, 3].sign() * math.sqrt(hd)
+    check(c, *c.launch(), dims=1)
