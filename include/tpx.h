@@ -477,10 +477,9 @@ tp_status tp_paged_attn_decode(const tp_shape* shape /* host */, const tp_pages*
  * counts as having no prefix).  n_groups is at most M; 0: as tp_paged_attn_decode (the two may then be NULL).
  * Where the table's M rows can name no more than 96 MB of cache (M max_pages page_size positions), sharing is not looked
  * at: that takes less time.
- * Scores, softmax statistics and sums are fp32.  Weights of shared positions enter the product rounded once, to bf16 over
- * bf16 pages (2^-8 of a weight, the tensor cores' operand type), those of a request's own positions as there (2^-16, two
- * bf16); over e4m3 pages all are fp16 (2^-11 of a weight and 2^-32 of the largest), and q is fp16 after a power of two per
- * head, exact down to 2^-24 of the head's largest |q|.  The parts' sums are joined in fp32.
+ * Scores, softmax statistics and sums are fp32.  The weights keep as many bits on their way into the tensor cores as there:
+ * over bf16 pages 2^-16 of a weight (two bf16), over e4m3 pages 2^-11 of it and 2^-32 of the largest (fp16; q is fp16 after a
+ * power of two per head, exact down to 2^-24 of the head's largest |q|).  The parts' sums are joined in fp32.
  * ws: tp_prefix_attn_workspace_bytes(shape, M) bytes, zero-filled once before first use (and after a
  * TP_ERR_DEVICE_TIMEOUT), left reusable by every call whose size it covers, tp_paged_attn_decode's included; calls that
  * share it must not overlap on the GPU (replays of two captured graphs included).  Up to three kernel launches; runs

@@ -9,6 +9,9 @@
 // as two blocks of 128 (128 dims and fewer), or 128 rows.  Products on tcgen05, 128 rows by 128 positions:
 //   S = Q K^T   both from shared memory, into tensor memory
 //   O += P V    P from tensor memory, where its rows' threads wrote it over S; V as TMA brought it, read transposed
+// Over bf16 pages P is two bf16, the upper halves of the weights and what these leave (2^-16 of a weight, as in paged
+// attention: half as many bits, 2^-8, showed beside the output's own rounding, 2.3e-3 of o against 1.7e-3).  That is half as
+// many MMAs again, 3072 cycles a chunk of 256 rows instead of 2048.
 // A softmax thread has one row: no shuffles, no shared memory; O stays in tensor memory and is scaled only when a
 // row's maximum passes its reference by 2^8.  With two blocks the MMAs of one run beside the exponentials of the
 // other; with one, S of the next chunk is computed before P V of this one, into the other half of S.
@@ -295,7 +298,8 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  auto S_at = [&](int r) { return tmem + 128 * r; };        // P takes the first 64 of its columns
+  // Columns of S in 64s: of P for 64 positions the first 32 hold the weights in 16 bits, over bf16 pages the last 32 the rest.
+  auto S_at = [&](int r) { return tmem + 128 * r; };
   auto O_at = [&](int x) { return tmem + 256 + HD * x; };
   // Item j as a role sees it.
   auto next_item = [&](Waits& wait, int j, bool whole_warp) {
@@ -472,14 +476,20 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
           }
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
-            uint32_t p[16];
+            uint32_t p[16], rest[16];
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
               const float2 y = make_float2(ex2(s[32 * part + 2 * q]), ex2(s[32 * part + 2 * q + 1]));
               l2[q & 1] = add2(l2[q & 1], y);
-              p[q] = pack16<FP8>(y.x, y.y);
+              if (FP8) {
+                p[q] = pack16<true>(y.x, y.y);
+              } else {  // the upper halves as they are, and what they leave, rounded: 2^-16 of a weight
+                p[q] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
+                rest[q] = pack_bf16(y.x - bf16_lo(p[q]), y.y - bf16_hi(p[q]));
+              }
             }
-            tmem_st16(sA + c / 2 + 16 * part, p);  // over columns that have been read
+            tmem_st16(sA + c + 16 * part, p);  // over columns that have been read
+            if (!FP8) tmem_st16(sA + c + 32 + 16 * part, rest);
           }
         }
         l = (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
@@ -653,23 +663,25 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
         };
         auto values = [&](int x, int region, int st, int sub, uint32_t groups, bool& live) {
           const uint64_t v0 = smem_desc(rA + st * C::STAGE, C::KS * 128, 1024, 2);
-          const uint32_t p = S_at(region) + 8 * sub * (C::KS / 16), d = O_at(x);
-          if (groups == 0xffu) {
+          const uint32_t p = S_at(region) + sub * C::KS, d = O_at(x);
 #pragma unroll 1
-            for (int i = 0; i < C::KS / 16; i += 4) {
+          for (int i = 0; i < C::KS / 16; i += 4) {  // 64 positions: 64 columns of P
+            if (groups == 0xffu) {
 #pragma unroll
-              for (int k = i; k < i + 4; ++k) {
-                warp_mma_tmem_a(d, p + 8 * k, v0 + tc::desc_off(2048) * k, idO, live);
+              for (int k = 0; k < 4; ++k) {
+                warp_mma_tmem_a(d, p + 16 * i + 8 * k, v0 + tc::desc_off(2048) * (i + k), idO, live);
+                if (!FP8) warp_mma_tmem_a(d, p + 16 * i + 32 + 8 * k, v0 + tc::desc_off(2048) * (i + k), idO, true);
                 live = true;
               }
+              continue;
             }
-            return;
-          }
 #pragma unroll 1
-          for (int i = 0; i < C::KS / 16; ++i) {
-            if (!(groups >> (sub * (C::KS / 16) + i) & 1)) continue;  // what was not loaded may hold anything
-            warp_mma_tmem_a(d, p + 8 * i, v0 + tc::desc_off(i * 2048), idO, live);
-            live = true;
+            for (int k = 0; k < 4; ++k) {
+              if (!(groups >> (sub * (C::KS / 16) + i + k) & 1)) continue;  // what was not loaded may hold anything
+              warp_mma_tmem_a(d, p + 16 * i + 8 * k, v0 + tc::desc_off(2048) * (i + k), idO, live);
+              if (!FP8) warp_mma_tmem_a(d, p + 16 * i + 32 + 8 * k, v0 + tc::desc_off(2048) * (i + k), idO, true);
+              live = true;
+            }
           }
         };
         for (int j = 0;; ++j) {

@@ -56,7 +56,9 @@ def check(c, o, lse, scale=0.0, window=0, dims=None):
 
 @pytest.mark.parametrize("kv", BOTH)
 @pytest.mark.parametrize("hd,n_q", [(64, 16), (128, 32), (256, 8)])
-@pytest.mark.parametrize("groups,lens", [([(1, 0)] * 6, [700, 33, 1000, 5, 129, 2500])])               # each request by itself
+@pytest.mark.parametrize("groups,lens", [([(1, 0)] * 6, [700, 33, 1000, 5, 129, 2500]),               # each request by itself
+                                         ([(3, 2000)], [2000, 2017, 2001]),                             # few rows share
+                                         ([(20, 1500), (2, 640)], [1500 + 3 * i for i in range(20)] + [700, 641])])
 def test_prefix_attention_weights_keep_their_bits(dev, kv, hd, n_q, groups, lens):
     """o is off by its own rounding and what tp_paged_attn_decode's weights are off by, whether a request's positions are
     shared or its own.  One element of q is not zero, so that scores are exact and spread over some ten powers of e."""
