@@ -69,7 +69,8 @@ constexpr int tail_positions(int hd, bool fp8) {
   const int n = 16384 / (hd * (fp8 ? 1 : 2));
   return n < 128 ? n : 128;
 }
-// launched behind launch_prefix_attn's first kernel, for whose end it does not wait before its own
+// launched behind launch_prefix_attn's first kernel, for whose end it does not wait before its own; that one has to begin
+// after all work that this one reads or overwrites
 cudaError_t launch_tail_attn(const GroupedAttnArgs& a, int kv_dtype, int hd, cudaStream_t st);
 // What groups share, the requests' own positions, and the two joined: three launches.  a: with groups and pages set; ws:
 // prefix_attn_workspace_bytes.

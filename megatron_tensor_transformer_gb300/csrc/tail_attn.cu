@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, TCfg<HD, FP8>::kPerSm)
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
-  // No wait for the kernel before: it waited for all work before itself, and this one reads nothing of its.  At the end
-  // it is waited for, so that what follows this kernel follows both.
+  // No wait for the kernel before: it began after all work before the call, so that this one did too, and this one reads
+  // nothing of its.  At the end it is waited for, so that what follows this kernel follows both.
   tc::griddep_launch_dependents();
   const int G = a.n_q / a.n_kv;
   const bool groups = __syncthreads_and(groups_in_order(a, tid, kThreads));

@@ -1,5 +1,6 @@
 """Decode attention with shared prefixes where the tests against the paged call's tolerances would not tell: the bits that
 weights keep, long runs of one CTA, long sums.  The reference is the formula in 64 bits, on the device."""
+import ctypes
 import math
 
 import numpy as np
@@ -67,3 +68,33 @@ def test_prefix_attention_weights_keep_their_bits(dev, kv, hd, n_q, groups, lens
     q[:, :, :3] = q[:, :, 4:] = 0
     q[:, :, 3] = 3.0 * q[:, :, 3].sign() * math.sqrt(hd)
     check(c, *c.launch(), dims=1)
+
+
+def test_prefix_attention_begins_behind_all_work_before(dev):
+    """The second and third kernel read what the call was given beside the first one, without a wait.  So the first has to
+    be launched in full stream order: in a captured call its edge from the work before is an ordinary one (full completion,
+    with visibility), and only the edges behind it are programmatic."""
+    groups = [(4, 300)]
+    c = Shared(dev, 1, 8, 2, 64, 16, groups, tails(groups, 3), seed=3)
+    want, _ = c.launch()
+    o, graph = torch.zeros_like(want), torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        c.q.mul_(1.0)                                                  # work that the call has to wait for
+        c.call(o, None)
+    f = ctypes.CDLL("libcudart.so.13").cudaGraphGetEdges
+    f.argtypes = [ctypes.c_void_p] * 5
+    n, handle = ctypes.c_size_t(0), ctypes.c_void_p(graph.raw_cuda_graph())
+    assert f(handle, None, None, None, ctypes.byref(n)) == 0
+    edges, ends = (ctypes.c_uint8 * (8 * n.value))(), [(ctypes.c_void_p * n.value)() for _ in range(2)]
+    assert f(handle, *ends, edges, ctypes.byref(n)) == 0
+    kinds = {ends[0][i]: (ends[1][i], edges[8 * i + 2]) for i in range(n.value)}  # node: the next one, the edge's type
+    at, order = (set(ends[0]) - set(ends[1])).pop(), []
+    while at in kinds:
+        at, kind = kinds[at]
+        order.append(kind)
+    assert order == [0, 1, 1], order
+    graph.instantiate()
+    for _ in range(3):
+        graph.replay()
+    sync()
+    assert torch.equal(o.view(torch.int16), want.view(torch.int16))
