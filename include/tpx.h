@@ -545,12 +545,12 @@ tp_status tp_token_logprobs(const float* logits, int64_t ldl, int32_t M, int32_t
  *   S = the ranks of N with w_i >= min_p, the largest w being 1             (min_p <= 0: all of N)
  * S always holds the first rank.  ids[m] is the lowest id of S up to which, ids in order, the sum of S's w exceeds u[m]
  * times all of it (u >= 1: the last id of S with a weight, u < 0: the first); logprob[m] = ln(w / that sum) of it.
- * temperature <= 0 takes the first rank, with logprob 0; one below 2^-100 counts as 2^-100.  A logit whose difference to
- * the largest passes fp32's range weighs 0.
+ * temperature <= 0 takes the first rank, with logprob 0; one below 2^-100 counts as 2^-100, at +inf all weigh 1.  A logit
+ * whose difference to the largest passes fp32's range weighs 0 at every temperature.
  * u, temperature, top_k, top_p, min_p: [M] on the device (int32 for top_k, else fp32); the last four, and logprob, may be
  * NULL (1, 0, 1, 0).  A row that holds a NaN or +inf, or only -inf, or has a NaN among its settings, has no
  * distribution: id -1, logprob NaN.
- * Weights are good to 2^-29 of themselves and held as whole multiples, rounded down, of 2^-44 of a power of two at or
+ * Weights are good to 2^-29 of themselves (2^-21 for logits beyond 2^120 at temperatures beyond 2^120) and held as whole multiples, rounded down, of 2^-44 of a power of two at or
  * just above the largest (a token that weighs less is never chosen), and their sums are exact: a row's result follows
  * from its logits and settings alone, not from how the work is split.
  * Pointers 4-byte aligned, logits' rows too; vocab at most 2^19 (TP_ERR_UNSUPPORTED otherwise).  No workspace.  One kernel

@@ -243,10 +243,12 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   const int tk = T <= 0.f ? 1 : a.top_k ? a.top_k[m] : 0;
   if (tid == kNT - 1) {  // 64-bit arithmetic is slow here: one thread's, beside the loads
     const double t64 = T <= 0.f ? 1.0 : fmax((double)T, 0x1p-100), scale = 1.4426950408889634 / t64;
-    s_scale[0] = (float)scale;
+    // An infinite temperature: the two parts add up to 0, but a difference times the first is small, not 0, so that one past
+    // fp32's range (a masked logit) is infinite and weighs 0 here too.
+    s_scale[0] = fmaxf((float)scale, 0x1p-149f);
     s_scale[1] = (float)(scale - (double)s_scale[0]);
     s_inv = 1.0 / t64;
-    s_min = mp > 0.f ? t64 * log((double)fminf(mp, 1.f)) : 0.0;
+    s_min = !(mp > 0.f) ? 0.0 : T < INFINITY ? t64 * log((double)fminf(mp, 1.f)) : -INFINITY;  // infinite: all weigh 1
   }
   float top = -INFINITY;
   {

@@ -149,7 +149,8 @@ def sample(x, u, T=1.0, k=0, p=1.0, q=0.0, slack=0.0):
     order = np.lexsort((np.arange(len(x)), -x))
     if T <= 0:
         return [int(order[0])], [0.0]
-    w = np.exp((x - x.max()) / max(T, 2.0 ** -100))
+    with np.errstate(invalid="ignore"):                                # a masked logit at an infinite temperature
+        w = np.exp((x - x.max()) / max(T, 2.0 ** -100))
     w[x.max() - x > np.finfo(np.float32).max] = 0
     ranks = order[:k] if k > 0 else order
     found = set()

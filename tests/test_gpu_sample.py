@@ -277,3 +277,21 @@ def test_sample_few_and_many_of_top_k(dev, V):
     x[1::5, 5] = 1.0
     f = lambda key, d: np.array([s.get(key, d) for _, s in rows], np.float32)
     check(dev, x, us(len(rows), V), T=f("T", 1.0), k=np.array([k for k, _ in rows]), p=f("p", 1.0), q=f("q", 0.0), sharp=False)
+
+
+@pytest.mark.parametrize("kw", [dict(q=1.0), dict(q=0.5), dict(), dict(p=0.3), dict(k=700, p=0.9, q=1.0), dict(k=40, p=0.6, q=1.0)])
+def test_sample_infinite_temperature(dev, kw):
+    """Every token that is not masked weighs the same, min_p of 1 and less leaves all of them."""
+    V = 5003
+    x = normal(6, V, 17)
+    u = np.array([0.0, 0.25, 0.5, 0.75, 1 - 2.0 ** -24, 0.1], np.float32)
+    check(dev, x, u, T=np.inf, sharp=False, **kw)                      # (u n is a whole number, a border, for some n and u)
+    x[:, 1000:1400] = -np.inf
+    x[3, 1:] = -np.inf
+    x[4, 7], x[4, 8] = 3e38, -3e38                                     # every difference to the largest but this one is finite
+    ids, lp = check(dev, x, u, T=np.inf, sharp=False, **kw)
+    assert ids[3] == 0 and lp[3] == 0.0 and not ((1000 <= ids) & (ids < 1400)).any() and ids[4] != 8
+    ids, _ = run(dev, np.where(np.arange(V) % 2 == 0, x[:1], -np.inf).repeat(6, 0), u, np.inf, 0, 1.0, 1.0)
+    n = (V + 1) // 2 - 200                                             # even ids, but for 1000 .. 1398
+    nth = np.floor(u.astype(np.float64) * n).astype(int)
+    assert np.array_equal(ids, np.where(nth < 500, 2 * nth, 2 * nth + 400))
