@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
   };
   const float T = a.temperature ? a.temperature[m] : 1.f, tp = a.top_p ? a.top_p[m] : 1.f,
               mp = a.min_p ? a.min_p[m] : 0.f, u = a.u[m];
-  const int tk = T <= 0.f ? 1 : a.top_k ? a.top_k[m] : 0;
+  const int tk = T <= 0.f || mp > 1.f ? 1 : a.top_k ? a.top_k[m] : 0;  // no weight passes a min-p above 1: the first rank
   if (tid == kNT - 1) {  // 64-bit arithmetic is slow here: one thread's, beside the loads
     const double t64 = T <= 0.f ? 1.0 : fmax((double)T, 0x1p-100), scale = 1.4426950408889634 / t64;
     // An infinite temperature: the two parts add up to 0, but a difference times the first is small, not 0, so that one past

@@ -160,7 +160,7 @@ def sample(x, u, T=1.0, k=0, p=1.0, q=0.0, slack=0.0):
             mass = np.cumsum(w[ranks]) - w[ranks]
             kept = ranks[(mass < p * (1 + s) * w[ranks].sum()) | (np.arange(len(ranks)) == 0)]
         if q > 0:
-            kept = kept[(w[kept] >= q) | (np.arange(len(kept)) == 0) | (x[kept] == x.max())]
+            kept = kept[(w[kept] >= q) | (np.arange(len(kept)) == 0)]
         live = np.sort(kept[w[kept] >= 2.0 ** -45])
         edge = np.cumsum(w[live])
         for s2 in ((0.0,) if slack == 0 else (-slack, 0.0, slack)):

@@ -295,3 +295,15 @@ def test_sample_infinite_temperature(dev, kw):
     n = (V + 1) // 2 - 200                                             # even ids, but for 1000 .. 1398
     nth = np.floor(u.astype(np.float64) * n).astype(int)
     assert np.array_equal(ids, np.where(nth < 500, 2 * nth, 2 * nth + 400))
+
+
+@pytest.mark.parametrize("q", [1.0 + 2.0 ** -23, 1.5, 3e38, np.inf])
+def test_sample_min_p_above_one(dev, q):
+    """No weight reaches it, so the first rank alone is left: of equal largest logits the lowest id."""
+    x = normal(8, 3001, 18)
+    x[::2, [2000, 50, 700]] = 40.0
+    for kw in (dict(), dict(T=0.3), dict(T=np.inf), dict(k=5), dict(k=1000, p=0.99), dict(p=0.2)):
+        ids, lp = check(dev, x, us(8, 18), q=q, **kw)
+        assert np.array_equal(ids, x.argmax(1)) and (lp == 0).all()
+    ids, lp = check(dev, x, us(8, 18), q=1.0)                          # reached by the equal ones
+    assert set(ids[::2]) <= {50, 700, 2000} and len(set(ids[::2])) > 1 and np.abs(lp[::2] + np.log(3)).max() < 1e-6

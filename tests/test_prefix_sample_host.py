@@ -104,3 +104,10 @@ def test_oracle_shared_rows():
     assert got == [(0, 0), (32, 1), (32, 1), (16, 3), (16, 3), (16, 3), (0, 6), (0, 7)]
     assert PO.shared_by([2, 1, 9], [50, 40], 8, 16, 10) == [(0, m) for m in range(8)]
     assert PO.shared_by([0, 4], [161], 4, 16, 10) == [(0, m) for m in range(4)]
+
+
+def test_oracle_sample_min_p_above_one_and_infinite_temperature():
+    x = np.array([0.0, 2.0, 2.0, -np.inf])
+    assert [PO.sample(x, u, q=1.5) for u in (0.0, 0.9)] == [([1], [0.0])] * 2
+    assert [PO.sample(x, u, q=1.0)[0] for u in (0.4, 0.6)] == [[1], [2]]
+    assert [PO.sample(x, u, T=np.inf, q=q)[0][0] for q in (0.0, 0.5, 1.0) for u in (0.0, 0.4, 0.7, 0.999)] == [0, 1, 2, 2] * 3
