@@ -550,9 +550,9 @@ tp_status tp_token_logprobs(const float* logits, int64_t ldl, int32_t M, int32_t
  * u, temperature, top_k, top_p, min_p: [M] on the device (int32 for top_k, else fp32); the last four, and logprob, may be
  * NULL (1, 0, 1, 0).  A row that holds a NaN or +inf, or only -inf, or has a NaN among its settings, has no
  * distribution: id -1, logprob NaN.
- * Weights are good to 2^-29 of themselves (2^-21 for logits beyond 2^120 at temperatures beyond 2^120) and held as whole multiples, rounded down, of 2^-44 of a power of two at or
- * just above the largest (a token that weighs less is never chosen), and their sums are exact: a row's result follows
- * from its logits and settings alone, not from how the work is split.
+ * Weights are good to 2^-29 of themselves (2^-21 where logits lie beyond 2^120) and held as whole multiples, rounded down,
+ * of 2^-44 of a power of two at or just above the largest (a token that weighs less is never chosen), and their sums are
+ * exact: a row's result follows from its logits and settings alone, not from how the work is split.
  * Pointers 4-byte aligned, logits' rows too; vocab at most 2^19 (TP_ERR_UNSUPPORTED otherwise).  No workspace.  One kernel
  * launch.  M == 0 is a no-op. */
 tp_status tp_sample_tokens(const float* logits, int64_t ldl, int32_t M, int32_t vocab, const float* u,

@@ -198,7 +198,9 @@ struct Shared {
   uint64_t key[kList], weight[kList];
   int listed;                    // tokens of the bin, of which the first kList are listed
   uint64_t above[kMaxC], in[kMaxC], all[kMaxC], least[kMaxC], most[kMaxC];  // of each CTA
+  // (the answer to all is in above[0], what lies above the bin, and all[0], the limit: fields of their own took 1.5% longer)
   int bin, state;                // the border's bin; what to do next
+  int ahead, behind, step;       // bins between which the border's is (the first CTA's, one thread's)
   uint64_t border;               // the lowest key that is kept
   Bins bins;
 };
@@ -446,6 +448,11 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
       __syncthreads();
     }
     for (bool first_sums = true;;) {
+      if (tid == 0) {
+        sh.ahead = -1;
+        sh.behind = bins.shift < 0 ? kLast * kPerOctave + 1 : kBins;
+        sh.step = 1;
+      }
       // Divided by key: what the bins hold, tokens, or roughly their weights in terms of the bin's heaviest (whole numbers, in
       // any order).
       if (bins.shift >= 0) {
@@ -611,15 +618,18 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
           if (by_weight && first_sums) limit = max(uint64_t(1), share_up(share, all));
           const int listed = sh.listed;
           in_list = listed;
-          int state = kFound, to = bin;
-          if (above >= limit) {
-            state = kAgain;
-            to = bin - 1;
-          } else if (above + in < limit) {
-            state = kAgain;
-            to = bin + 1;
-          } else if (listed >= kList) {  // some may not be there
-            state = kDivide;
+          // (where kList are listed, some may not be there)
+          const int state = above >= limit || above + in < limit ? kAgain : listed >= kList ? kDivide : kFound;
+          if (state == kAgain && tid == 0) {
+            // The first sums are fp32 and good to some 2^-20 of all, less than many bins hold.  Where they miss the border's bin:
+            // 1, 2, 4, .. bins on until it is passed, then halves of what is left.  (One after another took a thousand passes,
+            // 7 to 14 ms for 64 rows, where one token weighs nearly top-p of all; now 0.2.)
+            const int step = sh.step;
+            (above >= limit ? sh.behind : sh.ahead) = bin;
+            const int half = (sh.ahead + sh.behind) >> 1;
+            sh.step = 2 * step;
+            for (int r = 0; r < C; ++r)
+              cl.map_shared_rank(&sh, r)->bin = above >= limit ? max(bin - step, half) : min(bin + step, half);
           }
           uint64_t lowest_kept = ~0ull;
           if (state == kFound) {  // a token is kept if what is ahead of it is below the limit
@@ -638,7 +648,6 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
             for (int w = 0; w < kNW; ++w) lowest_kept = min(lowest_kept, s_least[w]);
             Shared* to_sh = cl.map_shared_rank(&sh, tid);
             to_sh->state = state;
-            to_sh->bin = to;
             to_sh->border = lowest_kept;
             const int bits = 64 - __clzll((long long)(most - least));
             to_sh->bins = Bins{least, most, max(0, bits - 10)};

@@ -1,5 +1,7 @@
 """Sampled tokens through the C ABI against the float64 oracle: the id exactly (or, where a sum lies within the
 weights' error of its border, one of the two beside it), logprob within its rounding."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -307,3 +309,42 @@ def test_sample_min_p_above_one(dev, q):
         assert np.array_equal(ids, x.argmax(1)) and (lp == 0).all()
     ids, lp = check(dev, x, us(8, 18), q=1.0)                          # reached by the equal ones
     assert set(ids[::2]) <= {50, 700, 2000} and len(set(ids[::2])) > 1 and np.abs(lp[::2] + np.log(3)).max() < 1e-6
+
+
+def timed(dev, x, p, M):
+    """Microseconds of a call over M rows x, the median of seven; and its ids."""
+    rows = torch.from_numpy(x).to(dev).expand(M, -1).contiguous()
+    u = torch.full((M,), 0.5, device=dev)
+    p = torch.tensor(np.broadcast_to(np.float32(p), M).copy(), device=dev)
+    ids, lp = torch.zeros(M, dtype=torch.int32, device=dev), torch.zeros(M, device=dev)
+    times = []
+    for _ in range(7):
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        e[0].record()
+        tpx.tp_sample_tokens(rows, u, ids, None, None, p, None, lp)
+        e[1].record()
+        torch.cuda.synchronize()
+        times.append(e[0].elapsed_time(e[1]) * 1e3)
+    return sorted(times)[3], ids.cpu().numpy(), lp.cpu().numpy()
+
+
+@pytest.mark.parametrize("share,low,high", [(0.5, 17.0, 17.0), (0.99, 24.0, 40.0), (1 - 2.0 ** -20, 36.0, 45.0)])
+def test_sample_border_at_the_heavy_tokens_end(dev, share, low, high):
+    """One token with nearly `share` of the weight, then many light ones octaves below; top-p on both sides of that share, to
+    the last bits.  Sums in fp32 cannot tell which side it is on; a row takes a few passes more for it, not a thousand."""
+    V, M = 128256, 64
+    rng = np.random.default_rng(int(low))
+    E = rng.uniform(low, high, V) if high > low else np.full(V, low)
+    x = (-E * np.log(2.0)).astype(np.float32)
+    rest = np.exp(x.astype(np.float64)).sum() - math.exp(x[777])
+    x[777] = math.log(share / (1 - share) * rest)
+    w = np.exp(x.astype(np.float64) - x[777])
+    own = 1 / w.sum()                                                  # the heavy token's share
+    step = np.spacing(np.float32(own))
+    p = np.minimum(np.float32(own) + step * np.arange(-M // 2, M // 2), 1 - 2.0 ** -24).astype(np.float32)
+    usual, _, _ = timed(dev, x[None], 0.7 * own, M)                    # far from the border: the heavy token alone is left
+    took, ids, lp = timed(dev, x[None], p, M)
+    for m in range(M):
+        may, _ = PO.sample(x, 0.5, 1.0, 0, np.float64(p[m]), 0.0, SLACK)
+        assert min(may) <= ids[m] <= max(may), (m, ids[m], may)
+    assert took <= 4 * usual + 40, (took, usual)
