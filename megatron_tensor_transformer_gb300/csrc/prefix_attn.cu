@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
         // divides out.  Beyond 2^20 it could be large: there the product is rounded by itself.
         const bool far = !(fabsf(sub) < 1048576.f), any_far = __any_sync(kFull, far);
         const float2 sc2 = make_float2(sc, sc), sub2 = make_float2(-sub, -sub);
-        float2 l2[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
         for (int c = 0; c < 128; c += 64) {
           float s[64];
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
             if (!FP8) tmem_st16(sA + c + 32 + 16 * part, rest);
           }
         }
-        l = (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
+        l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);  // a chunk by itself: n / 128 + 34 roundings for n positions
         tc::tmem_st_wait();
         live |= groups != 0;
         tc::tc_fence_before();

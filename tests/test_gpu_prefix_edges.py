@@ -98,3 +98,34 @@ def test_prefix_attention_begins_behind_all_work_before(dev):
         graph.replay()
     sync()
     assert torch.equal(o.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("kv", BOTH)
+@pytest.mark.parametrize("rows", [2, 20])
+def test_prefix_attention_long_sums_of_one_cta(dev, kv, rows):
+    """As many tiles as CTAs, each 16384 positions long and with one key ahead of equal others, whose weight a sum of many of
+    them rounds the same way every time: a chunk's sum is taken by itself, so a CTA rounds n / 128 + 34 times."""
+    sms, n = torch.cuda.get_device_properties(dev).multi_processor_count, 16384
+    n_kv = max(x for x in range(1, 17) if sms % x == 0)
+    n_q, G = 16 * n_kv if rows == 20 else n_kv, sms // n_kv            # 320 rows: a full tile and a narrow one; or 2
+    c = Shared(dev, 1, n_q, n_kv, 64, 64, [(2, n)], [n, n], kv, seed=3, poison=False, std=1.0)
+    # every group names the same pages
+    M = rows * G
+    c.lens, c.table = [n] * M, np.repeat(c.table[:1], M, 0)
+    c.cu, c.prefix = rows * np.arange(G + 1), [n] * G
+    c.ws = tpx.new_prefix_attn_workspace(c.sh, M, dev)
+    c.k.copy_(torch.zeros(c.k.shape, device=dev).to(c.k.dtype))
+    c.k[:, int(c.table[0, 0]), :, 0, 0] = torch.ones((1, n_kv), device=dev).to(c.k.dtype)
+    if kv == tpx.TP_FP8_E4M3:
+        c.ks.fill_(1.0)
+    q = torch.zeros((M, n_q, 64), device=dev)
+    d = torch.linspace(0.05, 3.0, M * n_q, device=dev).to(torch.bfloat16)
+    q[:, :, 0] = d.view(M, n_q).float()
+    c.q = q.to(torch.bfloat16).view(M, -1)
+    _, lse = c.launch(scale=1.0)
+    x = d.double().cpu().numpy().reshape(M, n_q)
+    want = x + np.log1p((n - 1) * np.exp(-x))
+    # a score's product within 2^-23 of itself, e^x 2^-21, the sum's roundings, lse's own (log2 and its product: 2^-22)
+    bound = 2.0 ** -23 * x + 2.0 ** -21 + (n / 128 + 34 + 10) * 2.0 ** -24 + 2.0 ** -22 * want
+    over = np.abs(lse.cpu().numpy().astype(np.float64) - want) - bound
+    assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
