@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
   } else {
     if (warp == kProducer) {
       // ---- k and v in the order in which the MMAs take them: a stage is SUB-th of a chunk's k or v
-      Waits wait{a.err, 54u, false};
+      Waits wait{a.err, 59u, false};
       const int box_rows = min(1 << a.page_shift, C::KS), nbp = C::KS / box_rows;  // boxes along the positions
       const int box = lane % nbp, side = lane / nbp;
       int cnt = 0, kc = 0;
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
         }
       }
       const int last = cnt - 1 - lane;  // copies in flight: each stage's last
-      if (lane < C::NT && last >= 0) wait_long(B(tfull[last % C::NT]), (last / C::NT) & 1, a.err, 54u);
+      if (lane < C::NT && last >= 0) wait_long(B(tfull[last % C::NT]), (last / C::NT) & 1, a.err, 59u);
     } else if (warp == kMma) {
       // ---- one warp issues all MMAs; they run in the order of issue, so a region of S is written anew behind the
       // product that read P from it

@@ -1,7 +1,10 @@
 """Host side of the attention with shared prefixes and of the sampled tokens: refusals before any device work (no call
 here launches a kernel), the workspaces' sizes, and the oracle's own pins."""
 import ctypes
+import glob
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -111,3 +114,14 @@ def test_oracle_sample_min_p_above_one_and_infinite_temperature():
     assert [PO.sample(x, u, q=1.5) for u in (0.0, 0.9)] == [([1], [0.0])] * 2
     assert [PO.sample(x, u, q=1.0)[0] for u in (0.4, 0.6)] == [[1], [2]]
     assert [PO.sample(x, u, T=np.inf, q=q)[0][0] for q in (0.0, 0.5, 1.0) for u in (0.0, 0.4, 0.7, 0.999)] == [0, 1, 2, 2] * 3
+
+
+def test_error_words_name_their_kernel():
+    """A wait that runs out leaves a word by which its file is known."""
+    from megatron_tensor_transformer_gb300 import build
+    words = {}
+    for f in glob.glob(os.path.join(build.CSRC, "*.cu")):
+        with open(f) as src:
+            for w in set(re.findall(r"err(?:or)?,\s*(\d+)u", src.read())):
+                words.setdefault(int(w), []).append(os.path.basename(f))
+    assert len(words) > 20 and all(len(f) == 1 for f in words.values()), words
