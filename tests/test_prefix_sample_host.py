@@ -125,3 +125,39 @@ def test_error_words_name_their_kernel():
             for w in set(re.findall(r"err(?:or)?,\s*(\d+)u", src.read())):
                 words.setdefault(int(w), []).append(os.path.basename(f))
     assert len(words) > 20 and all(len(f) == 1 for f in words.values()), words
+
+
+def test_sample_binding_refuses_what_the_call_would_misread():
+    """A column of a table of settings, another type, too few elements: data_ptr() alone says nothing of them."""
+    x, f, n = torch.zeros((4, 100)), torch.zeros(4), torch.zeros(4, dtype=torch.int32)
+    column, far = torch.zeros((4, 5))[:, 0], torch.zeros((4, 5), dtype=torch.int32)[:, 1]
+    good = dict(u=f, ids=n, temperature=f, top_k=n, top_p=f, min_p=f, logprob=f)
+    bad = [{k: far if k in ("ids", "top_k") else column} for k in good] + [{k: f.double()} for k in good] + [{k: n[:3]} for k in good]
+    bad += [{k: (n if k in ("ids", "top_k") else f)[:3]} for k in good]
+    for b in bad + [dict(logits=x.double())]:
+        a = {**good, "logits": x, **b}
+        with pytest.raises(tpx.TpxError) as e:
+            tpx.tp_sample_tokens(a.pop("logits"), a.pop("u"), a.pop("ids"), **a)
+        assert e.value.status == tpx.TP_ERR_INVALID_ARG, b
+
+
+def test_prefix_attention_binding_refuses_what_the_call_would_misread():
+    M, row = 4, SH.n_q_heads * SH.head_dim
+    pages = tpx.make_pages(16, 5, 3, table_stride=7)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    n32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    pool = bf(SH.t, 5, SH.n_kv_heads // SH.t, 16, SH.head_dim)
+    good = dict(q=bf(M, row), k_pages=pool, v_pages=pool, block_table=n32(M, 7)[:, :3], lens=n32(M), cu_groups=n32(3),
+                prefix_lens=n32(2), o_in=bf(M, row), lse=torch.zeros((M, SH.n_q_heads)))
+    for b in (dict(q=bf(M, 2 * row)[:, :row]), dict(q=torch.zeros((M, row))), dict(o_in=bf(row, M).t()), dict(o_in=bf(M - 1, row)),
+              dict(k_pages=pool.view(torch.uint8)), dict(v_pages=pool.transpose(3, 4)), dict(k_pages=pool[:, :4].contiguous()),
+              dict(lens=n32(M, 2)[:, 0]), dict(lens=n32(M).long()), dict(lens=n32(M - 1)), dict(cu_groups=n32(6)[::2]),
+              dict(prefix_lens=n32(4)[::2]), dict(prefix_lens=n32(2).float()), dict(lse=torch.zeros((SH.n_q_heads, M)).t()),
+              dict(block_table=n32(M, 3)), dict(block_table=n32(7, M).t()), dict(block_table=n32(M, 7)[:, :2]),
+              dict(block_table=n32(M - 1, 7)), dict(block_table=n32(M, 7).long()), dict(block_table=n32(M * 7))):
+        with pytest.raises(tpx.TpxError) as e:
+            tpx.tp_prefix_attn_decode(SH, pages, ws=torch.zeros(1, dtype=torch.uint8), **{**good, **b})
+        assert e.value.status == tpx.TP_ERR_INVALID_ARG, list(b)
+    with pytest.raises(tpx.TpxError) as e:                             # the good ones reach the call, which sees the workspace
+        tpx.tp_prefix_attn_decode(SH, pages, ws=torch.zeros(1, dtype=torch.uint8), **good)
+    assert e.value.status == tpx.TP_ERR_WORKSPACE
