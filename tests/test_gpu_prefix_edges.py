@@ -129,3 +129,39 @@ def test_prefix_attention_long_sums_of_one_cta(dev, kv, rows):
     bound = 2.0 ** -23 * x + 2.0 ** -21 + (n / 128 + 34 + 10) * 2.0 ** -24 + 2.0 ** -22 * want
     over = np.abs(lse.cpu().numpy().astype(np.float64) - want) - bound
     assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+@pytest.mark.parametrize("kv", BOTH)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_prefix_attention_long_runs_of_one_cta(dev, kv, hd, page):
+    """Enough tiles that a CTA walks most of one, wide or narrow: dozens of chunks, page ids fetched 32 at a time, every
+    group's pages its own."""
+    rng = np.random.default_rng(page + hd)
+    groups = [(int(n), int(p)) for n, p in zip(rng.permutation(np.arange(2, 18).tolist() * 2), rng.integers(3000, 6000, 32))]
+    lens = tails(groups, page, 60)
+    c = Shared(dev, 1, 64, 4, hd, page, groups, lens, kv, seed=page, poison=False)
+    check(c, *c.launch())
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_prefix_attention_rows_beside_an_infinite_key(dev, n):
+    """A shared key of -inf weighs nothing, to the same bits as if it were not there."""
+    groups = [(n, 208)]
+    c = Shared(dev, 1, 8, 2, 64, 16, groups, [230] * n, seed=9, poison=False)
+    c.q.fill_(1.0)
+    c.k[:, int(c.table[0, 0]), :, 5] = float("-inf")
+    o, lse = c.launch()
+    got, got_l = O.as_f64(bits(o)).reshape(n, 8, 64), lse.cpu().numpy().astype(np.float64)
+    keep = np.array([j for j in range(230) if j != 5])
+    for m in (0, n - 1):
+        k, v = (x[0].double()[c.table[m, keep // 16], :, keep % 16].cpu().numpy() for x in (c.k, c.v))
+        for h in range(8):
+            s = k[:, h // 4].sum(1) / 8
+            top = s.max()
+            p = np.exp(s - top)
+            ref, A, rl = p @ v[:, h // 4] / p.sum(), p @ np.abs(v[:, h // 4]) / p.sum(), top + math.log(p.sum())
+            ps = (64 + 8) * 2.0 ** -23 * np.abs(k[:, h // 4]).sum(1).max() / 8 + 2.0 ** -21 + 320 * 2.0 ** -24
+            e = A * (2 * ps + 2.0 ** -16)
+            assert_within(got[m, h], ref, e + HALF * (np.abs(ref) + e), f"o of request {m}, head {h}")
+            assert abs(got_l[m, h] - rl) <= ps + 2.0 ** -21 * (1 + abs(rl))
