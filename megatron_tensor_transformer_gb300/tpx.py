@@ -153,11 +153,9 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _given(where, *tensors):
-    """(name, tensor or None, its type, least elements): the C call reads them one after another from data_ptr() on."""
-    for name, t, dtype, n in tensors:
-        if t is not None and (t.dtype != dtype or t.numel() < n or not t.is_contiguous()):
-            raise TpxError(TP_ERR_INVALID_ARG, f"{where}: {name} has to be contiguous, {dtype}, with {n} elements")
+def _flat(t, dtype, n):
+    """Whether the C call can read n elements one after another from t.data_ptr() on (None: it is not given)."""
+    return t is None or (t.dtype is dtype and t.is_contiguous() and t.numel() >= n)
 
 
 _raw_stream = _device = None
@@ -435,22 +433,23 @@ def tp_prefix_attn_decode(shape, pages, q, k_pages, v_pages, block_table, lens, 
     """As tp_paged_attn_decode, with the requests cu_groups[g] .. cu_groups[g + 1] - 1 sharing their first
     prefix_lens[g] positions' whole pages; cu_groups [n + 1], prefix_lens [n]: int32 on the device.  All tensors but the
     block table, whose rows are pages.table_stride apart, are contiguous."""
-    if cu_groups.shape[0] != prefix_lens.shape[0] + 1:
+    n_groups = prefix_lens.shape[0]
+    if cu_groups.shape[0] != n_groups + 1:
         raise TpxError(TP_ERR_INVALID_ARG, "tp_prefix_attn_decode: cu_groups and prefix_lens")
-    M, row, i32, f32 = q.shape[0], shape.n_q_heads * shape.head_dim, torch.int32, torch.float32
-    held = pages.n_pages * shape.n_kv_heads * pages.page_size * shape.head_dim
-    kv = torch.bfloat16 if pages.kv_dtype == TP_BF16 else torch.uint8 if k_pages.dtype == torch.uint8 else torch.float8_e4m3fn
-    _given("tp_prefix_attn_decode", ("q", q, torch.bfloat16, M * row), ("o_in", o_in, torch.bfloat16, M * row),
-           ("k_pages", k_pages, kv, held), ("v_pages", v_pages, kv, held), ("lens", lens, i32, M),
-           ("cu_groups", cu_groups, i32, 0), ("prefix_lens", prefix_lens, i32, 0), ("lse", lse, f32, M * shape.n_q_heads),
-           ("k_scale", k_scale, f32, shape.n_kv_heads), ("v_scale", v_scale, f32, shape.n_kv_heads))
-    if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] < M or \
-            block_table.shape[1] < pages.max_pages or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or \
-            (M > 1 and block_table.stride(0) != pages.table_stride):
+    M, heads, i32, f32, bf16 = q.shape[0], shape.n_q_heads, torch.int32, torch.float32, torch.bfloat16
+    row, held = heads * shape.head_dim, pages.n_pages * pages.page_size * shape.n_kv_heads * shape.head_dim
+    kv = bf16 if pages.kv_dtype == TP_BF16 else torch.uint8 if k_pages.dtype is torch.uint8 else torch.float8_e4m3fn
+    if not (_flat(q, bf16, M * row) and _flat(o_in, bf16, M * row) and _flat(k_pages, kv, held) and _flat(v_pages, kv, held)
+            and _flat(lens, i32, M) and _flat(cu_groups, i32, 1) and _flat(prefix_lens, i32, 0) and _flat(lse, f32, M * heads)
+            and _flat(k_scale, f32, shape.n_kv_heads) and _flat(v_scale, f32, shape.n_kv_heads)):
+        raise TpxError(TP_ERR_INVALID_ARG, "tp_prefix_attn_decode: a tensor's type, length or strides")
+    rows, pitch = block_table.shape, block_table.stride()
+    if block_table.dtype is not i32 or len(rows) != 2 or rows[0] < M or rows[1] < pages.max_pages or \
+            (pitch[1] != 1 and rows[1] > 1) or (pitch[0] != pages.table_stride and M > 1):
         raise TpxError(TP_ERR_INVALID_ARG, "tp_prefix_attn_decode: block_table")
     _check(lib().tp_prefix_attn_decode(ctypes.byref(shape), ctypes.byref(pages), _ptr(q), _ptr(k_pages), _ptr(v_pages),
-                                       _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(lens), q.shape[0],
-                                       _ptr(cu_groups), _ptr(prefix_lens), prefix_lens.shape[0], scale, window,
+                                       _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(lens), M,
+                                       _ptr(cu_groups), _ptr(prefix_lens), n_groups, scale, window,
                                        _ptr(o_in), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
            "tp_prefix_attn_decode")
     return o_in
@@ -499,13 +498,13 @@ def tp_sample_tokens(logits, u, ids, temperature=None, top_k=None, top_p=None, m
     """logits: [M, vocab] fp32, rows logits.stride(0) apart, a row's logits next to one another; u, temperature, top_p,
     min_p, logprob: [M] fp32, ids, top_k: [M] int32, contiguous (all on the device; the settings and logprob may be
     None)."""
-    if logits.dtype != torch.float32 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    (M, V), (pitch, step), i32, f32 = logits.shape, logits.stride(), torch.int32, torch.float32
+    if logits.dtype is not f32 or (V > 1 and step != 1):
         raise TpxError(TP_ERR_INVALID_ARG, "tp_sample_tokens: logits' type, or stride along the vocabulary")
-    M, i32, f32 = logits.shape[0], torch.int32, torch.float32
-    _given("tp_sample_tokens", ("u", u, f32, M), ("ids", ids, i32, M), ("temperature", temperature, f32, M),
-           ("top_k", top_k, i32, M), ("top_p", top_p, f32, M), ("min_p", min_p, f32, M), ("logprob", logprob, f32, M))
-    ldl = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
-    _check(lib().tp_sample_tokens(_ptr(logits), ldl, logits.shape[0], logits.shape[1], _ptr(u), _ptr(temperature),
-                                  _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(ids), _ptr(logprob), _stream(stream)),
+    if not (_flat(u, f32, M) and _flat(ids, i32, M) and _flat(temperature, f32, M) and _flat(top_k, i32, M)
+            and _flat(top_p, f32, M) and _flat(min_p, f32, M) and _flat(logprob, f32, M)):
+        raise TpxError(TP_ERR_INVALID_ARG, "tp_sample_tokens: a tensor's type, length or strides")
+    _check(lib().tp_sample_tokens(_ptr(logits), pitch if M > 1 else V, M, V, _ptr(u), _ptr(temperature), _ptr(top_k),
+                                  _ptr(top_p), _ptr(min_p), _ptr(ids), _ptr(logprob), _stream(stream)),
            "tp_sample_tokens")
     return ids
