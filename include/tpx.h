@@ -475,8 +475,9 @@ tp_status tp_paged_attn_decode(const tp_shape* shape /* host */, const tp_pages*
  * cu_groups [n_groups + 1] and prefix_lens [n_groups]: int32 on the device; 0 <= cu_groups[0] <= cu_groups[1] <= .. <= M
  * (a group may be empty; a group that breaks this, or whose prefix is negative or longer than a row of the table,
  * counts as having no prefix).  n_groups is at most M; 0: as tp_paged_attn_decode (the two may then be NULL).
- * Where the table's M rows can name no more than 96 MB of cache (M max_pages page_size positions), sharing is not looked
- * at: that takes less time.
+ * Where the table's M rows can name no more than 96 MB of cache (M max_pages page_size positions), and for one request,
+ * sharing is not looked at: that takes less time.  The rule goes by max_pages since lengths are on the device: a caller
+ * that knows the longest request of a batch gives the pages that it holds as max_pages (table_stride stays the table's own).
  * Scores, softmax statistics and sums are fp32.  The weights keep as many bits on their way into the tensor cores as there:
  * over bf16 pages 2^-16 of a weight (two bf16), over e4m3 pages 2^-11 of it and 2^-32 of the largest (fp16; q is fp16 after a
  * power of two per head, exact down to 2^-24 of the head's largest |q|).  The parts' sums are joined in fp32.

@@ -1229,13 +1229,16 @@ tp_status tp_prefix_attn_decode(const tp_shape* sh, const tp_pages* pages, const
   st = attn_args(sh, pages, q, k_pages, v_pages, k_scale, v_scale, block_table, lens, M, scale, window, o_in, lse, ws,
                  ws_bytes, &a);
   if (st != TP_OK || M == 0) return st;
-  // Where all that the table's rows can name is little, each request by itself takes less than the three launches.
-  // One group, 32 q and 8 kv heads of 128, microseconds by itself and shared: bf16, 16 requests of 1000 positions (68 MB)
-  // 19.7 and 23.1, 8 of 4000 (133 MB) 27.6 and 29.1, 32 of 1000 (136 MB) 28.8 and 25.5, 128 of 250 (151 MB) 41.4 and 37.0;
-  // e4m3, 32 of 1000 (68 MB) 25.0 and 29.1, 128 of 250 (76 MB) 43.0 and 46.1.
+  // Where all that the table's rows can name is little, each request by itself takes less than the three launches; and one
+  // request shares nothing.  One group, 32 q and 8 kv heads of 128, microseconds by itself and shared: bf16, 16 requests of
+  // 1000 positions (68 MB) 19.7 and 26.7, 8 of 4000 (133 MB) 27.6 and 32.8, 32 of 1000 (136 MB) 28.7 and 28.7, 128 of 250
+  // (151 MB) 41.0 and 38.3, 64 of 800 (222 MB) 40.8 and 32.7; e4m3, 32 of 1000 (68 MB) 25.0 and 32.5, 128 of 250 (76 MB) 42.8
+  // and 46.1, 64 of 800 (111 MB) 37.4 and 37.1.  So up to 40 MB above the bound sharing still takes a few microseconds
+  // more.  Lengths are on the device: the rule goes by what the host knows.
   const double held = (double)M * pages->max_pages * pages->page_size * sh->n_kv_heads * sh->head_dim * 2 *
                       (pages->kv_dtype == TP_BF16 ? 2 : 1);
-  if (n_groups == 0 || held <= kSharedFrom) return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
+  if (n_groups == 0 || M == 1 || held <= kSharedFrom)
+    return cuda_status(launch_paged_attn(a, pages->kv_dtype, sh->head_dim, k_pages, v_pages, S(stream)));
   a.cu_groups = cu_groups;
   a.prefix_lens = prefix_lens;
   a.n_groups = n_groups;

@@ -432,7 +432,8 @@ def tp_prefix_attn_decode(shape, pages, q, k_pages, v_pages, block_table, lens, 
                           lse=None, scale=0.0, window=0, k_scale=None, v_scale=None, stream=None):
     """As tp_paged_attn_decode, with the requests cu_groups[g] .. cu_groups[g + 1] - 1 sharing their first
     prefix_lens[g] positions' whole pages; cu_groups [n + 1], prefix_lens [n]: int32 on the device.  All tensors but the
-    block table, whose rows are pages.table_stride apart, are contiguous."""
+    block table, whose rows are pages.table_stride apart, are contiguous.  pages.max_pages, what a row can name, says
+    whether sharing is worth looking at: give the longest request's pages where the host knows them."""
     n_groups = prefix_lens.shape[0]
     if cu_groups.shape[0] != n_groups + 1:
         raise TpxError(TP_ERR_INVALID_ARG, "tp_prefix_attn_decode: cu_groups and prefix_lens")

@@ -165,3 +165,28 @@ def test_prefix_attention_rows_beside_an_infinite_key(dev, n):
             e = A * (2 * ps + 2.0 ** -16)
             assert_within(got[m, h], ref, e + HALF * (np.abs(ref) + e), f"o of request {m}, head {h}")
             assert abs(got_l[m, h] - rl) <= ps + 2.0 ** -21 * (1 + abs(rl))
+
+
+@pytest.mark.parametrize("kv", BOTH)
+def test_prefix_attention_by_what_a_row_of_the_table_can_name(dev, kv):
+    """A table with room for very long requests takes three launches; with the longest one's pages given as max_pages, the
+    rows as far apart as before, the call is one launch and gives the bits of a tight table.  So does one request alone."""
+    def launches(c):
+        before = tpx.tp_launch_count()
+        out = c.launch()
+        return tpx.tp_launch_count() - before, out
+    groups = [(4, 300)]
+    lens = tails(groups, 4)
+    tight, wide, far = (Shared(dev, 1, 8, 2, 128, 16, groups, lens, kv, seed=4, small=s, stride_pad=p)
+                        for s, p in ((True, 0), (False, 0), (True, 8000)))
+    (n, (o, lse)), (n2, (o2, lse2)), (n3, _) = launches(tight), launches(far), launches(wide)
+    assert (n, n2, n3) == (1, 1, 3)
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+    one = Shared(dev, 1, 8, 2, 128, 16, [(1, 300)], [317], kv, seed=5)
+    n, (o, lse) = launches(one)
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    pages = tpx.make_pages(16, one.n_pages, one.max_pages, kv, one.table.shape[1])
+    tpx.tp_paged_attn_decode(one.sh, pages, one.q, one.k, one.v, one.table_d, one.lens_d, o2, one.ws, lse=lse2, k_scale=one.ks,
+                             v_scale=one.vs)
+    sync()
+    assert n == 1 and torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
