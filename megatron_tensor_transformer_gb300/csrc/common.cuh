@@ -25,6 +25,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // one conv
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 2^x, good to 2^-22 of itself
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Shared memory written by ordinary stores is seen by TMA and the tensor cores after it.
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -42,11 +42,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kNT = 512, kNW = kNT / 32, kMaxC = 8, kVec = 4;
 static_assert(kNT == 64 * 8, "raise_bar takes 64 groups");
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // the larger of the two, NaN if x is one (fmaxf drops it)
 __device__ __forceinline__ float max_nan(float x, float y) {

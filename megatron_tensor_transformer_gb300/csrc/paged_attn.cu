@@ -185,27 +185,6 @@ __device__ __forceinline__ uint32_t group_bits(const Item& it, int c, uint32_t l
   const int a0 = max(0, it.lo - c * kP), a1 = min(kP, it.n - c * kP);
   return loaded & ((1u << ((a1 + 15) >> 4)) - 1) & ~((1u << (a0 >> 4)) - 1);
 }
-// A role's bounded waits.  After one that runs out (it sets the error word) the producer issues no more copies and
-// the two issuing threads no more MMAs, and each waits, bounded again, for what it has in flight; the softmax warps
-// go on without waiting to the item's end, so that their team's barriers are met.  Then the kernel ends: no copy
-// lands in shared memory and no MMA in tensor memory that the CTA has given back.
-// (The loop is a function of its own: inlined at every wait it made the roles' code together larger than the
-// SM's instruction cache, and the kernel's time depend on where the compiler put what, by up to a quarter.)
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
-  const bool ok = tc::mbar_wait(bar, parity);
-  if (!ok) atomicExch(err, code);
-  return !ok;
-}
-struct Waits {
-  unsigned* err;
-  unsigned code;
-  bool failed;
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
-    if (tc::mbar_try_wait(bar, parity) || tc::mbar_try_wait(bar, parity)) return true;
-    if (!failed) failed = wait_long(bar, parity, err, code);
-    return !failed;
-  }
-};
 
 // grid: one CTA per SM.  Softmax teams of NG groups of 4 warps; a group's threads hold HPT heads, NG HPT >= n_q / n_kv.
 template <int HD, bool FP8, int HPT, int NG>

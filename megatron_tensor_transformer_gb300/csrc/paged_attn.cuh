@@ -19,11 +19,6 @@ constexpr float kNoRef = -3.402823466e38f;  // no reference yet: fp32's lowest, 
                                             // that only reaches it is rightly a weight of 1 under it)
 constexpr int kP = 128;                    // positions per chunk: the rows of an MMA
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // what a sum taken under reference m counts under the reference mx (0 where nothing was summed)
 __device__ __forceinline__ float weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
 
@@ -42,6 +37,48 @@ __device__ __forceinline__ __half2 e4m3x2_half2(uint32_t v) {
   return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3));
 }
 __device__ __forceinline__ float2 e4m3x2_value(uint32_t v) { return __half22float2(e4m3x2_half2(v)); }
+
+// 16 bytes of a row of q, which RP neighbouring lanes hold, as fp16: q / 2^(e - 127) below 2^15, e the exponent field of the
+// row's largest value less 14 (both factors stay normal).  An infinity makes the row NaN, as its scores would.
+template <int RP>
+__device__ __forceinline__ uint4 q_as_fp16(const uint4& v, int& e) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t top = 0, h[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top = max(top, max((w[k] >> 7) & 0xffu, (w[k] >> 23) & 0xffu));
+#pragma unroll
+  for (int x = 1; x < RP; x <<= 1) top = max(top, __shfl_xor_sync(kFull, top, x));
+  e = min(max((int)top, 15), 254) - 14;
+  const float inv = top == 255u ? NAN : __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 x = __floats2half2_rn(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
+    h[k] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// A role's bounded waits.  After one that runs out (it sets the error word) the producer issues no more copies and
+// an issuing thread no more MMAs, and each waits, bounded again, for what it has in flight; the softmax warps
+// go on without waiting to the item's end, so that their team's barriers are met.  Then the kernel ends: no copy
+// lands in shared memory and no MMA in tensor memory that the CTA has given back.
+// (The loop is a function of its own: inlined at every wait it made the roles' code together larger than the
+// SM's instruction cache, and the kernel's time depend on where the compiler put what, by up to a quarter.)
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
+  const bool ok = tc::mbar_wait(bar, parity);
+  if (!ok) atomicExch(err, code);
+  return !ok;
+}
+struct Waits {
+  unsigned* err;
+  unsigned code;
+  bool failed;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
+    if (tc::mbar_try_wait(bar, parity) || tc::mbar_try_wait(bar, parity)) return true;
+    if (!failed) failed = wait_long(bar, parity, err, code);
+    return !failed;
+  }
+};
 
 // The positions [lo, n) a request attends to, in chunks [c0, c1); c0 == c1 if there are none.
 struct Span {

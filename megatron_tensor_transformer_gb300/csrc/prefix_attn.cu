@@ -170,24 +170,6 @@ __device__ __forceinline__ void warp_commit(uint32_t bar) {
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(kFull, v, 0); }
 
-// Waits as in paged_attn.cu: after one that runs out (it sets the error word) the producer issues no more copies, the
-// issuing thread no more MMAs, and both wait for what is in flight; the softmax warps go on without waiting.
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, unsigned code) {
-  const bool ok = tc::mbar_wait(bar, parity);
-  if (!ok) atomicExch(err, code);
-  return !ok;
-}
-struct Waits {
-  unsigned* err;
-  unsigned code;
-  bool failed;
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {  // whether the phase is over
-    if (tc::mbar_try_wait(bar, parity) || tc::mbar_try_wait(bar, parity)) return true;
-    if (!failed) failed = wait_long(bar, parity, err, code);
-    return !failed;
-  }
-};
-
 // 16-bit operands (bf16, or fp16 with FP8 pages), fp32 sums
 template <bool FP8>
 __host__ __device__ constexpr uint32_t idesc16(int M, int N) {
@@ -358,21 +340,9 @@ __global__ void __launch_bounds__(XCfg<HD, FP8>::kThreads, 1)
                        : "memory");
           continue;
         }
-        // q / 2^e below 2^15, as fp16
         const uint4 v = there ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t top = 0, h[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) top = max(top, max((w[q] >> 7) & 0xffu, (w[q] >> 23) & 0xffu));
-#pragma unroll
-        for (int o = 1; o < RP; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-        // exponent field of the largest value, less 14 for 2^14 <= q / 2^e < 2^15; both factors stay normal
-        const int e = min(max((int)top, 15), 254) - 14;
-        // an infinity makes the row NaN, as its scores would
-        const float inv = top == 255u ? NAN : __uint_as_float((uint32_t)(254 - e) << 23);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = pack16<true>(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+        int e;
+        *reinterpret_cast<uint4*>(dst) = q_as_fp16<RP>(v, e);
         const int mine = __shfl_sync(kFull, e, lane % kRows * RP);
         if (lane / kRows * kRows == i) pow = __uint_as_float((uint32_t)mine << 23);
       }

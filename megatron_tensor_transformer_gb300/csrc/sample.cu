@@ -143,11 +143,6 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
   return z;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float logit_of(uint32_t order) {  // of order_of
   return __uint_as_float(order >> 31 ? order & 0x7fffffffu : ~order);
 }
@@ -414,18 +409,18 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
           }
         });
       } else {
-      each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
-        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+        each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float p = exponent_of(v[q], s);
-          if (!(p < kLightest)) continue;
-          const int b = nearest_64th(p);
-          if (b / kPerOctave != octave || !low.reached(v[q], i + q - lead)) continue;
-          const uint32_t n = by_weight ? __float2uint_rn(ex2(bin_exponent(b) - p) * kUnit) : 1u;
-          if (n) atomicAdd(&fine[b % kPerOctave], n);
-        }
-      });
+          for (int q = 0; q < 4; ++q) {
+            const float p = exponent_of(v[q], s);
+            if (!(p < kLightest)) continue;
+            const int b = nearest_64th(p);
+            if (b / kPerOctave != octave || !low.reached(v[q], i + q - lead)) continue;
+            const uint32_t n = by_weight ? __float2uint_rn(ex2(bin_exponent(b) - p) * kUnit) : 1u;
+            if (n) atomicAdd(&fine[b % kPerOctave], n);
+          }
+        });
       }
       __syncthreads();
       for (int t = tid; t < C * kPerOctave; t += kNT)
@@ -456,66 +451,66 @@ __global__ void __launch_bounds__(kNT, kPerSm) sample_kernel(const SampleArgs a,
       // Divided by key: what the bins hold, tokens, or roughly their weights in terms of the bin's heaviest (whole numbers, in
       // any order).
       if (bins.shift >= 0) {
-      each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
-        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+        each(i0 + 4 * tid, i1, 4 * kNT, [&](int i, float4 v4) {
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int b = bin_of(v[q], i + q);
-          if (b < 0) continue;
-          uint32_t n = 1;
-          if (by_weight) n = __float2uint_rn(ex2(bin_exponent(b) - exponent_of(v[q], s)) * kUnit);
-          if (n) atomicAdd(&sh.hist[b], n);
-        }
-      });
-      __syncthreads();
-      if (c != 0) {
-        for (int b = tid; b < kBins; b += kNT) {
-          const uint32_t n = sh.hist[b];
-          if (n) {
-            atomicAdd(&first->hist[b], n);
-            sh.hist[b] = 0;
+          for (int q = 0; q < 4; ++q) {
+            const int b = bin_of(v[q], i + q);
+            if (b < 0) continue;
+            uint32_t n = 1;
+            if (by_weight) n = __float2uint_rn(ex2(bin_exponent(b) - exponent_of(v[q], s)) * kUnit);
+            if (n) atomicAdd(&sh.hist[b], n);
+          }
+        });
+        __syncthreads();
+        if (c != 0) {
+          for (int b = tid; b < kBins; b += kNT) {
+            const uint32_t n = sh.hist[b];
+            if (n) {
+              atomicAdd(&first->hist[b], n);
+              sh.hist[b] = 0;
+            }
           }
         }
-      }
-      cl.sync();
-      if (c == 0) {  // the bin with the border, as far as these tell
-        constexpr int kEach = kBins / kNT;
-        uint64_t n[kEach], sum = 0;  // in units of 2^-24 of the bins' first weight
-        const float p0 = bin_exponent(0);
+        cl.sync();
+        if (c == 0) {  // the bin with the border, as far as these tell
+          constexpr int kEach = kBins / kNT;
+          uint64_t n[kEach], sum = 0;  // in units of 2^-24 of the bins' first weight
+          const float p0 = bin_exponent(0);
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-          const int b = tid * kEach + q;
-          const uint32_t h = sh.hist[b];
-          sh.hist[b] = 0;
-          n[q] = !by_weight || h == 0 ? h : (uint64_t)((float)h * ex2(p0 - bin_exponent(b)) * (0x1p24f / kUnit));
-          sum += n[q];
-        }
-        uint64_t before = sum;
+          for (int q = 0; q < kEach; ++q) {
+            const int b = tid * kEach + q;
+            const uint32_t h = sh.hist[b];
+            sh.hist[b] = 0;
+            n[q] = !by_weight || h == 0 ? h : (uint64_t)((float)h * ex2(p0 - bin_exponent(b)) * (0x1p24f / kUnit));
+            sum += n[q];
+          }
+          uint64_t before = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t x = __shfl_up_sync(kFull, before, o);
-          if (lane >= o) before += x;
-        }
-        if (lane == 31) s_sum[warp] = before;
-        before -= sum;
-        if (tid == 0) sh.bin = kBins - 1;  // where none is found below: too few tokens, or rounding
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) before += s_sum[w];
-        uint64_t goal = limit - base;
-        if (by_weight) goal = (uint64_t)((float)goal * (0x1p-20f * s.above_top * ex2(p0)));
-        if (goal == 0) goal = 1;
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t x = __shfl_up_sync(kFull, before, o);
+            if (lane >= o) before += x;
+          }
+          if (lane == 31) s_sum[warp] = before;
+          before -= sum;
+          if (tid == 0) sh.bin = kBins - 1;  // where none is found below: too few tokens, or rounding
+          __syncthreads();
+          for (int w = 0; w < warp; ++w) before += s_sum[w];
+          uint64_t goal = limit - base;
+          if (by_weight) goal = (uint64_t)((float)goal * (0x1p-20f * s.above_top * ex2(p0)));
+          if (goal == 0) goal = 1;
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-          if (before < goal && before + n[q] >= goal) atomicMin(&sh.bin, tid * kEach + q);
-          before += n[q];
+          for (int q = 0; q < kEach; ++q) {
+            if (before < goal && before + n[q] >= goal) atomicMin(&sh.bin, tid * kEach + q);
+            before += n[q];
+          }
+          __syncthreads();
+          if (tid < C) {
+            const int bin = sh.bin;
+            cl.map_shared_rank(&sh, tid)->bin = bin;
+          }
         }
-        __syncthreads();
-        if (tid < C) {
-          const int bin = sh.bin;
-          cl.map_shared_rank(&sh, tid)->bin = bin;
-        }
-      }
-      cl.sync();
+        cl.sync();
       }
       for (;;) {
         // The exact sums above the bin and in it, its keys' ends, and its tokens, listed as far as they fit.

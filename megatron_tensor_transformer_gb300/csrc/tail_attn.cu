@@ -237,21 +237,9 @@ __global__ void __launch_bounds__(kThreads, TCfg<HD, FP8>::kPerSm)
       for (int i = 0; i < QV; ++i) {
         const int r = (lane + 32 * i) / RP, c8 = (lane + 32 * i) % RP;
         uint8_t* dst = sQ + (buf * 16 + r) * C::QROW + 16 * c8;
-        if (FP8) {  // q / 2^e below 2^15, as fp16
-          const uint32_t w[4] = {qn[i].x, qn[i].y, qn[i].z, qn[i].w};
-          uint32_t top = 0, h[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max((w[k] >> 7) & 0xffu, (w[k] >> 23) & 0xffu));
-#pragma unroll
-          for (int x = 1; x < RP; x <<= 1) top = max(top, __shfl_xor_sync(kFull, top, x));
-          const int e = min(max((int)top, 15), 254) - 14;  // both factors stay normal
-          const float inv = top == 255u ? NAN : __uint_as_float((uint32_t)(254 - e) << 23);  // an infinity: NaN
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2 x = __floats2half2_rn(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
-            h[k] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (FP8) {
+          int e;
+          *reinterpret_cast<uint4*>(dst) = q_as_fp16<RP>(qn[i], e);
           if (c8 == 0) q_pow[buf][r] = __uint_as_float((uint32_t)e << 23);
         } else {
           *reinterpret_cast<uint4*>(dst) = qn[i];
