@@ -18,10 +18,11 @@
 // e4m3 pages are widened to fp16 in shared memory by four warps (exact), and q is fp16 after a power of two per row.
 //
 // Measured (one launch, cold; of nominal HBM, of the tensor pipe's cycles): 2048 rows by 30000 positions for each of 8 kv heads
-// of 128: 189 us, 58% and 58%, 1.33 PFLOP/s; 131072 positions of few rows, 92 us, 5.8 TB/s; e4m3, 1536 rows in two groups by
-// 15000: 98 us, 44% of the pipe.  A chunk of a full tile takes 3370 cycles, its MMAs 2048: of 128 rows S, the exponentials and
-// P V follow one another, and two blocks do not quite cover that; tensor memory has no room for a third.  A CTA's beginning (cold
-// code, the groups' scan, q, first copies) takes 11 us.
+// of 128: 243 us, 44% and 70%, 1.04 PFLOP/s of 4 R P hd, 1.55 with the rests' products; 131072 positions of few rows, 94 us,
+// 5.7 TB/s; e4m3, 1536 rows in two groups by 15000: 101 us, 43% of the pipe.  A chunk of a full tile takes 4360 cycles, its MMAs
+// 3072: of 128 rows S, the exponentials and P V follow one another, and two blocks do not quite cover that; tensor memory has
+// no room for a third.  A CTA's beginning (cold code, the groups' scan, q, first copies) took 11 us with P as one bf16, and
+// takes 2 to 4 more with the longer code.
 #include <cuda.h>
 
 #include <algorithm>
@@ -56,7 +57,7 @@ struct XCfg {
   static constexpr float kStep = 8.f;                   // ref may be behind the maximum by this, in powers of two
   static constexpr float kPLog = FP8 ? 7.f : 0.f;       // weights are held times 2^this: at most 2^15 in fp16
   // Units of work: a chunk of a full tile, of one with up to 128 rows, and a tile's beginning and end.  e4m3, two groups of 768
-  // rows, with (wide, narrow, ends) of (4, 3, 8) 135 us, (3, 3, 8) 142, (4, 4, 8) 142, (4, 2, 8) 157, (4, 3, 4) 137; bf16 +-1.
+  // rows, with (wide, narrow, ends) of (4, 3, 8) 139 us, (3, 3, 8) 144, (4, 4, 8) 144, (4, 2, 8) 160, (4, 3, 4) 141; bf16 +-1.
   static constexpr int OWN = tail_positions(HD, FP8);   // positions of a stage of a request by itself
   static constexpr int kWide = 4, kNarrow = T == 2 ? 3 : 4, kEnds = 8;
 };

@@ -21,8 +21,8 @@
 // bin is divided again by key.
 //
 // Measured (128256 tokens): one row with top-p 23 us (256 threads a CTA 30, 1024 29: seven barriers of the cluster, and code that
-// is run once); 256 rows with a temperature and min-p 104 us, 1.3 TB/s, half of the issue slots; 1000 rows with top-p 884 us, 0.6 TB/s,
-// 53% of the issue slots.  Bound by issue and by the barriers between the passes, of which the exact sums are the
+// is run once); 256 rows with a temperature and min-p 105 us, 1.3 TB/s, half of the issue slots; 1000 rows with top-p 886 us, 0.6 TB/s,
+// 51% of the issue slots.  Bound by issue and by the barriers between the passes, of which the exact sums are the
 // longest; two CTAs per SM overlap.
 #include <cooperative_groups.h>
 

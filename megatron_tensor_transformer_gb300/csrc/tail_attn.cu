@@ -12,8 +12,10 @@
 // not show beside the output's own rounding; the tensor cores have the time), or as fp16 over e4m3 pages, whose codes become
 // fp16 in registers (exact).  Scores of positions that are not attended to are -inf, and their v is zeroed in shared memory.
 //
-// Measured (one launch, cold): 2048 runs of up to 250 positions (194 MB) 46 us, 4.2 TB/s; runs that take 71 MB 25 us, 2.9 TB/s,
-// 10 us of which pass before the first product.  With the paged kernel's CTAs in its place a batch of the latter took 69 us in all.
+// Measured (one launch, cold): 2048 runs of up to 250 positions (194 MB) 47 us, 4.1 TB/s; runs that take 71 MB 26 us, 2.8 TB/s,
+// 10 us of which pass before the first product; one bf16 for a weight instead of two takes no less.  With the paged kernel's
+// CTAs in its place a batch of the latter took 69 us in all.  Long runs take more here than there: 16 requests of up to 30000
+// positions that share nothing 159 us for a call, 144 as paged attention (e4m3 98 and 81).
 #include <cuda.h>
 
 #include <algorithm>
