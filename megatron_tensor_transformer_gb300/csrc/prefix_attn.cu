@@ -11,7 +11,7 @@
 //   O += P V    P from tensor memory, where its rows' threads wrote it over S; V as TMA brought it, read transposed
 // Over bf16 pages P is two bf16, the upper halves of the weights and what these leave (2^-16 of a weight, as in paged
 // attention: half as many bits, 2^-8, showed beside the output's own rounding, 2.3e-3 of o against 1.7e-3).  That is half as
-// many MMAs again, 3072 cycles a chunk of 256 rows instead of 2048.
+// many MMAs again, 48 of 64 cycles a chunk of 256 rows instead of 32.
 // A softmax thread has one row: no shuffles, no shared memory; O stays in tensor memory and is scaled only when a
 // row's maximum passes its reference by 2^8.  With two blocks the MMAs of one run beside the exponentials of the
 // other; with one, S of the next chunk is computed before P V of this one, into the other half of S.
@@ -20,7 +20,7 @@
 // Measured (one launch, cold; of nominal HBM, of the tensor pipe's cycles): 2048 rows by 30000 positions for each of 8 kv heads
 // of 128: 243 us, 44% and 70%, 1.04 PFLOP/s of 4 R P hd, 1.55 with the rests' products; 131072 positions of few rows, 94 us,
 // 5.7 TB/s; e4m3, 1536 rows in two groups by 15000: 101 us, 43% of the pipe.  A chunk of a full tile takes 4360 cycles, its MMAs
-// 3072: of 128 rows S, the exponentials and P V follow one another, and two blocks do not quite cover that; tensor memory has
+// 70% of them: of 128 rows S, the exponentials and P V follow one another, and two blocks do not quite cover that; tensor memory has
 // no room for a third.  A CTA's beginning (cold code, the groups' scan, q, first copies) took 11 us with P as one bf16, and
 // takes 2 to 4 more with the longer code.
 #include <cuda.h>
